@@ -27,3 +27,9 @@ from .binding import (  # noqa: F401
     library_path,
     make_config,
 )
+from .weights import (  # noqa: F401
+    pack_weights_w4,
+    quantize_weights,
+    rows8_parts,
+    unpack_weights_w4,
+)

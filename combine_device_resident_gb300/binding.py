@@ -33,6 +33,11 @@ FLAG_SPLITS_TILED = 1 << 1
 FLAG_COMBINE_TMA = 1 << 2
 FLAG_ROUTE_FUSED = 1 << 3
 FLAG_ROUTE_WARP = 1 << 4
+W_BF16 = 0  # weight types of the experts' products
+W_E4M3 = 1
+W_INT4 = 2
+ACTIVATIONS = {None: 0, "none": 0, "swiglu": 1}
+ROW8_TAIL = 16  # bytes behind the values of an 8-bit row: the fp32 scale and padding
 
 # Every function the header declares, for load checks.
 EXPORTED = [
@@ -41,7 +46,8 @@ EXPORTED = [
     "a2av_read_device_status", "a2av_device_status_ptr", "a2av_plan_launches",
     "a2av_status_string", "a2av_last_error", "a2av_dispatch_static",
     "a2av_dispatch_padded", "a2av_pack_padded", "a2av_exchange_padded", "a2av_set_active_tokens",
-    "a2av_route", "a2av_route_splits", "a2av_set_wait_limit",
+    "a2av_route", "a2av_route_splits", "a2av_set_wait_limit", "a2av_rms_norm", "a2av_quantize_rows",
+    "a2av_expert_matmul",
 ]
 
 
@@ -139,6 +145,12 @@ def load_library(path: Optional[str] = None):
     L.a2av_route_splits.restype = i32
     L.a2av_set_wait_limit.argtypes = [vp, ctypes.c_int64]
     L.a2av_set_wait_limit.restype = i32
+    L.a2av_rms_norm.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp]
+    L.a2av_rms_norm.restype = i32
+    L.a2av_quantize_rows.argtypes = [vp, vp, i32, spp, vp, vp]
+    L.a2av_quantize_rows.restype = i32
+    L.a2av_expert_matmul.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, spp, vp]
+    L.a2av_expert_matmul.restype = i32
     if path is None:
         _lib = L
     return L
@@ -196,6 +208,15 @@ def _stream_ptr(stream, device):
 
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _width(t, name):
+    """Length of a tensor's last dimension."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dim() < 1:
+        raise A2avError(f"{name} must be a torch tensor with at least one dimension")
+    return t.shape[-1]
 
 
 class Plan:
@@ -381,6 +402,93 @@ class Plan:
             self.handle, self._rows(recv, "recv"), self._t(topk_idx, torch.int32, (self.R, self.T, self.k), "topk_idx"),
             self._t(slot_map, torch.int32, (self.R, self.T, self.k), "slot_map"), self._rows(y, "y"),
             _stream_ptr(stream, self.device)), "a2av_expert_scale")
+
+    # ---- the norm in front and the experts in between ---------------------------
+    def new_rows8(self, rows, K):
+        """Zeroed 8-bit rows [rows][K+16] (uint8; `rows` a number or a leading
+        shape): K e4m3 values, the fp32 scale, padding (``rows8_parts``)."""
+        import torch
+
+        lead = (int(rows),) if isinstance(rows, int) else tuple(rows)
+        return torch.zeros(lead + (int(K) + ROW8_TAIL,), dtype=torch.uint8, device=self.device)
+
+    def rms_norm(self, x, weight, y=None, rows8=None, residual=None, residual_out=None, eps=1e-6, stream=None):
+        """Root-mean-square norm of x (+ residual) over H, times `weight`
+        (a2av_rms_norm): into y (bf16) and/or rows8 (8-bit rows [R][T][H+16]),
+        the sum into residual_out (which may be x or residual itself)."""
+        import torch
+
+        shape = (self.R, self.T, self.H)
+        _check(self.lib, self.lib.a2av_rms_norm(
+            self.handle, self._t(x, torch.bfloat16, shape, "x"), self._opt(residual, torch.bfloat16, shape, "residual"),
+            self._t(weight, torch.bfloat16, (self.H,), "weight"), float(eps),
+            self._opt(residual_out, torch.bfloat16, shape, "residual_out"), self._opt(y, torch.bfloat16, shape, "y"),
+            self._opt(rows8, torch.uint8, (self.R, self.T, self.H + ROW8_TAIL), "rows8"),
+            _stream_ptr(stream, self.device)), "a2av_rms_norm")
+
+    def quantize_rows(self, x, splits: Splits, rows8, stream=None):
+        """8-bit rows of the live rows of an arena x [arena_rows][K] (a2av_quantize_rows)."""
+        import torch
+
+        K = _width(x, "x")
+        _check(self.lib, self.lib.a2av_quantize_rows(
+            self.handle, self._t(x, torch.bfloat16, (self.arena_rows, K), "x"), K, self._sp(splits),
+            self._t(rows8, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "rows8"),
+            _stream_ptr(stream, self.device)), "a2av_quantize_rows")
+
+    def expert_matmul(self, x, w, splits: Splits, y, w_scale=None, activation=None, stream=None):
+        """y[r] = act(x[r] . w[e]^T) for every live row r, e its expert (a2av_expert_matmul).
+
+        w [E][Nw][K] bf16 with x bf16 [arena_rows][K], or float8_e4m3fn with
+        w_scale fp32 [E][Nw] and x 8-bit rows [arena_rows][K+16]; y bf16
+        [arena_rows][N].  activation "swiglu": Nw = 2N, gate rows then up rows."""
+        import torch
+
+        eight = getattr(w, "dtype", None) == torch.float8_e4m3fn
+        K = _width(w, "w")
+        xt = self._t(x, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "x") if eight else \
+            self._t(x, torch.bfloat16, (self.arena_rows, K), "x")
+        self._matmul(xt, w, w.dtype if eight else torch.bfloat16, K, K, W_E4M3 if eight else W_BF16, 0,
+                     self._opt(w_scale, torch.float32, (self.E, w.shape[1] if w.dim() == 3 else 0), "w_scale"),
+                     splits, y, activation, stream)
+
+    def expert_matmul_w4(self, x, w4, w_scale, splits: Splits, y, activation=None, stream=None):
+        """``expert_matmul`` with 4-bit weights, for few rows per expert: w4 int32
+        [E][Nw][K/8], w_scale bf16 [E][Nw][K/group] (``pack_weights_w4``), x bf16."""
+        import torch
+
+        K = _width(w4, "w4") * 8
+        groups = max(1, _width(w_scale, "w_scale"))
+        if K % groups:
+            raise A2avError(f"w_scale has {groups} groups, which do not divide K = {K}")
+        self._matmul(self._t(x, torch.bfloat16, (self.arena_rows, K), "x"), w4, torch.int32, K, K // 8, W_INT4,
+                     K // groups,
+                     self._t(w_scale, torch.bfloat16, (self.E, w4.shape[1] if w4.dim() == 3 else 0, groups), "w_scale"),
+                     splits, y, activation, stream)
+
+    def _matmul(self, x, w, w_dtype, K, w_width, weight_type, group, w_scale, splits, y, activation, stream):
+        import torch
+
+        if activation not in ACTIVATIONS:
+            raise A2avError(f"activation must be None or 'swiglu', got {activation!r}")
+        act = ACTIVATIONS[activation]
+        N = _width(y, "y")
+        _check(self.lib, self.lib.a2av_expert_matmul(
+            self.handle, x, self._t(w, w_dtype, (self.E, N << act, w_width), "w"), w_scale,
+            self._t(y, torch.bfloat16, (self.arena_rows, N), "y"), K, N, weight_type, group, act, self._sp(splits),
+            _stream_ptr(stream, self.device)), "a2av_expert_matmul")
+
+    def _opt(self, t, dtype, shape, name):
+        return None if t is None else self._t(t, dtype, shape, name)
+
+    def _sp(self, splits):
+        """The split arrays of this plan's sizes, on its device."""
+        if not isinstance(splits, Splits):
+            raise A2avError("splits must be a Splits")
+        if tuple(splits.send_counts.shape) != (self.R, self.E) or splits.send_counts.device != self.device:
+            raise A2avError(f"splits were made for {tuple(splits.send_counts.shape)} on {splits.send_counts.device}, "
+                            f"the plan has {(self.R, self.E)} on {self.device}")
+        return ctypes.byref(splits.ptrs)
 
     def set_wait_limit(self, polls: int = -1):
         """Main-loop poll limit of the TMA kernels' bounded waits for later

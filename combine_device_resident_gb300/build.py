@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liba2av.so")
-SOURCES = ["a2av_api.cu", "splits.cu", "pack.cu", "combine.cu", "static_scratch.cu", "router.cu"]
+SOURCES = ["a2av_api.cu", "splits.cu", "pack.cu", "combine.cu", "static_scratch.cu", "router.cu",
+           "norm.cu", "expert_gemm.cu", "expert_w4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

@@ -425,6 +425,146 @@ a2av_status_t a2av_route_splits(a2av_plan_t p, const float *logits, int32_t *top
     return A2AV_OK;
 }
 
+static a2av_status_t refuse(const char *why) {
+    a2av::set_last_error(why);
+    return A2AV_ERR_INVALID_ARG;
+}
+
+a2av_status_t a2av_rms_norm(a2av_plan_t p, const void *x, const void *residual, const void *weight, float eps,
+                            void *residual_out, void *y, void *rows8, void *stream) {
+    if (!p || !aligned(x, 16) || !aligned(weight, 16) || (uintptr_t)residual % 16 || (uintptr_t)residual_out % 16 ||
+        (uintptr_t)y % 16 || (uintptr_t)rows8 % 16)
+        return refuse("a2av_rms_norm: a null or misaligned pointer");
+    if (!y && !rows8) return refuse("a2av_rms_norm: neither y nor rows8");
+    if (residual_out && !residual) return refuse("a2av_rms_norm: residual_out without residual");
+    if (!(eps >= 0.0f)) return refuse("a2av_rms_norm: eps must not be negative");
+    if (p->g.H > a2av::kMaxNormRow) return refuse("a2av_rms_norm: H <= 32768");
+    if (rows8 && p->g.H % 16) return refuse("a2av_rms_norm: rows8 needs H % 16 == 0");
+    const size_t n = tokens(p) * row_bytes(p), n8 = tokens(p) * ((size_t)p->g.H + 16), nw = row_bytes(p);
+    const void *in[3] = {x, residual, weight};
+    for (int i = 0; i < 3; ++i) {
+        const size_t ni = i == 2 ? nw : n;
+        if (!in[i]) continue;
+        if ((y && overlap(y, n, in[i], ni)) || (rows8 && overlap(rows8, n8, in[i], ni)))
+            return refuse("a2av_rms_norm: an output overlaps an input");
+        // residual_out: x or residual themselves, or apart from both
+        if (residual_out && residual_out != in[i] && overlap(residual_out, n, in[i], ni))
+            return refuse("a2av_rms_norm: residual_out overlaps an input in part");
+    }
+    if ((residual_out && y && overlap(residual_out, n, y, n)) ||
+        (residual_out && rows8 && overlap(residual_out, n, rows8, n8)) || (y && rows8 && overlap(y, n, rows8, n8)) ||
+        residual_out == weight)
+        return refuse("a2av_rms_norm: outputs overlap");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    a2av::NormArgs a;
+    memset(&a, 0, sizeof a);
+    a.g = p->g;
+    a.num_tokens = p->num_tokens;
+    a.x = static_cast<const uint16_t *>(x);
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.weight = static_cast<const uint16_t *>(weight);
+    a.residual_out = static_cast<uint16_t *>(residual_out);
+    a.y = static_cast<uint16_t *>(y);
+    a.rows8 = static_cast<uint8_t *>(rows8);
+    a.rows = (int32_t)tokens(p);
+    a.H = p->g.H;
+    a.eps = eps;
+    cudaError_t e = a2av::launch_norm(*p, a, true, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm kernel launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
+a2av_status_t a2av_quantize_rows(a2av_plan_t p, const void *x, int32_t K, const a2av_splits_t *splits, void *rows8,
+                                 void *stream) {
+    if (!p || !aligned(x, 16) || !aligned(rows8, 16) || !splits || !aligned(splits->recv_total, 4) ||
+        !aligned(splits->window_base, 4))
+        return refuse("a2av_quantize_rows: a null or misaligned pointer");
+    if (p->cfg.window_mode == A2AV_WINDOW_PADDED) return refuse("a2av_quantize_rows: not with padded windows");
+    if (K < 16 || K % 16 || K > a2av::kMaxNormRow)
+        return refuse("a2av_quantize_rows: K must be a multiple of 16, at most 32768");
+    const int64_t rows = a2av_recv_arena_rows(&p->cfg);
+    if (overlap(x, (size_t)rows * K * 2, rows8, (size_t)rows * ((size_t)K + 16)))
+        return refuse("a2av_quantize_rows: rows8 overlaps x");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    if (rows == 0) return A2AV_OK;
+    a2av::NormArgs a;
+    memset(&a, 0, sizeof a);
+    a.g = p->g;
+    a.x = static_cast<const uint16_t *>(x);
+    a.rows8 = static_cast<uint8_t *>(rows8);
+    a.recv_total = splits->recv_total;
+    a.window_base = splits->window_base;
+    a.rows = (int32_t)rows;
+    a.H = K;
+    cudaError_t e = a2av::launch_norm(*p, a, false, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "quantize kernel launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
+a2av_status_t a2av_expert_matmul(a2av_plan_t p, const void *x, const void *w, const void *w_scale, void *y, int32_t K,
+                                 int32_t N, int32_t weight_type, int32_t group, int32_t activation,
+                                 const a2av_splits_t *splits, void *stream) {
+    if (weight_type != A2AV_W_BF16 && weight_type != A2AV_W_E4M3 && weight_type != A2AV_W_INT4)
+        return refuse("a2av_expert_matmul: unknown weight_type");
+    if (activation != A2AV_ACT_NONE && activation != A2AV_ACT_SWIGLU)
+        return refuse("a2av_expert_matmul: unknown activation");
+    const bool scaled = weight_type != A2AV_W_BF16;
+    if (!p || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !splits || !aligned(splits->recv_total, 4) ||
+        !aligned(splits->window_base, 4) || (scaled && !aligned(w_scale, weight_type == A2AV_W_INT4 ? 2 : 4)))
+        return refuse("a2av_expert_matmul: a null or misaligned pointer");
+    if (!scaled && w_scale) return refuse("a2av_expert_matmul: bf16 weights have no scales");
+    if (p->cfg.window_mode == A2AV_WINDOW_PADDED) return refuse("a2av_expert_matmul: not with padded windows");
+    if (p->g.epr > 1 && p->cfg.recv_order != A2AV_ORDER_EXPERT)
+        return refuse("a2av_expert_matmul: rows must be grouped by expert (A2AV_ORDER_EXPERT, or one expert per rank)");
+    if (p->g.epr > 1 && !aligned(splits->recv_expert_offsets, 4))
+        return refuse("a2av_expert_matmul: recv_expert_offsets is needed");
+    if (N < 8 || N % 8 || N > a2av::kMaxWidth)
+        return refuse("a2av_expert_matmul: N must be a multiple of 8, at most 2^20");
+    if (weight_type == A2AV_W_INT4 && group != 32 && group != 64 && group != 128)
+        return refuse("a2av_expert_matmul: group must be 32, 64 or 128");
+    const int32_t unit = weight_type == A2AV_W_BF16 ? 8 : weight_type == A2AV_W_E4M3 ? 16 : group;
+    if (K < unit || K % unit || K > a2av::kMaxWidth)
+        return refuse("a2av_expert_matmul: K must be a multiple of 8 (bf16), 16 (e4m3) or the group (int4), at most 2^20");
+    const int64_t rows = a2av_recv_arena_rows(&p->cfg);
+    const bool swiglu = activation == A2AV_ACT_SWIGLU;
+    const size_t pitch = weight_type == A2AV_W_E4M3 ? (size_t)K + 16 : (size_t)K * 2;
+    const size_t w_bytes = (size_t)p->g.E * N * (swiglu ? 2 : 1) * K /
+                           (weight_type == A2AV_W_INT4 ? 2 : 1) * (weight_type == A2AV_W_BF16 ? 2 : 1);
+    const size_t y_bytes = (size_t)rows * N * 2;
+    if (overlap(y, y_bytes, x, (size_t)rows * pitch) || overlap(y, y_bytes, w, w_bytes))
+        return refuse("a2av_expert_matmul: y overlaps an input");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    if (rows == 0) return A2AV_OK;
+    a2av::MatmulArgs a;
+    memset(&a, 0, sizeof a);
+    a.g = p->g;
+    a.recv_expert_offsets = splits->recv_expert_offsets;
+    a.recv_total = splits->recv_total;
+    a.window_base = splits->window_base;
+    a.x = static_cast<const uint8_t *>(x);
+    a.w = w;
+    a.w_scale = w_scale;
+    a.y = static_cast<uint16_t *>(y);
+    a.status = p->status;
+    a.arena_rows = rows;
+    a.x_pitch = (int64_t)pitch;
+    a.wait_polls = p->wait_polls;
+    a.K = K;
+    a.N = N;
+    a.group = group;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = weight_type == A2AV_W_INT4 ? a2av::launch_expert_w4(*p, a, swiglu, s)
+                                               : a2av::launch_expert_gemm(*p, a, weight_type == A2AV_W_E4M3, swiglu, s);
+    if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
 a2av_status_t a2av_set_active_tokens(a2av_plan_t p, const int32_t *num_tokens) {
     if (!p || (num_tokens && (reinterpret_cast<uintptr_t>(num_tokens) % 4) != 0)) return A2AV_ERR_INVALID_ARG;
     p->num_tokens = num_tokens;

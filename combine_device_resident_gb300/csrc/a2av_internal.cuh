@@ -18,6 +18,8 @@ constexpr int kHistTile = kHistThreads * kHistRounds;  // assignments per tile
 constexpr int kMaxRanks = 64;
 constexpr int kMaxExperts = 2048;
 constexpr int kMaxTopk = 32;
+constexpr int kMaxNormRow = 32768;    // row length of the norm: one block holds the row
+constexpr int kMaxWidth = 1 << 20;    // K and N of the experts' products
 
 // Status bit set when a bounded wait gives up (should never happen: every wait
 // in these kernels is on copies this CTA issued itself).
@@ -128,6 +130,28 @@ struct ScaleArgs {
     uint32_t *status;
 };
 
+struct NormArgs {
+    Geometry g;
+    const int32_t *num_tokens;
+    const uint16_t *x, *residual, *weight;  // residual may be null
+    uint16_t *residual_out, *y;             // may be null
+    uint8_t *rows8;                         // may be null
+    const int32_t *recv_total, *window_base;  // which rows are live (quantize_rows)
+    int32_t rows, H;                        // rows of x and its row length (K in quantize_rows)
+    float eps;
+};
+
+struct MatmulArgs {
+    Geometry g;
+    const int32_t *recv_expert_offsets, *recv_total, *window_base;
+    const uint8_t *x;  // rows of x_pitch bytes
+    const void *w, *w_scale;
+    uint16_t *y;
+    uint32_t *status;
+    int64_t arena_rows, x_pitch, wait_polls;
+    int32_t K, N, group;
+};
+
 // Status bit for a slot_map entry outside the arena handed to combine or the
 // expert stand-in (the row is skipped, nothing is read or written there).
 constexpr uint32_t kDevBadSlot = 1u << 2;
@@ -175,8 +199,8 @@ namespace a2av {
 
 // Launch with the programmatic stream-serialization attribute (the kernel
 // calls grid_dependency_wait() before reading its predecessor's output).
-template <typename Kernel, typename Args>
-cudaError_t launch_pdl(Kernel kernel, int grid, int block, size_t smem, cudaStream_t s, const Args &args) {
+template <typename Kernel, typename... Args>
+cudaError_t launch_pdl(Kernel kernel, int grid, int block, size_t smem, cudaStream_t s, const Args &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
@@ -187,7 +211,7 @@ cudaError_t launch_pdl(Kernel kernel, int grid, int block, size_t smem, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Launchers (return the cudaGetLastError() after the launch).
@@ -202,6 +226,9 @@ cudaError_t launch_route(const a2av_plan_s &p, const RouteArgs &a, cudaStream_t 
 bool routed_splits_supported(const a2av_plan_s &p);
 cudaError_t launch_routed_hist(const a2av_plan_s &p, const HistArgs &a, cudaStream_t s);
 cudaError_t configure_route(a2av_plan_s &p);
+cudaError_t launch_norm(const a2av_plan_s &p, const NormArgs &a, bool norm, cudaStream_t s);
+cudaError_t launch_expert_gemm(const a2av_plan_s &p, const MatmulArgs &a, bool fp8, bool swiglu, cudaStream_t s);
+cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s);
 
 // Records the text a2av_last_error() returns on the calling thread.
 void set_last_error(const char *msg);
@@ -226,6 +253,16 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+
+// 16-byte load of data that is read once and that this thread may store to afterwards.
+__device__ __forceinline__ uint4 ld_row(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 

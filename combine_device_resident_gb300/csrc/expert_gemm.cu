@@ -1,0 +1,389 @@
+// The experts' products on the dispatched rows, bf16 or e4m3 (tcgen05):
+//
+//   y[r][n] = act( sum_k x[r][k] * w[e(r)][n][k] ),  the rows of expert e = rows [start_e, start_e + count_e)
+//
+// with start and count read on the device from the split arrays.  The weights
+// are the M side of the matrix instruction (128 channels per tile) and an
+// expert's rows the N side: N may be any multiple of 16 up to 256, so a group
+// of c rows costs ceil(c/16)*16 columns, not a multiple of 128, and a group of
+// a few rows streams the weights once with a narrow instruction.
+//
+// One persistent block per SM: warp 0 feeds a ring of shared-memory stages by
+// TMA, warp 1 issues the matrix instructions into one of two TMEM
+// accumulators, warps 2-5 drain the other one (lane = channel, column = row),
+// apply scales and activation in fp32 and store bf16.
+//
+// SwiGLU: a tile holds the gate and the up weights of 64 channels in
+// alternating blocks of eight rows (one TMA box of a five-dimensional view
+// of w), so the two halves of a channel sit eight TMEM lanes apart in the
+// same warp: one shuffle per two rows brings them together.
+#include <cuda_bf16.h>
+
+#include "expert_common.cuh"
+
+namespace a2av {
+namespace {
+
+constexpr int kThreads = 192;       // producer warp, matrix warp, four epilogue warps
+constexpr int kStages = 4;
+constexpr int kRowBytes = 128;      // K bytes per stage row: one 128-byte swizzle span
+constexpr int kTileM = 128;         // weight rows per tile
+constexpr int kTileN = 256;         // expert rows per tile, at most
+constexpr int kABytes = kTileM * kRowBytes;
+constexpr int kBBytes = kTileN * kRowBytes;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of x
+constexpr int kBand = 8;            // row tiles of an expert that run with one channel tile in turn
+
+struct __align__(8) Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    uint32_t abort;
+    int32_t warp_sum[8];
+};
+
+// Shared-memory operand descriptor: K-major, 128-byte swizzle, eight-row
+// groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+template <bool kFp8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    const uint32_t acc = accumulate ? 1u : 0u;
+    if (kFp8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *m, int k, int row, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(m), "r"(k), "r"(row), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap *m, int k, int block, int e, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(m), "r"(k), "r"(0), "r"(block), "r"(e), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Bounded wait that also ends when another warp of the block gave up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, long long limit, Shared *sh,
+                                              uint32_t *status) {
+    volatile uint32_t *abort = &sh->abort;
+    for (long long it = 0; it < limit; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+    }
+    *abort = 1;
+    atomicOr(status, kDevWaitTimeout);
+    return false;
+}
+
+// One unit of work: rows [row, row + rows) of expert e times channel tile `ctile`.
+struct Tile {
+    int e, row, rows, ctile;
+};
+
+__device__ __forceinline__ Tile tile_at(long long t, const int32_t *start, const int32_t *count, const int32_t *pre,
+                                        int E, int ctiles) {
+    const int lo = expert_of(t, pre, E, ctiles);
+    const int n = count[lo];
+    const int rt = (n + kTileN - 1) / kTileN;
+    // An expert's row tiles are taken kBand at a time, every channel tile of
+    // a band before the next band: the band's rows and the weights stay in L2
+    // while they are used again.
+    const int in = (int)(t - (long long)pre[lo] * ctiles);
+    const int band = in / (kBand * ctiles);
+    const int wide = min(kBand, rt - band * kBand);
+    const int rem = in - band * kBand * ctiles;
+    Tile r;
+    r.e = lo;
+    r.ctile = rem / wide;
+    // even shares, multiples of 16 rows (the last one takes what is left)
+    const int share = ((n + rt - 1) / rt + 15) / 16 * 16;
+    const int first = (band * kBand + rem % wide) * share;
+    r.row = start[lo] + first;
+    r.rows = max(0, min(share, n - first));
+    return r;
+}
+
+template <bool kFp8, bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_big,
+                       const __grid_constant__ CUtensorMap map_small, const MatmulArgs a) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    Shared *sh = reinterpret_cast<Shared *>(stages + kStages * kStageBytes);
+    const int E = a.g.E;
+    int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
+    int32_t *count = start + E;
+    int32_t *pre = count + E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sh->acc_full[b], 1);
+            mbar_init(&sh->acc_empty[b], 4);
+        }
+        mbar_init(&sh->drain, 1);
+        sh->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 64) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_big));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_small));
+    }
+    grid_dependency_wait();
+
+    tmem_fence_before();
+    const int total = place_experts<kThreads>(a, kTileN, start, count, pre, sh->warp_sum);  // ends in a barrier
+    tmem_fence_after();
+
+    const uint32_t tmem = sh->tmem;
+    constexpr int kChan = kSwiglu ? kTileM / 2 : kTileM;  // output channels per tile
+    const int ctiles = (a.N + kChan - 1) / kChan;
+    const long long tiles = (long long)total * ctiles;
+    constexpr int kStep = kFp8 ? kRowBytes : kRowBytes / 2;  // K elements per stage
+    const int kblocks = (a.K + kStep - 1) / kStep;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t round = 0;  // times the ring has gone round
+            bool ok = true;
+            for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile w = tile_at(t, start, count, pre, E, ctiles);
+                const int n16 = (w.rows + 15) / 16 * 16;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (round > 0 && !wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, sh, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = smem_u32(stages + s * kStageBytes);
+                    mbar_arrive_expect_tx(&sh->full[s], kABytes + n16 * kRowBytes);
+                    tma_weights(at, &map_w, kb * kStep, w.ctile * (kChan / 8), w.e, &sh->full[s]);
+                    int i = 0;
+                    for (; i + kBoxBig <= n16; i += kBoxBig)
+                        tma_rows(at + kABytes + i * kRowBytes, &map_big, kb * kStep, w.row + i, &sh->full[s]);
+                    for (; i < n16; i += kBoxSmall)
+                        tma_rows(at + kABytes + i * kRowBytes, &map_small, kb * kStep, w.row + i, &sh->full[s]);
+                    if (++s == kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            if (!ok)  // given up: let every load that was issued land before the block ends
+                for (int i = 0; i < kStages; ++i) {
+                    const uint32_t fills = round + (i < s ? 1 : 0);
+                    if (fills > 0) mbar_wait_bounded(&sh->full[i], (fills - 1) & 1);
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // fp32 accumulator; A and B bf16 (1) or e4m3 (0), both K-major
+            constexpr uint32_t kIdesc = 1u << 4 | (kFp8 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)(kTileM >> 4) << 24;
+            int s = 0;
+            uint32_t round = 0, it = 0;
+            bool ok = true;
+            for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++it) {
+                const Tile w = tile_at(t, start, count, pre, E, ctiles);
+                const int n16 = (w.rows + 15) / 16 * 16;
+                const int b = it & 1;
+                if (it >= 2 && !wait_or_abort(&sh->acc_empty[b], ((it >> 1) - 1) & 1, a.wait_polls, sh, a.status)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t idesc = kIdesc | (uint32_t)(n16 >> 3) << 17;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!wait_or_abort(&sh->full[s], round & 1, a.wait_polls, sh, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+                    const uint32_t at = smem_u32(stages + s * kStageBytes);
+                    const uint64_t da = operand_desc(at), db = operand_desc(at + kABytes);
+                    if (n16 > 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)  // 32 bytes of K per instruction
+                            mma<kFp8>(tmem + b * kTileN, da + j * 2, db + j * 2, idesc, kb > 0 || j > 0);
+                    }
+                    mma_commit(&sh->empty[s]);
+                    if (++s == kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+                if (ok) mma_commit(&sh->acc_full[b]);
+            }
+            if (!ok) {  // given up: let the instructions that were issued end before TMEM is freed
+                mma_commit(&sh->drain);
+                mbar_wait_bounded(&sh->drain, 0);
+            }
+        }
+    } else {
+        const int quad = warp & 3;  // the TMEM lanes this warp may read
+        uint32_t it = 0;
+        const bool up = kSwiglu && (lane & 8);
+        for (long long t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+            const Tile w = tile_at(t, start, count, pre, E, ctiles);
+            const int b = it & 1;
+            // swiglu: lanes 0-7 gate of channels 0-7, 8-15 their up, 16-23 gate of channels 8-15, ...
+            const int chan = w.ctile * kChan + (kSwiglu ? quad * 16 + (lane >> 4) * 8 + (lane & 7) : quad * 32 + lane);
+            const bool store = chan < a.N;
+            float ws = 1.0f;
+            if (kFp8 && store)
+                ws = __ldg(static_cast<const float *>(a.w_scale) + (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + chan);
+            // one answer for the warp: the TMEM loads below want all of its lanes
+            const bool ready = wait_or_abort(&sh->acc_full[b], (it >> 1) & 1, a.wait_polls, sh, a.status);
+            if (!__all_sync(0xffffffffu, ready)) break;
+            tmem_fence_after();
+            uint16_t *y = a.y + (size_t)w.row * a.N + chan;
+            for (int c = 0; c < w.rows; c += 32) {
+                float v[32];
+                float xs = 1.0f;
+                if (kFp8 && c + lane < w.rows)  // the row's scale behind its values
+                    xs = __ldg(reinterpret_cast<const float *>(a.x + (size_t)(w.row + c + lane) * a.x_pitch + a.K));
+                tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + b * kTileN + c, v);
+                if (kFp8) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= ws * __shfl_sync(0xffffffffu, xs, i);
+                }
+                if (kSwiglu) {
+                    // of rows i, i+1 the gate lane finishes the first, the up lane the second
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 8);
+                        const float g = up ? other : v[i], u = up ? v[i + 1] : other;
+                        const int row = c + i + (up ? 1 : 0);
+                        const float out = __fdividef(g, 1.0f + __expf(-g)) * u;
+                        if (store && row < w.rows)
+                            y[(size_t)row * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
+                    }
+                } else if (store) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < w.rows)
+                            y[(size_t)(c + i) * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->acc_empty[b]);
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+template <bool kFp8, bool kSwiglu>
+cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    const cuuint64_t es = kFp8 ? 1 : 2, K = a.K, N = a.N, E = a.g.E, halves = kSwiglu ? 2 : 1;
+    const cuuint32_t step = kRowBytes / (cuuint32_t)es;
+    CUtensorMap mw, mb, ms;
+    // w as [E][N/8][gate, up][8][K]
+    const cuuint64_t wd[5] = {K, 8, halves, N / 8, E};
+    const cuuint64_t wst[4] = {K * es, N * K * es, 8 * K * es, halves * N * K * es};
+    const cuuint32_t wb[5] = {step, 8, (cuuint32_t)halves, (cuuint32_t)(kTileM / 8 / halves), 1};
+    const cuuint64_t xd[2] = {K, (cuuint64_t)a.arena_rows};
+    const cuuint64_t xst[1] = {(cuuint64_t)a.x_pitch};
+    const cuuint32_t xb[2] = {step, kBoxBig}, xs[2] = {step, kBoxSmall};
+    const CUtensorMapDataType type = kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!encode_map(&mw, type, 5, a.w, wd, wst, wb) || !encode_map(&mb, type, 2, a.x, xd, xst, xb) ||
+        !encode_map(&ms, type, 2, a.x, xd, xst, xs))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared) + (size_t)a.g.E * 3 * 4;
+    cudaError_t e = cudaFuncSetAttribute(expert_gemm_kernel<kFp8, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    // at most this many tiles: each expert with rows begins one more than its rows fill
+    const long long rows = (long long)a.g.R * a.g.T * a.g.k, chan = kSwiglu ? kTileM / 2 : kTileM;
+    const long long most = ((rows < (long long)E ? rows : (long long)E) + rows / kTileN) * ((a.N + chan - 1) / chan);
+    const int grid = (int)(most < p.num_sms ? most : p.num_sms);
+    return launch_pdl(expert_gemm_kernel<kFp8, kSwiglu>, grid, kThreads, smem, s, mw, mb, ms, a);
+}
+
+}  // namespace
+
+bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
+                const cuuint64_t *strides, const cuuint32_t *box) {
+    using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    // the driver's function, found through the runtime: the library links no driver stub
+    static const EncodeFn encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                                            &q) == cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<EncodeFn>(f) : nullptr;
+    }();
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return encode && encode(m, type, rank, const_cast<void *>(base), dims, strides, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_expert_gemm(const a2av_plan_s &p, const MatmulArgs &a, bool fp8, bool swiglu, cudaStream_t s) {
+    if (fp8) return swiglu ? launch_gemm<true, true>(p, a, s) : launch_gemm<true, false>(p, a, s);
+    return swiglu ? launch_gemm<false, true>(p, a, s) : launch_gemm<false, false>(p, a, s);
+}
+
+}  // namespace a2av

@@ -1,0 +1,178 @@
+// Root-mean-square norm with the residual's addition, in bf16 and/or as 8-bit
+// rows with scales, and the 8-bit rows of an arena without the norm.
+//
+//   z = x + residual                       fp32, residual_out = bf16(z)
+//   t_i = z_i * w_i,  r = 1 / sqrt(mean z^2 + eps),  v_i = t_i * r
+//   y = bf16(v);  a = max|v|;  scale = a / 448;  q = e4m3(v * (448 / a))
+//
+// One block per row, the row in registers between the two uses of it, so x
+// and the residual are read once.  Rounding is monotone, so max|v| is exactly
+// max|t| * r: the sum of squares and the maximum come out of one block
+// reduction and there is one barrier per row.  Bound by HBM: 2 + 2 bytes read,
+// 2 + (1 or 2) written per element.
+#include <cuda_bf16.h>
+
+#include "a2av_internal.cuh"
+
+namespace a2av {
+namespace {
+
+constexpr float kLow8 = 448.0f;      // largest finite e4m3
+constexpr float kZeroRow = 1e-30f;   // a row whose maximum is below this is stored as zeros
+
+// NaN-keeping maximum: a NaN anywhere in a row has to reach its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Rounded to nearest even, values past 448 (one rounding of 448/a away at most) to 448.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Row `row` of the token arrays takes part / row `row` of the arena is live.
+template <bool kNorm>
+__device__ __forceinline__ bool row_active(const NormArgs &a, int row) {
+    if (kNorm) {
+        if (!a.num_tokens) return true;
+        const int s = row / a.g.T;
+        return row - s * a.g.T < active_tokens(a.num_tokens, s, a.g.T);
+    }
+    if (a.g.window_mode == A2AV_WINDOW_FIXED) {
+        const int d = (int)(row / a.g.window_rows);
+        return row - (long long)d * a.g.window_rows < __ldg(a.recv_total + d);
+    }
+    return row < __ldg(a.window_base + a.g.R - 1) + __ldg(a.recv_total + a.g.R - 1);
+}
+
+// V 16-byte vectors of the row per thread (vector tid + j * blockDim).
+template <int V, bool kNorm>
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
+    __shared__ float part[2][2][32];  // [row parity][sum, max][warp]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+    const int nvec = a.H >> 3;
+    grid_dependency_wait();
+
+    uint4 w[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = tid + j * blockDim.x;
+        w[j] = kNorm && i < nvec ? ld_stream_v4(a.weight + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
+    }
+    int parity = 0;
+    for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (!row_active<kNorm>(a, row)) continue;
+        const size_t at = (size_t)row * a.H;
+        float t[V][8];
+        uint4 xv[V], rv[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = tid + j * blockDim.x;
+            xv[j] = i < nvec ? ld_row(a.x + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
+            rv[j] = kNorm && a.residual && i < nvec ? ld_row(a.residual + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
+        }
+        float sum = 0.0f, peak = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = tid + j * blockDim.x;
+            const uint32_t xs[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+            const uint32_t rs[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
+            const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+            uint32_t zs[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                float z0 = lo_f(xs[p]), z1 = hi_f(xs[p]);
+                if (kNorm) {
+                    z0 += lo_f(rs[p]);
+                    z1 += hi_f(rs[p]);
+                    sum = fmaf(z0, z0, sum);
+                    sum = fmaf(z1, z1, sum);
+                    zs[p] = bf16x2(z0, z1);
+                    z0 *= lo_f(ws[p]);
+                    z1 *= hi_f(ws[p]);
+                }
+                t[j][2 * p] = z0;
+                t[j][2 * p + 1] = z1;
+                peak = max_nan(peak, max_nan(fabsf(z0), fabsf(z1)));
+            }
+            if (kNorm && a.residual_out && i < nvec)
+                st_v4(a.residual_out + at + (size_t)i * 8, make_uint4(zs[0], zs[1], zs[2], zs[3]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            if (kNorm) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            peak = max_nan(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+        }
+        if (lane == 0) {
+            part[parity][0][warp] = sum;
+            part[parity][1][warp] = peak;
+        }
+        __syncthreads();  // the other parity's slots are free: every thread has read them before this barrier
+        sum = lane < nwarps ? part[parity][0][lane] : 0.0f;
+        peak = lane < nwarps ? part[parity][1][lane] : 0.0f;
+        parity ^= 1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            if (kNorm) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            peak = max_nan(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+        }
+        const float r = kNorm ? 1.0f / sqrtf(sum / (float)a.H + a.eps) : 1.0f;
+        if (kNorm) peak *= r;
+        const bool zero = peak < kZeroRow;  // false for NaN
+        const float inv = zero ? 0.0f : kLow8 / peak;
+        uint8_t *q = a.rows8 ? a.rows8 + (size_t)row * (a.H + 16) : nullptr;
+        if (q && tid == 0)
+            st_v4(q + a.H, make_uint4(__float_as_uint(zero ? 0.0f : peak / kLow8), 0, 0, 0));
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = tid + j * blockDim.x;
+            if (i >= nvec) break;
+            if (kNorm) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p) t[j][p] *= r;
+                if (a.y)
+                    st_v4(a.y + at + (size_t)i * 8, make_uint4(bf16x2(t[j][0], t[j][1]), bf16x2(t[j][2], t[j][3]),
+                                                               bf16x2(t[j][4], t[j][5]), bf16x2(t[j][6], t[j][7])));
+            }
+            if (q) {
+                uint2 v;
+                v.x = e4m3x2(t[j][0] * inv, t[j][1] * inv) | e4m3x2(t[j][2] * inv, t[j][3] * inv) << 16;
+                v.y = e4m3x2(t[j][4] * inv, t[j][5] * inv) | e4m3x2(t[j][6] * inv, t[j][7] * inv) << 16;
+                *reinterpret_cast<uint2 *>(q + (size_t)i * 8) = v;
+            }
+        }
+    }
+}
+
+template <int V>
+cudaError_t launch_v(const a2av_plan_s &p, const NormArgs &a, bool norm, cudaStream_t s) {
+    const int nvec = a.H / 8;
+    const int block = ((nvec + V - 1) / V + 31) / 32 * 32;
+    const int resident = 2048 / block < 1 ? 1 : 2048 / block;
+    const long long cap = (long long)p.num_sms * resident;
+    const int grid = (int)(a.rows < cap ? a.rows : cap);
+    return norm ? launch_pdl(norm_kernel<V, true>, grid, block, 0, s, a)
+                : launch_pdl(norm_kernel<V, false>, grid, block, 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const a2av_plan_s &p, const NormArgs &a, bool norm, cudaStream_t s) {
+    if (a.H <= 8192) return launch_v<1>(p, a, norm, s);
+    if (a.H <= 16384) return launch_v<2>(p, a, norm, s);
+    return launch_v<4>(p, a, norm, s);
+}
+
+}  // namespace a2av

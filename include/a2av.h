@@ -79,6 +79,9 @@
  *                                          sources below s
  *   splits.recv_total         [R]          rows window d receives
  *   splits.window_base        [R]          arena row where window d starts
+ *   rows8        8-bit rows [n][K+16] bytes: K e4m3 values, their fp32 scale, 12 zero bytes;
+ *                the row stands for value * scale.  A row moves as one: a plan made
+ *                for a hidden of (K+16)/2 dispatches it like a bf16 row of that length.
  */
 #ifndef A2AV_H
 #define A2AV_H
@@ -323,11 +326,75 @@ a2av_status_t a2av_route_splits(a2av_plan_t plan, const float *logits, int32_t *
  * alternating receive buffers (double buffering).] */
 a2av_status_t a2av_set_active_tokens(a2av_plan_t plan, const int32_t *num_tokens);
 
+/* Weights of a2av_expert_matmul. */
+enum {
+    A2AV_W_BF16 = 0, /* bf16 [E][Nw][K], x bf16 rows */
+    A2AV_W_E4M3 = 1, /* e4m3 [E][Nw][K] with fp32 scales [E][Nw], x 8-bit rows */
+    A2AV_W_INT4 = 2, /* int32 words [E][Nw][K/8] with bf16 scales [E][Nw][K/group], x bf16 rows; a word
+                        holds eight weights q - 8, q unsigned 4 bits: k = 0, 2, 4, 6 in bits 0, 4, 8, 12
+                        and k = 1, 3, 5, 7 in bits 16, 20, 24, 28 */
+};
+
+/* Activation applied to the product before it is rounded. */
+enum {
+    A2AV_ACT_NONE = 0,
+    A2AV_ACT_SWIGLU = 1, /* w holds N gate rows, then N up rows: y = g / (1 + exp(-g)) * u */
+};
+
+/* Root-mean-square norm of every token with the residual's addition (one
+ * kernel): z = x + residual in fp32 (residual NULL: z = x); residual_out =
+ * bf16_rne(z) if not NULL (needs residual; may be x or residual itself);
+ * v_i = z_i * w_i / sqrt(mean_j z_j^2 + eps), fp32;
+ *   y (bf16 [R][T][H])     = bf16_rne(v), if not NULL;
+ *   rows8 ([R][T][H+16] B) = the 8-bit rows of v, if not NULL: scale = max|v| / 448
+ *                            and e4m3_rne(v * (448 / max|v|)); a row whose maximum is
+ *                            below 1e-30 is all zero with scale 0; a NaN or an infinity
+ *                            anywhere in a row makes its scale NaN or infinite.
+ * x, residual, residual_out bf16 [R][T][H], weight bf16 [H]; at least one of
+ * y and rows8; y and rows8 overlap nothing else.  H <= 32768, and H % 16 == 0
+ * for rows8 (then 16-byte aligned).  Tokens that take no part
+ * (a2av_set_active_tokens) are left untouched.  [No counterpart on the
+ * pages: they start at the router.] */
+a2av_status_t a2av_rms_norm(a2av_plan_t plan, const void *x, const void *residual, const void *weight, float eps,
+                            void *residual_out, void *y, void *rows8, void *stream);
+
+/* The 8-bit rows of the live rows of an arena (one kernel): rows8[r] from
+ * x[r], bf16 [arena_rows][K], by the rule of a2av_rms_norm with v = x, for
+ * every row of every window up to its recv_total.  K % 16 == 0, K <= 32768.
+ * x and rows8 do not overlap.  Reads splits->recv_total and window_base.  Not
+ * with A2AV_WINDOW_PADDED.  It makes the second product's input out of what
+ * the first one's activation gives. */
+a2av_status_t a2av_quantize_rows(a2av_plan_t plan, const void *x, int32_t K, const a2av_splits_t *splits, void *rows8,
+                                 void *stream);
+
+/* The experts' products on the dispatched rows (one kernel): for every live
+ * row r of the arena, e its expert,
+ *   y[r] = bf16_rne(act(x[r] . w[e]^T)),   y bf16 [arena_rows][N],
+ * with fp32 sums.  The rows of an expert lie together: the plan's receive
+ * order is A2AV_ORDER_EXPERT, or it has one expert per rank; not with
+ * A2AV_WINDOW_PADDED.  Sizes and places are read on the device (splits->
+ * window_base, recv_total, recv_expert_offsets), so routing may change
+ * between replays of a captured graph; experts without rows cost nothing, and
+ * rows that are not live are neither used nor written.  Nw is N, or 2*N with
+ * A2AV_ACT_SWIGLU; weights and scales as for weight_type above.
+ *   A2AV_W_BF16: K % 8 == 0; w_scale NULL.
+ *   A2AV_W_E4M3: K % 16 == 0; the sum is scaled by w_scale[e][n] and the row's scale.
+ *   A2AV_W_INT4: `group` is 32, 64 or 128 and K % group == 0; each group's sum is scaled in
+ *                fp32; for few rows per expert (decode): weights are read again for
+ *                every 32 rows of an expert.
+ * N % 8 == 0; K and N at most 2^20; x, w and y 16-byte aligned; y overlaps neither x nor w.
+ * [Figure 13: the received tokens go on to their experts; the pages do not
+ * define the experts.] */
+a2av_status_t a2av_expert_matmul(a2av_plan_t plan, const void *x, const void *w, const void *w_scale, void *y,
+                                 int32_t K, int32_t N, int32_t weight_type, int32_t group, int32_t activation,
+                                 const a2av_splits_t *splits, void *stream);
+
 /* Diagnostic hook for the failure path of the bounded waits (not part of
  * the method).  The TMA pack (default), the TMA combine
- * (A2AV_FLAG_COMBINE_TMA) and the lane-per-token router (a2av_route's
- * default) wait on mbarriers for the bulk copies they issued
- * themselves; each wait gives up after a bounded number of polls, sets
+ * (A2AV_FLAG_COMBINE_TMA), the lane-per-token router (a2av_route's
+ * default) and the experts' products (a2av_expert_matmul with bf16 or 8-bit
+ * weights) wait on mbarriers for the bulk copies (and matrix
+ * instructions) they issued themselves; each wait gives up after a bounded number of polls, sets
  * A2AV_DEV_WAIT_TIMEOUT in the status word and ends the CTA in order (it
  * first lets every copy it issued land, with the full bound).  This call sets
  * the main-loop limit of those waits for later enqueues on `plan`: polls >= 0
