@@ -12,6 +12,8 @@ import ctypes
 import os
 from typing import Optional
 
+import torch
+
 from . import build as _build
 
 A2AV_OK = 0
@@ -210,10 +212,14 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The current stream's handle by device ordinal: torch's own short way where it has one (making a
+# Stream object takes longer than a small kernel).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _width(t, name):
     """Length of a tensor's last dimension."""
-    import torch
-
     if not isinstance(t, torch.Tensor) or t.dim() < 1:
         raise A2avError(f"{name} must be a torch tensor with at least one dimension")
     return t.shape[-1]
@@ -407,8 +413,6 @@ class Plan:
     def new_rows8(self, rows, K):
         """Zeroed 8-bit rows [rows][K+16] (uint8; `rows` a number or a leading
         shape): K e4m3 values, the fp32 scale, padding (``rows8_parts``)."""
-        import torch
-
         lead = (int(rows),) if isinstance(rows, int) else tuple(rows)
         return torch.zeros(lead + (int(K) + ROW8_TAIL,), dtype=torch.uint8, device=self.device)
 
@@ -416,25 +420,25 @@ class Plan:
         """Root-mean-square norm of x (+ residual) over H, times `weight`
         (a2av_rms_norm): into y (bf16) and/or rows8 (8-bit rows [R][T][H+16]),
         the sum into residual_out (which may be x or residual itself)."""
-        import torch
-
-        shape = (self.R, self.T, self.H)
-        _check(self.lib, self.lib.a2av_rms_norm(
-            self.handle, self._t(x, torch.bfloat16, shape, "x"), self._opt(residual, torch.bfloat16, shape, "residual"),
-            self._t(weight, torch.bfloat16, (self.H,), "weight"), float(eps),
-            self._opt(residual_out, torch.bfloat16, shape, "residual_out"), self._opt(y, torch.bfloat16, shape, "y"),
-            self._opt(rows8, torch.uint8, (self.R, self.T, self.H + ROW8_TAIL), "rows8"),
-            _stream_ptr(stream, self.device)), "a2av_rms_norm")
+        bf16, shape, p = torch.bfloat16, (self.R, self.T, self.H), self._p
+        rc = self.lib.a2av_rms_norm(
+            self.handle, p(x, bf16, shape, "x"), None if residual is None else p(residual, bf16, shape, "residual"),
+            p(weight, bf16, (self.H,), "weight"), eps,
+            None if residual_out is None else p(residual_out, bf16, shape, "residual_out"),
+            None if y is None else p(y, bf16, shape, "y"),
+            None if rows8 is None else p(rows8, torch.uint8, (self.R, self.T, self.H + ROW8_TAIL), "rows8"),
+            self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_rms_norm")
 
     def quantize_rows(self, x, splits: Splits, rows8, stream=None):
         """8-bit rows of the live rows of an arena x [arena_rows][K] (a2av_quantize_rows)."""
-        import torch
-
         K = _width(x, "x")
-        _check(self.lib, self.lib.a2av_quantize_rows(
-            self.handle, self._t(x, torch.bfloat16, (self.arena_rows, K), "x"), K, self._sp(splits),
-            self._t(rows8, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "rows8"),
-            _stream_ptr(stream, self.device)), "a2av_quantize_rows")
+        rc = self.lib.a2av_quantize_rows(
+            self.handle, self._p(x, torch.bfloat16, (self.arena_rows, K), "x"), K, self._sp(splits),
+            self._p(rows8, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "rows8"), self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_quantize_rows")
 
     def expert_matmul(self, x, w, splits: Splits, y, w_scale=None, activation=None, stream=None):
         """y[r] = act(x[r] . w[e]^T) for every live row r, e its expert (a2av_expert_matmul).
@@ -442,53 +446,56 @@ class Plan:
         w [E][Nw][K] bf16 with x bf16 [arena_rows][K], or float8_e4m3fn with
         w_scale fp32 [E][Nw] and x 8-bit rows [arena_rows][K+16]; y bf16
         [arena_rows][N].  activation "swiglu": Nw = 2N, gate rows then up rows."""
-        import torch
-
-        eight = getattr(w, "dtype", None) == torch.float8_e4m3fn
         K = _width(w, "w")
-        xt = self._t(x, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "x") if eight else \
-            self._t(x, torch.bfloat16, (self.arena_rows, K), "x")
-        self._matmul(xt, w, w.dtype if eight else torch.bfloat16, K, K, W_E4M3 if eight else W_BF16, 0,
-                     self._opt(w_scale, torch.float32, (self.E, w.shape[1] if w.dim() == 3 else 0), "w_scale"),
-                     splits, y, activation, stream)
+        if w.dtype is torch.float8_e4m3fn:
+            kind, dtype, xp = W_E4M3, w.dtype, self._p(x, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "x")
+        else:
+            kind, dtype, xp = W_BF16, torch.bfloat16, self._p(x, torch.bfloat16, (self.arena_rows, K), "x")
+        if w_scale is not None:
+            w_scale = self._p(w_scale, torch.float32, w.shape[:2], "w_scale")
+        self._matmul(xp, w, dtype, K, K, kind, 0, w_scale, splits, y, activation, stream)
 
     def expert_matmul_w4(self, x, w4, w_scale, splits: Splits, y, activation=None, stream=None):
         """``expert_matmul`` with 4-bit weights, for few rows per expert: w4 int32
         [E][Nw][K/8], w_scale bf16 [E][Nw][K/group] (``pack_weights_w4``), x bf16."""
-        import torch
-
         K = _width(w4, "w4") * 8
         groups = max(1, _width(w_scale, "w_scale"))
         if K % groups:
             raise A2avError(f"w_scale has {groups} groups, which do not divide K = {K}")
-        self._matmul(self._t(x, torch.bfloat16, (self.arena_rows, K), "x"), w4, torch.int32, K, K // 8, W_INT4,
-                     K // groups,
-                     self._t(w_scale, torch.bfloat16, (self.E, w4.shape[1] if w4.dim() == 3 else 0, groups), "w_scale"),
+        self._matmul(self._p(x, torch.bfloat16, (self.arena_rows, K), "x"), w4, torch.int32, K, K // 8, W_INT4,
+                     K // groups, self._p(w_scale, torch.bfloat16, (*w4.shape[:2], groups), "w_scale"),
                      splits, y, activation, stream)
 
-    def _matmul(self, x, w, w_dtype, K, w_width, weight_type, group, w_scale, splits, y, activation, stream):
-        import torch
-
-        if activation not in ACTIVATIONS:
+    def _matmul(self, x, w, w_dtype, K, w_width, kind, group, w_scale, splits, y, activation, stream):
+        act = ACTIVATIONS.get(activation, -1)
+        if act < 0:
             raise A2avError(f"activation must be None or 'swiglu', got {activation!r}")
-        act = ACTIVATIONS[activation]
         N = _width(y, "y")
-        _check(self.lib, self.lib.a2av_expert_matmul(
-            self.handle, x, self._t(w, w_dtype, (self.E, N << act, w_width), "w"), w_scale,
-            self._t(y, torch.bfloat16, (self.arena_rows, N), "y"), K, N, weight_type, group, act, self._sp(splits),
-            _stream_ptr(stream, self.device)), "a2av_expert_matmul")
+        rc = self.lib.a2av_expert_matmul(
+            self.handle, x, self._p(w, w_dtype, (self.E, N << act, w_width), "w"), w_scale,
+            self._p(y, torch.bfloat16, (self.arena_rows, N), "y"), K, N, kind, group, act, self._sp(splits),
+            self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_expert_matmul")
 
-    def _opt(self, t, dtype, shape, name):
-        return None if t is None else self._t(t, dtype, shape, name)
+    def _p(self, t, dtype, shape, name):
+        """Device pointer of a tensor that is as it has to be; else ``_t`` says what is wrong."""
+        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.device == self.device):
+            return t.data_ptr()
+        return self._t(t, dtype, shape, name)
+
+    def _s(self, stream):
+        return _raw_stream(self.device.index) if stream is None else stream.cuda_stream
 
     def _sp(self, splits):
         """The split arrays of this plan's sizes, on its device."""
         if not isinstance(splits, Splits):
             raise A2avError("splits must be a Splits")
-        if tuple(splits.send_counts.shape) != (self.R, self.E) or splits.send_counts.device != self.device:
+        if splits.send_counts.shape != (self.R, self.E) or splits.send_counts.device != self.device:
             raise A2avError(f"splits were made for {tuple(splits.send_counts.shape)} on {splits.send_counts.device}, "
                             f"the plan has {(self.R, self.E)} on {self.device}")
-        return ctypes.byref(splits.ptrs)
+        return splits.ptrs
 
     def set_wait_limit(self, polls: int = -1):
         """Main-loop poll limit of the TMA kernels' bounded waits for later

@@ -76,6 +76,19 @@ __device__ __forceinline__ int expert_of(long long t, const int32_t *pre, int E,
     return lo;
 }
 
+// Bounded wait that also ends when another warp of the block gave up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, long long limit, uint32_t *abort_flag,
+                                              uint32_t *status) {
+    volatile uint32_t *abort = abort_flag;
+    for (long long it = 0; it < limit; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+    }
+    *abort = 1;
+    atomicOr(status, kDevWaitTimeout);
+    return false;
+}
+
 // A 128-byte-swizzled tensor map with zeros outside; the reason of a failure in the last error.
 bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
                 const cuuint64_t *strides, const cuuint32_t *box);

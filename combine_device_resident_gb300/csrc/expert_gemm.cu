@@ -106,19 +106,6 @@ __device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap *m, 
         : "memory");
 }
 
-// Bounded wait that also ends when another warp of the block gave up.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, long long limit, Shared *sh,
-                                              uint32_t *status) {
-    volatile uint32_t *abort = &sh->abort;
-    for (long long it = 0; it < limit; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-    }
-    *abort = 1;
-    atomicOr(status, kDevWaitTimeout);
-    return false;
-}
-
 // One unit of work: rows [row, row + rows) of expert e times channel tile `ctile`.
 struct Tile {
     int e, row, rows, ctile;
@@ -205,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile w = tile_at(t, start, count, pre, E, ctiles);
                 const int n16 = (w.rows + 15) / 16 * 16;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (round > 0 && !wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, sh, a.status)) {
+                    if (round > 0 && !wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, &sh->abort, a.status)) {
                         ok = false;
                         break;
                     }
@@ -240,14 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile w = tile_at(t, start, count, pre, E, ctiles);
                 const int n16 = (w.rows + 15) / 16 * 16;
                 const int b = it & 1;
-                if (it >= 2 && !wait_or_abort(&sh->acc_empty[b], ((it >> 1) - 1) & 1, a.wait_polls, sh, a.status)) {
+                if (it >= 2 && !wait_or_abort(&sh->acc_empty[b], ((it >> 1) - 1) & 1, a.wait_polls, &sh->abort, a.status)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
                 const uint32_t idesc = kIdesc | (uint32_t)(n16 >> 3) << 17;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!wait_or_abort(&sh->full[s], round & 1, a.wait_polls, sh, a.status)) {
+                    if (!wait_or_abort(&sh->full[s], round & 1, a.wait_polls, &sh->abort, a.status)) {
                         ok = false;
                         break;
                     }
@@ -286,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kFp8 && store)
                 ws = __ldg(static_cast<const float *>(a.w_scale) + (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + chan);
             // one answer for the warp: the TMEM loads below want all of its lanes
-            const bool ready = wait_or_abort(&sh->acc_full[b], (it >> 1) & 1, a.wait_polls, sh, a.status);
+            const bool ready = wait_or_abort(&sh->acc_full[b], (it >> 1) & 1, a.wait_polls, &sh->abort, a.status);
             if (!__all_sync(0xffffffffu, ready)) break;
             tmem_fence_after();
             uint16_t *y = a.y + (size_t)w.row * a.N + chan;

@@ -236,19 +236,255 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kRing], (got / kRing) & 1);
 }
 
-template <int kMT, bool kSwiglu>
-cudaError_t launch_w4(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
-    constexpr int kRows = kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows;
-    const cuuint64_t halves = kSwiglu ? 2 : 1, row = (cuuint64_t)a.K / 2;
-    CUtensorMap m;
+// ---- many work items: rows shared out among the warps -------------------------
+//
+// A producer warp fills a ring of stages with the weights' boxes (every
+// consumer warp's kMT*16 rows at once) and the expert rows' same span of K; x is then read
+// once per block instead of once per warp, and a consumer keeps whole sums.
+constexpr int kXPitch = kSpan * 2 + 64;  // a row of x in a stage; 64 more bytes spread two rows over all banks
+
+template <int kW, int kMT, int kNT, bool kSwiglu, int kPer>
+__device__ __forceinline__ void stage_sums(const uint8_t *weights, const uint8_t *x, int words, const float *scale,
+                                           float (&acc)[kMT][4][4]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    constexpr int kChan = kW * kMT * (kSwiglu ? 8 : 16);
+#pragma unroll
+    for (int j0 = 0; j0 < 8; j0 += kPer) {
+        if (j0 >= words) break;
+        float part[kMT][kNT][4] = {};
+#pragma unroll
+        for (int j = j0; j < j0 + kPer; ++j) {
+            uint4 b[kNT];
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+                b[n] = *reinterpret_cast<const uint4 *>(x + (n * 8 + g) * kXPitch + j * 64 + t * 16);
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                const int low = kSwiglu ? (warp * kMT + m) * 8 : (warp * kMT + m) * 16;
+                const int high = kSwiglu ? kChan + low : low + 8;
+                const uint32_t at = (j ^ g) * 16 + t * 4 + g * 128;
+                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(weights + low * 128 + at);
+                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(weights + high * 128 + at);
+                const uint32_t p0 = pair_of(w0, 0), p1 = pair_of(w0, 1), p2 = pair_of(w0, 2), p3 = pair_of(w0, 3);
+                const uint32_t q0 = pair_of(w1, 0), q1 = pair_of(w1, 1), q2 = pair_of(w1, 2), q3 = pair_of(w1, 3);
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) {
+                    mma16816(part[m][n], p0, q0, p1, q1, b[n].x, b[n].y);
+                    mma16816(part[m][n], p2, q2, p3, q3, b[n].z, b[n].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            const float s0 = scale[(j0 / kPer * kMT + m) * 2], s1 = scale[(j0 / kPer * kMT + m) * 2 + 1];
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+                acc[m][n][0] = fmaf(s0, part[m][n][0], acc[m][n][0]);
+                acc[m][n][1] = fmaf(s0, part[m][n][1], acc[m][n][1]);
+                acc[m][n][2] = fmaf(s1, part[m][n][2], acc[m][n][2]);
+                acc[m][n][3] = fmaf(s1, part[m][n][3], acc[m][n][3]);
+            }
+        }
+    }
+}
+
+struct SharedRows {
+    uint64_t full[4], empty[4];
+    uint32_t abort;
+    int32_t warp_sum[32];
+};
+
+// kPer: 32-wide steps per group of K.
+template <int kW, int kMT, bool kSwiglu, int kPer, int kRing>
+__global__ void __launch_bounds__((kW + 1) * 32, 2)
+    expert_w4_rows_kernel(const __grid_constant__ CUtensorMap map_w, const MatmulArgs a) {
+    constexpr int kRows = kW * kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows, kBlock = (kW + 1) * 32;
+    constexpr int kWBytes = kRows * 128, kStage = kWBytes + (kMaxRows * kXPitch + 1023) / 1024 * 1024;
+    extern __shared__ uint8_t raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    SharedRows *sh = reinterpret_cast<SharedRows *>(ring + kRing * kStage);
+    const int E = a.g.E;
+    int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
+    int32_t *count = start + E;
+    int32_t *pre = count + E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], kW);
+        }
+        sh->abort = 0;
+        fence_mbar_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
+    }
+    grid_dependency_wait();
+    const int total = place_experts<kBlock>(a, kMaxRows, start, count, pre, sh->warp_sum);  // ends in a barrier
+    const int blocks = (a.N + kChan - 1) / kChan;
+    const long long items = (long long)total * blocks;
+    const int spans = (a.K + kSpan - 1) / kSpan;
+
+    if (warp == kW) {
+        int s = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
+            const Item w = item_at(t, start, count, pre, E, blocks);
+            const uint8_t *x = a.x + (size_t)(w.row + lane) * a.x_pitch;
+            for (int span = 0; span < spans; ++span) {
+                if (round > 0) {
+                    const bool in = wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, &sh->abort, a.status);
+                    if (!__all_sync(0xffffffffu, in)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                uint8_t *stage = ring + s * kStage;
+                const uint32_t bytes = min(kSpan, a.K - span * kSpan) * 2;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh->full[s], kWBytes + w.rows * bytes);
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                        "%3, %4, %5}], [%6];" ::"r"(smem_u32(stage)),
+                        "l"(&map_w), "r"(span * (kSpan / 8)), "r"(w.block * kChan), "r"(0), "r"(w.e),
+                        "r"(smem_u32(&sh->full[s]))
+                        : "memory");
+                }
+                __syncwarp();
+                if (lane < w.rows)
+                    bulk_load(stage + kWBytes + lane * kXPitch, x + (size_t)span * kSpan * 2, bytes, &sh->full[s]);
+                if (++s == kRing) {
+                    s = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok && lane == 0)  // given up: every load that was issued lands before the block ends
+            for (int i = 0; i < kRing; ++i) {
+                const uint32_t fills = round + (i < s ? 1 : 0);
+                if (fills > 0) mbar_wait_bounded(&sh->full[i], (fills - 1) & 1);
+            }
+    } else {
+        constexpr int kGroups = 8 / kPer;  // groups of a stage
+        const int g = lane >> 2, q = lane & 3;
+        const int groups = a.K / a.group;
+        int s = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
+            const Item w = item_at(t, start, count, pre, E, blocks);
+            const uint16_t *from[kMT][2];
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int chan = w.block * kChan + (kSwiglu ? (warp * kMT + m) * 8 : (warp * kMT + m) * 16 + h * 8) + g;
+                    const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (kSwiglu && h ? a.N : 0) + min(chan, a.N - 1);
+                    from[m][h] = static_cast<const uint16_t *>(a.w_scale) + row * groups;
+                }
+            // the scales of a stage, one stage ahead
+            uint16_t next[kGroups * kMT * 2];
+            auto fetch = [&](int span) {
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = min(span * kGroups + i, groups - 1);
+                            next[(i * kMT + m) * 2 + h] = __ldg(from[m][h] + at);
+                        }
+            };
+            fetch(0);
+            float acc[kMT][4][4] = {};
+            for (int span = 0; span < spans; ++span) {
+                float scale[kGroups * kMT * 2];
+#pragma unroll
+                for (int i = 0; i < kGroups * kMT * 2; ++i) scale[i] = __uint_as_float((uint32_t)next[i] << 16);
+                fetch(min(span + 1, spans - 1));
+                const bool in = wait_or_abort(&sh->full[s], round & 1, a.wait_polls, &sh->abort, a.status);
+                if (!__all_sync(0xffffffffu, in)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t *stage = ring + s * kStage;
+                const int words = min(kSpan, a.K - span * kSpan) / 32;
+                if (w.rows <= 8) stage_sums<kW, kMT, 1, kSwiglu, kPer>(stage, stage + kWBytes, words, scale, acc);
+                else if (w.rows <= 16) stage_sums<kW, kMT, 2, kSwiglu, kPer>(stage, stage + kWBytes, words, scale, acc);
+                else stage_sums<kW, kMT, 4, kSwiglu, kPer>(stage, stage + kWBytes, words, scale, acc);
+                __syncwarp();  // every lane has read the stage
+                if (lane == 0) mbar_arrive(&sh->empty[s]);
+                if (++s == kRing) {
+                    s = 0;
+                    ++round;
+                }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = n * 8 + q * 2 + c;
+                        const int chan = w.block * kChan + (warp * kMT + m) * (kSwiglu ? 8 : 16) + g;
+                        if (r >= w.rows) continue;
+                        uint16_t *y = a.y + (size_t)(w.row + r) * a.N + chan;
+                        const float lo = acc[m][n][c], hi = acc[m][n][c + 2];
+                        if (kSwiglu) {
+                            if (chan < a.N)
+                                y[0] = __bfloat16_as_ushort(
+                                    __float2bfloat16_rn(__fdividef(lo, 1.0f + __expf(-lo)) * hi));
+                        } else {
+                            if (chan < a.N) y[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+                            if (chan + 8 < a.N) y[8] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
+                        }
+                    }
+        }
+    }
+}
+
+cudaError_t map_words(CUtensorMap *m, const MatmulArgs &a, bool swiglu, int chan) {
+    const cuuint64_t halves = swiglu ? 2 : 1, row = (cuuint64_t)a.K / 2;
     // w as [E][gate, up][N][K/8]
     const cuuint64_t dims[4] = {(cuuint64_t)a.K / 8, (cuuint64_t)a.N, halves, (cuuint64_t)a.g.E};
     const cuuint64_t strides[3] = {row, a.N * row, halves * a.N * row};
-    const cuuint32_t box[4] = {kSpan / 8, kChan, (cuuint32_t)halves, 1};
-    if (!encode_map(&m, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, a.w, dims, strides, box)) return cudaErrorInvalidValue;
+    const cuuint32_t box[4] = {kSpan / 8, (cuuint32_t)chan, (cuuint32_t)halves, 1};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, a.w, dims, strides, box) ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int kW, int kMT, bool kSwiglu, int kPer, int kRing>
+cudaError_t launch_w4_rows(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    constexpr int kRows = kW * kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows;
+    constexpr int kStage = kRows * 128 + (kMaxRows * kXPitch + 1023) / 1024 * 1024;
+    CUtensorMap m;
+    cudaError_t e = map_words(&m, a, kSwiglu, kChan);
+    if (e != cudaSuccess) return e;
+    const auto kernel = expert_w4_rows_kernel<kW, kMT, kSwiglu, kPer, kRing>;
+    const size_t smem = 1024 + (size_t)kRing * kStage + sizeof(SharedRows) + (size_t)a.g.E * 3 * 4;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.g.R * a.g.T * a.g.k;
+    const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxRows) * ((a.N + kChan - 1) / kChan);
+    const int grid = (int)(most < 2 * p.num_sms ? most : 2 * p.num_sms);
+    return launch_pdl(kernel, grid, (kW + 1) * 32, smem, s, m, a);
+}
+
+template <int kW, int kMT, bool kSwiglu, int kRing>
+cudaError_t launch_w4_group(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    return a.group == 32   ? launch_w4_rows<kW, kMT, kSwiglu, 1, kRing>(p, a, s)
+           : a.group == 64 ? launch_w4_rows<kW, kMT, kSwiglu, 2, kRing>(p, a, s)
+                           : launch_w4_rows<kW, kMT, kSwiglu, 4, kRing>(p, a, s);
+}
+
+template <int kMT, bool kSwiglu>
+cudaError_t launch_w4(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    constexpr int kRows = kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows;
+    CUtensorMap m;
+    cudaError_t e = map_words(&m, a, kSwiglu, kChan);
+    if (e != cudaSuccess) return e;
     const size_t smem = 1024 + (size_t)kWarps * (kStages / kMT) * kRows * 128 + (size_t)kWarps * kRows * (kMaxRows + 1) * 4 +
                         sizeof(Shared4) + (size_t)a.g.E * 3 * 4;
-    cudaError_t e = cudaFuncSetAttribute(expert_w4_kernel<kMT, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(expert_w4_kernel<kMT, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.g.R * a.g.T * a.g.k;
@@ -260,10 +496,9 @@ cudaError_t launch_w4(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s)
 }  // namespace
 
 cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s) {
-    // 32 weight rows per item halve what is read of x, once there are items enough for every SM
     const long long rows = (long long)a.g.R * a.g.T * a.g.k, experts = rows < a.g.E ? rows : a.g.E;
-    const bool wide = experts * (swiglu ? 2 : 1) * a.N / 32 >= 4 * p.num_sms;
-    if (wide) return swiglu ? launch_w4<2, true>(p, a, s) : launch_w4<2, false>(p, a, s);
+    const bool wide = experts * (swiglu ? 2 : 1) * a.N / 128 >= 2 * p.num_sms;
+    if (wide) return swiglu ? launch_w4_group<8, 1, true, 3>(p, a, s) : launch_w4_group<8, 1, false, 3>(p, a, s);
     return swiglu ? launch_w4<1, true>(p, a, s) : launch_w4<1, false>(p, a, s);
 }
 

@@ -57,9 +57,16 @@ __device__ __forceinline__ bool row_active(const NormArgs &a, int row) {
     return row < __ldg(a.window_base + a.g.R - 1) + __ldg(a.recv_total + a.g.R - 1);
 }
 
+// The first row from `row` on, in steps of the grid, that takes part; a.rows if none.
+template <bool kNorm>
+__device__ __forceinline__ int next_row(const NormArgs &a, long long row) {
+    while (row < a.rows && !row_active<kNorm>(a, (int)row)) row += gridDim.x;
+    return (int)min(row, (long long)a.rows);
+}
+
 // V 16-byte vectors of the row per thread (vector tid + j * blockDim).
-template <int V, bool kNorm>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
+template <int V, int kThreads, int kBlocks, bool kNorm>
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_kernel(NormArgs a) {
     __shared__ float part[2][2][32];  // [row parity][sum, max][warp]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
     const int nvec = a.H >> 3;
@@ -72,17 +79,23 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
         w[j] = kNorm && i < nvec ? ld_stream_v4(a.weight + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
     }
     int parity = 0;
-    for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        if (!row_active<kNorm>(a, row)) continue;
+    uint4 xv[V], rv[V];
+    int row = next_row<kNorm>(a, blockIdx.x);
+    auto load = [&] {  // the next row is asked for while this one is finished
+        if (row >= a.rows) return;
         const size_t at = (size_t)row * a.H;
-        float t[V][8];
-        uint4 xv[V], rv[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = tid + j * blockDim.x;
             xv[j] = i < nvec ? ld_row(a.x + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
             rv[j] = kNorm && a.residual && i < nvec ? ld_row(a.residual + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
         }
+    };
+    load();
+    while (row < a.rows) {
+        const size_t at = (size_t)row * a.H;
+        uint8_t *q = a.rows8 ? a.rows8 + (size_t)row * (a.H + 16) : nullptr;
+        float t[V][8];
         float sum = 0.0f, peak = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -110,6 +123,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
             if (kNorm && a.residual_out && i < nvec)
                 st_v4(a.residual_out + at + (size_t)i * 8, make_uint4(zs[0], zs[1], zs[2], zs[3]));
         }
+        row = next_row<kNorm>(a, (long long)row + gridDim.x);
+        load();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             if (kNorm) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -132,7 +147,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
         if (kNorm) peak *= r;
         const bool zero = peak < kZeroRow;  // false for NaN
         const float inv = zero ? 0.0f : kLow8 / peak;
-        uint8_t *q = a.rows8 ? a.rows8 + (size_t)row * (a.H + 16) : nullptr;
         if (q && tid == 0)
             st_v4(q + a.H, make_uint4(__float_as_uint(zero ? 0.0f : peak / kLow8), 0, 0, 0));
 #pragma unroll
@@ -156,23 +170,26 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
     }
 }
 
-template <int V>
-cudaError_t launch_v(const a2av_plan_s &p, const NormArgs &a, bool norm, cudaStream_t s) {
-    const int nvec = a.H / 8;
-    const int block = ((nvec + V - 1) / V + 31) / 32 * 32;
-    const int resident = 2048 / block < 1 ? 1 : 2048 / block;
-    const long long cap = (long long)p.num_sms * resident;
-    const int grid = (int)(a.rows < cap ? a.rows : cap);
-    return norm ? launch_pdl(norm_kernel<V, true>, grid, block, 0, s, a)
-                : launch_pdl(norm_kernel<V, false>, grid, block, 0, s, a);
+template <int V, int kThreads, int kBlocks, bool kNorm>
+cudaError_t launch_rows(const a2av_plan_s &p, const NormArgs &a, cudaStream_t s) {
+    const int block = ((a.H / 8 + V - 1) / V + 31) / 32 * 32;
+    const long long cap = (long long)p.num_sms * (kThreads * kBlocks / block);
+    return launch_pdl(norm_kernel<V, kThreads, kBlocks, kNorm>, (int)(a.rows < cap ? a.rows : cap), block, 0, s, a);
 }
 
 }  // namespace
 
+// Two vectors per thread and room for 64 registers (two blocks of 512 threads
+// per SM): with the next row's loads held in registers that is 64 KiB in
+// flight per SM.  65,536 x 7168 to 8 bits: 492 us (6.68 TB/s); one vector and
+// 1024 threads 586 us, two and three blocks (42 registers, spills) 621 us,
+// four vectors 611-676 us.  Without the norm the row needs fewer registers and
+// a third block pays: 32,768 x 2048 33.3 us against 37.1 us.  Longer rows take
+// as many threads as a block has.
 cudaError_t launch_norm(const a2av_plan_s &p, const NormArgs &a, bool norm, cudaStream_t s) {
-    if (a.H <= 8192) return launch_v<1>(p, a, norm, s);
-    if (a.H <= 16384) return launch_v<2>(p, a, norm, s);
-    return launch_v<4>(p, a, norm, s);
+    if (a.H > 16384) return norm ? launch_rows<4, 1024, 1, true>(p, a, s) : launch_rows<4, 1024, 1, false>(p, a, s);
+    if (a.H > 8192) return norm ? launch_rows<2, 1024, 1, true>(p, a, s) : launch_rows<2, 1024, 1, false>(p, a, s);
+    return norm ? launch_rows<2, 512, 2, true>(p, a, s) : launch_rows<2, 512, 3, false>(p, a, s);
 }
 
 }  // namespace a2av
