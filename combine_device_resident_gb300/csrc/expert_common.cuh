@@ -76,17 +76,30 @@ __device__ __forceinline__ int expert_of(long long t, const int32_t *pre, int E,
     return lo;
 }
 
-// Bounded wait that also ends when another warp of the block gave up.
+// Bounded wait that also ends when another warp of the block gave up; a
+// warp that gives up tells the other block of its pair, too (`peer`, the
+// address of that block's flag, or 0).
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, long long limit, uint32_t *abort_flag,
-                                              uint32_t *status) {
+                                              uint32_t *status, uint32_t peer = 0) {
     volatile uint32_t *abort = abort_flag;
     for (long long it = 0; it < limit; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
     *abort = 1;
+    if (peer) asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(peer) : "memory");
     atomicOr(status, kDevWaitTimeout);
     return false;
+}
+
+// One answer for the warp.
+__device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
+
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(v));
+    return v != 0;
 }
 
 // A 128-byte-swizzled tensor map with zeros outside; the reason of a failure in the last error.

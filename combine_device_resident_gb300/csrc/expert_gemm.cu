@@ -8,12 +8,15 @@
 // of c rows costs ceil(c/16)*16 columns, not a multiple of 128, and a group of
 // a few rows streams the weights once with a narrow instruction.
 //
-// One persistent block per SM: warp 0 feeds a ring of shared-memory stages by
-// TMA, warp 1 issues the matrix instructions into one of two TMEM
-// accumulators, warps 2-5 drain the other one (lane = channel, column = row),
-// apply scales and activation in fp32 and store bf16.
+// One persistent pair of blocks per two SMs (a cluster, cta_group::2): each
+// block loads its 128 of the tile's 256 weight rows and half of its expert
+// rows, and the instruction reads both halves of the latter out of the two
+// shared memories.  In each block warp 0 feeds a ring of stages by TMA; warp 1 of the
+// first block issues the instructions into one of two TMEM accumulators;
+// warps 2-5 drain the other one (lane = channel, column = row), apply scales
+// and activation in fp32 and store bf16.
 //
-// SwiGLU: a tile holds the gate and the up weights of 64 channels in
+// SwiGLU: a block's tile holds the gate and the up weights of 64 channels in
 // alternating blocks of eight rows (one TMA box of a five-dimensional view
 // of w), so the two halves of a channel sit eight TMEM lanes apart in the
 // same warp: one shuffle per two rows brings them together.
@@ -25,12 +28,12 @@ namespace a2av {
 namespace {
 
 constexpr int kThreads = 192;       // producer warp, matrix warp, four epilogue warps
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 constexpr int kRowBytes = 128;      // K bytes per stage row: one 128-byte swizzle span
-constexpr int kTileM = 128;         // weight rows per tile
+constexpr int kTileM = 128;         // weight rows per block of a pair
 constexpr int kTileN = 256;         // expert rows per tile, at most
 constexpr int kABytes = kTileM * kRowBytes;
-constexpr int kBBytes = kTileN * kRowBytes;
+constexpr int kBBytes = kTileN / 2 * kRowBytes;  // half of them in each block
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of x
 constexpr int kBand = 8;            // row tiles of an expert that run with one channel tile in turn
@@ -40,6 +43,7 @@ struct __align__(8) Shared {
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     uint32_t abort;
+    uint32_t other_fills;  // of the ring, by the other block
     int32_t warp_sum[8];
 };
 
@@ -56,19 +60,36 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
     if (kFp8)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc)
             : "memory");
     else
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc)
             : "memory");
 }
+// Arrives on `bar` of this block, or of both blocks of the pair, once the instructions issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
+}
+__device__ __forceinline__ void mma_commit_both(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// The address of this block's shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -91,18 +112,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *m, int k, int row, uint64_t *bar) {
+// Loads into this block's shared memory that count on a barrier of the pair's first block (`bar`).
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *m, int k, int row, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(m), "r"(k), "r"(row), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(k), "r"(row), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap *m, int k, int block, int e, uint64_t *bar) {
+__device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap *m, int k, int block, int e, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(m), "r"(k), "r"(0), "r"(block), "r"(e), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(m), "r"(k), "r"(0), "r"(block), "r"(e), "r"(bar)
         : "memory");
 }
 
@@ -126,16 +148,21 @@ __device__ __forceinline__ Tile tile_at(long long t, const int32_t *start, const
     Tile r;
     r.e = lo;
     r.ctile = rem / wide;
-    // even shares, multiples of 16 rows (the last one takes what is left)
-    const int share = ((n + rt - 1) / rt + 15) / 16 * 16;
+    // even shares, multiples of 32 rows (the last one takes what is left)
+    const int share = ((n + rt - 1) / rt + 31) / 32 * 32;
     const int first = (band * kBand + rem % wide) * share;
     r.row = start[lo] + first;
     r.rows = max(0, min(share, n - first));
     return r;
 }
 
+__device__ __forceinline__ Tile uniform(const Tile &t) {
+    return Tile{__shfl_sync(0xffffffffu, t.e, 0), __shfl_sync(0xffffffffu, t.row, 0), __shfl_sync(0xffffffffu, t.rows, 0),
+                __shfl_sync(0xffffffffu, t.ctile, 0)};
+}
+
 template <bool kFp8, bool kSwiglu>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_big,
                        const __grid_constant__ CUtensorMap map_small, const MatmulArgs a) {
     extern __shared__ uint8_t raw[];
@@ -145,7 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
     int32_t *count = start + E;
     int32_t *pre = count + E;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const uint32_t rank = blockIdx.x & 1;  // in the pair (the cluster's dimension is two)
+    const uint32_t peer_abort = in_block(&sh->abort, rank ^ 1);
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -154,16 +183,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh->acc_full[b], 1);
-            mbar_init(&sh->acc_empty[b], 4);
+            mbar_init(&sh->acc_empty[b], 8);  // four warps in each block
         }
         mbar_init(&sh->drain, 1);
         sh->abort = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem))
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem))
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     if (tid == 64) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
@@ -174,88 +203,107 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tmem_fence_before();
     const int total = place_experts<kThreads>(a, kTileN, start, count, pre, sh->warp_sum);  // ends in a barrier
+    cluster_sync();  // the other block's barriers are set up, too
     tmem_fence_after();
 
     const uint32_t tmem = sh->tmem;
-    constexpr int kChan = kSwiglu ? kTileM / 2 : kTileM;  // output channels per tile
-    const int ctiles = (a.N + kChan - 1) / kChan;
+    constexpr int kChan = kSwiglu ? kTileM / 2 : kTileM;  // output channels per block
+    const int ctiles = (a.N + 2 * kChan - 1) / (2 * kChan);
     const long long tiles = (long long)total * ctiles;
     constexpr int kStep = kFp8 ? kRowBytes : kRowBytes / 2;  // K elements per stage
     const int kblocks = (a.K + kStep - 1) / kStep;
 
-    if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t round = 0;  // times the ring has gone round
-            bool ok = true;
-            for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const Tile w = tile_at(t, start, count, pre, E, ctiles);
-                const int n16 = (w.rows + 15) / 16 * 16;
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    if (round > 0 && !wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, &sh->abort, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t at = smem_u32(stages + s * kStageBytes);
-                    mbar_arrive_expect_tx(&sh->full[s], kABytes + n16 * kRowBytes);
-                    tma_weights(at, &map_w, kb * kStep, w.ctile * (kChan / 8), w.e, &sh->full[s]);
+    // Where the loads stand (warp 0): tile, K block, stage, the parity that
+    // says a stage is free, and how many fills were issued.
+    long long put_t = blockIdx.x / 2;
+    int put_kb = 0, put_s = 0;
+    uint32_t put_parity = 1, fills = 0;
+    // Issues fills as stages come free, until the end (true) or a give-up; or, without waiting, until
+    // `until` were issued.  The whole warp runs the loop and one elected lane issues, so that the
+    // instructions' operands are uniform registers.
+    auto produce = [&](bool wait, uint32_t until) {
+        Tile w;
+        for (; put_t < tiles; put_t += gridDim.x / 2, put_kb = 0) {
+            w = uniform(tile_at(put_t, start, count, pre, E, ctiles));
+            const int half = (w.rows + 31) / 32 * 16;  // expert rows per block
+            const int row = w.row + rank * half, block = (w.ctile * 2 + rank) * (kChan / 8);
+            for (; put_kb < kblocks; ++put_kb) {
+                if (wait ? !all_of(wait_or_abort(&sh->empty[put_s], put_parity, a.wait_polls, &sh->abort, a.status,
+                                                 peer_abort))
+                         : (int32_t)(until - fills) <= 0)
+                    return false;
+                if (elect_one()) {
+                    const uint32_t at = smem_u32(stages) + put_s * kStageBytes, bar = in_block(&sh->full[put_s], 0);
+                    const int k = put_kb * kStep;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[put_s], 2 * (kABytes + half * kRowBytes));
+                    tma_weights(at, &map_w, k, block, w.e, bar);
                     int i = 0;
-                    for (; i + kBoxBig <= n16; i += kBoxBig)
-                        tma_rows(at + kABytes + i * kRowBytes, &map_big, kb * kStep, w.row + i, &sh->full[s]);
-                    for (; i < n16; i += kBoxSmall)
-                        tma_rows(at + kABytes + i * kRowBytes, &map_small, kb * kStep, w.row + i, &sh->full[s]);
-                    if (++s == kStages) {
-                        s = 0;
-                        ++round;
-                    }
+                    for (; i + kBoxBig <= half; i += kBoxBig)
+                        tma_rows(at + kABytes + i * kRowBytes, &map_big, k, row + i, bar);
+                    for (; i < half; i += kBoxSmall)
+                        tma_rows(at + kABytes + i * kRowBytes, &map_small, k, row + i, bar);
+                }
+                __syncwarp();
+                ++fills;
+                if (++put_s == kStages) {
+                    put_s = 0;
+                    put_parity ^= 1;
                 }
             }
-            if (!ok)  // given up: let every load that was issued land before the block ends
-                for (int i = 0; i < kStages; ++i) {
-                    const uint32_t fills = round + (i < s ? 1 : 0);
-                    if (fills > 0) mbar_wait_bounded(&sh->full[i], (fills - 1) & 1);
-                }
         }
+        return true;
+    };
+
+    if (warp == 0) {
+        bool ok = produce(true, 0);
+        // the arrivals on the last fills' barriers come from the first block: they are in before this one may end
+        for (int i = 0, s = put_s, par = put_parity; ok && i < kStages; ++i) {
+            ok = all_of(wait_or_abort(&sh->empty[s], par, a.wait_polls, &sh->abort, a.status, peer_abort));
+            if (++s == kStages) {
+                s = 0;
+                par ^= 1;
+            }
+        }
+        // how far this block got, for the other one if the pair gives up
+        if (lane == 0)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_block(&sh->other_fills, rank ^ 1)), "r"(fills)
+                         : "memory");
     } else if (warp == 1) {
-        if (lane == 0) {
-            // fp32 accumulator; A and B bf16 (1) or e4m3 (0), both K-major
-            constexpr uint32_t kIdesc = 1u << 4 | (kFp8 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)(kTileM >> 4) << 24;
-            int s = 0;
-            uint32_t round = 0, it = 0;
+        if (rank == 0) {
+            // fp32 accumulator; A and B bf16 (1) or e4m3 (0), both K-major; M of the pair
+            constexpr uint32_t kIdesc = 1u << 4 | (kFp8 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)(2 * kTileM >> 4) << 24;
+            int s = 0, b = 0;
+            uint32_t parity = 0, acc_parity = 1;
             bool ok = true;
-            for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++it) {
-                const Tile w = tile_at(t, start, count, pre, E, ctiles);
-                const int n16 = (w.rows + 15) / 16 * 16;
-                const int b = it & 1;
-                if (it >= 2 && !wait_or_abort(&sh->acc_empty[b], ((it >> 1) - 1) & 1, a.wait_polls, &sh->abort, a.status)) {
-                    ok = false;
-                    break;
-                }
+            for (long long t = blockIdx.x / 2; ok && t < tiles; t += gridDim.x / 2) {
+                const int rows = uniform(tile_at(t, start, count, pre, E, ctiles)).rows;
+                ok = all_of(wait_or_abort(&sh->acc_empty[b], acc_parity, a.wait_polls, &sh->abort, a.status, peer_abort));
                 tmem_fence_after();
-                const uint32_t idesc = kIdesc | (uint32_t)(n16 >> 3) << 17;
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!wait_or_abort(&sh->full[s], round & 1, a.wait_polls, &sh->abort, a.status)) {
-                        ok = false;
-                        break;
-                    }
+                const uint32_t idesc = kIdesc | (uint32_t)((rows + 31) / 32 * 4) << 17, d = tmem + b * kTileN;
+                for (int kb = 0; ok && kb < kblocks; ++kb) {
+                    ok = all_of(wait_or_abort(&sh->full[s], parity, a.wait_polls, &sh->abort, a.status, peer_abort));
+                    if (!ok) break;
                     tmem_fence_after();
-                    const uint32_t at = smem_u32(stages + s * kStageBytes);
-                    const uint64_t da = operand_desc(at), db = operand_desc(at + kABytes);
-                    if (n16 > 0) {
+                    if (elect_one()) {
+                        const uint32_t at = smem_u32(stages) + s * kStageBytes;
+                        const uint64_t da = operand_desc(at), db = operand_desc(at + kABytes);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)  // 32 bytes of K per instruction
-                            mma<kFp8>(tmem + b * kTileN, da + j * 2, db + j * 2, idesc, kb > 0 || j > 0);
+                            mma<kFp8>(d, da + j * 2, db + j * 2, idesc, kb > 0 || j > 0);
+                        mma_commit_both(&sh->empty[s]);
+                        if (kb == kblocks - 1) mma_commit_both(&sh->acc_full[b]);
                     }
-                    mma_commit(&sh->empty[s]);
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
-                        ++round;
+                        parity ^= 1;
                     }
                 }
-                if (ok) mma_commit(&sh->acc_full[b]);
+                b ^= 1;
+                if (b == 0) acc_parity ^= 1;
             }
             if (!ok) {  // given up: let the instructions that were issued end before TMEM is freed
-                mma_commit(&sh->drain);
+                if (elect_one()) mma_commit(&sh->drain);
                 mbar_wait_bounded(&sh->drain, 0);
             }
         }
@@ -263,18 +311,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3;  // the TMEM lanes this warp may read
         uint32_t it = 0;
         const bool up = kSwiglu && (lane & 8);
-        for (long long t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+        for (long long t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, ++it) {
             const Tile w = tile_at(t, start, count, pre, E, ctiles);
             const int b = it & 1;
             // swiglu: lanes 0-7 gate of channels 0-7, 8-15 their up, 16-23 gate of channels 8-15, ...
-            const int chan = w.ctile * kChan + (kSwiglu ? quad * 16 + (lane >> 4) * 8 + (lane & 7) : quad * 32 + lane);
+            const int chan = (w.ctile * 2 + rank) * kChan +
+                             (kSwiglu ? quad * 16 + (lane >> 4) * 8 + (lane & 7) : quad * 32 + lane);
             const bool store = chan < a.N;
             float ws = 1.0f;
             if (kFp8 && store)
                 ws = __ldg(static_cast<const float *>(a.w_scale) + (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + chan);
             // one answer for the warp: the TMEM loads below want all of its lanes
-            const bool ready = wait_or_abort(&sh->acc_full[b], (it >> 1) & 1, a.wait_polls, &sh->abort, a.status);
-            if (!__all_sync(0xffffffffu, ready)) break;
+            if (!all_of(wait_or_abort(&sh->acc_full[b], (it >> 1) & 1, a.wait_polls, &sh->abort, a.status, peer_abort)))
+                break;
             tmem_fence_after();
             uint16_t *y = a.y + (size_t)w.row * a.N + chan;
             for (int c = 0; c < w.rows; c += 32) {
@@ -307,15 +356,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->acc_empty[b]);
+            if (lane == 0)  // the first block issues
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 in_block(&sh->acc_empty[b], 0))
+                             : "memory");
         }
     }
     __syncwarp();
     tmem_fence_before();
-    __syncthreads();
+    cluster_sync();  // both blocks are done with the other's shared memory and with TMEM
+    if (*(volatile uint32_t *)&sh->abort) {
+        // Given up (both blocks know: the flag is set in both before this
+        // barrier).  The block that is behind issues the loads the other has
+        // issued, so that every fill is whole, and the first block waits for
+        // them to land: the last fill of each stage.
+        if (warp == 0) {
+            produce(false, *(volatile uint32_t *)&sh->other_fills);
+            for (int i = 0; rank == 0 && i < kStages; ++i) {
+                if (--put_s < 0) {
+                    put_s = kStages - 1;
+                    put_parity ^= 1;
+                }
+                if (fills-- > 0) mbar_wait_bounded(&sh->full[put_s], put_parity ^ 1);
+                else break;
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1) {
         tmem_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
 
@@ -340,9 +411,9 @@ cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t 
                                          (int)smem);
     if (e != cudaSuccess) return e;
     // at most this many tiles: each expert with rows begins one more than its rows fill
-    const long long rows = (long long)a.g.R * a.g.T * a.g.k, chan = kSwiglu ? kTileM / 2 : kTileM;
+    const long long rows = (long long)a.g.R * a.g.T * a.g.k, chan = kSwiglu ? kTileM : 2 * kTileM;
     const long long most = ((rows < (long long)E ? rows : (long long)E) + rows / kTileN) * ((a.N + chan - 1) / chan);
-    const int grid = (int)(most < p.num_sms ? most : p.num_sms);
+    const int grid = 2 * (int)(most < p.num_sms / 2 ? most : p.num_sms / 2);
     return launch_pdl(expert_gemm_kernel<kFp8, kSwiglu>, grid, kThreads, smem, s, mw, mb, ms, a);
 }
 

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         for (int span = (warp + i) % kWarps; ok && span < spans; span += kWarps) {
             const int s = got % kRing;
             const bool in = mbar_wait_bounded(&sh->full[warp][s], (got / kRing) & 1, a.wait_polls);
-            if (!__all_sync(0xffffffffu, in)) {
+            if (!all_of(in)) {
                 ok = false;
                 break;
             }
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__((kW + 1) * 32, 2)
             for (int span = 0; span < spans; ++span) {
                 if (round > 0) {
                     const bool in = wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, &sh->abort, a.status);
-                    if (!__all_sync(0xffffffffu, in)) {
+                    if (!all_of(in)) {
                         ok = false;
                         break;
                     }
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__((kW + 1) * 32, 2)
                 }
             }
         }
-        if (!ok && lane == 0)  // given up: every load that was issued lands before the block ends
+        if (lane == 0)  // every load that was issued lands before the block ends, also if the others gave up
             for (int i = 0; i < kRing; ++i) {
                 const uint32_t fills = round + (i < s ? 1 : 0);
                 if (fills > 0) mbar_wait_bounded(&sh->full[i], (fills - 1) & 1);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__((kW + 1) * 32, 2)
                 for (int i = 0; i < kGroups * kMT * 2; ++i) scale[i] = __uint_as_float((uint32_t)next[i] << 16);
                 fetch(min(span + 1, spans - 1));
                 const bool in = wait_or_abort(&sh->full[s], round & 1, a.wait_polls, &sh->abort, a.status);
-                if (!__all_sync(0xffffffffu, in)) {
+                if (!all_of(in)) {
                     ok = false;
                     break;
                 }
