@@ -35,7 +35,8 @@ constexpr int kTileN = 256;         // expert rows per tile, at most
 constexpr int kABytes = kTileM * kRowBytes;
 constexpr int kBBytes = kTileN / 2 * kRowBytes;  // half of them in each block
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of x
+// Rows of x a block loads at once: the first box that holds its share (128 at most).
+__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : i == 1 ? 64 : 128; }
 constexpr int kBand = 8;            // row tiles of an expert that run with one channel tile in turn
 
 struct __align__(8) Shared {
@@ -128,6 +129,10 @@ __device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap *m, 
         : "memory");
 }
 
+struct RowMaps {
+    CUtensorMap box[3];
+};
+
 // One unit of work: rows [row, row + rows) of expert e times channel tile `ctile`.
 struct Tile {
     int e, row, rows, ctile;
@@ -163,8 +168,8 @@ __device__ __forceinline__ Tile uniform(const Tile &t) {
 
 template <bool kFp8, bool kSwiglu>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_big,
-                       const __grid_constant__ CUtensorMap map_small, const MatmulArgs a) {
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x,
+                       const MatmulArgs a) {
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     Shared *sh = reinterpret_cast<Shared *>(stages + kStages * kStageBytes);
@@ -196,8 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (tid == 64) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_big));
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_small));
+        for (int i = 0; i < 3; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x.box[i]));
     }
     grid_dependency_wait();
 
@@ -218,37 +222,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     long long put_t = blockIdx.x / 2;
     int put_kb = 0, put_s = 0;
     uint32_t put_parity = 1, fills = 0;
+    const uint32_t base = smem_u32(stages), full0 = in_block(&sh->full[0], 0);
     // Issues fills as stages come free, until the end (true) or a give-up; or, without waiting, until
     // `until` were issued.  The whole warp runs the loop and one elected lane issues, so that the
-    // instructions' operands are uniform registers.
+    // instructions' operands are uniform registers; the next stage's barrier is looked at before the
+    // loads are issued, so that its answer is there afterwards.
     auto produce = [&](bool wait, uint32_t until) {
-        Tile w;
+        bool free = false;
         for (; put_t < tiles; put_t += gridDim.x / 2, put_kb = 0) {
-            w = uniform(tile_at(put_t, start, count, pre, E, ctiles));
+            const Tile w = uniform(tile_at(put_t, start, count, pre, E, ctiles));
             const int half = (w.rows + 31) / 32 * 16;  // expert rows per block
             const int row = w.row + rank * half, block = (w.ctile * 2 + rank) * (kChan / 8);
+            const int box = half <= box_rows(0) ? 0 : half <= box_rows(1) ? 1 : 2;
+            const CUtensorMap *const map = &map_x.box[box];
+            const uint32_t bytes = 2 * (kABytes + box_rows(box) * kRowBytes);
             for (; put_kb < kblocks; ++put_kb) {
-                if (wait ? !all_of(wait_or_abort(&sh->empty[put_s], put_parity, a.wait_polls, &sh->abort, a.status,
-                                                 peer_abort))
-                         : (int32_t)(until - fills) <= 0)
+                if (!wait ? (int32_t)(until - fills) <= 0
+                          : !free && !all_of(wait_or_abort(&sh->empty[put_s], put_parity, a.wait_polls, &sh->abort,
+                                                           a.status, peer_abort)))
                     return false;
-                if (elect_one()) {
-                    const uint32_t at = smem_u32(stages) + put_s * kStageBytes, bar = in_block(&sh->full[put_s], 0);
-                    const int k = put_kb * kStep;
-                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[put_s], 2 * (kABytes + half * kRowBytes));
-                    tma_weights(at, &map_w, k, block, w.e, bar);
-                    int i = 0;
-                    for (; i + kBoxBig <= half; i += kBoxBig)
-                        tma_rows(at + kABytes + i * kRowBytes, &map_big, k, row + i, bar);
-                    for (; i < half; i += kBoxSmall)
-                        tma_rows(at + kABytes + i * kRowBytes, &map_small, k, row + i, bar);
-                }
-                __syncwarp();
-                ++fills;
+                const int s = put_s;
                 if (++put_s == kStages) {
                     put_s = 0;
                     put_parity ^= 1;
                 }
+                free = wait && a.wait_polls > 0 && mbar_test_wait(&sh->empty[put_s], put_parity);
+                if (elect_one()) {
+                    const uint32_t at = base + s * kStageBytes, bar = full0 + s * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], bytes);
+                    tma_weights(at, &map_w, put_kb * kStep, block, w.e, bar);
+                    tma_rows(at + kABytes, map, put_kb * kStep, row, bar);
+                }
+                __syncwarp();
+                free = all_of(free);
+                ++fills;
             }
         }
         return true;
@@ -274,30 +281,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdesc = 1u << 4 | (kFp8 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)(2 * kTileM >> 4) << 24;
             int s = 0, b = 0;
             uint32_t parity = 0, acc_parity = 1;
-            bool ok = true;
+            bool ok = true, in = false;
             for (long long t = blockIdx.x / 2; ok && t < tiles; t += gridDim.x / 2) {
                 const int rows = uniform(tile_at(t, start, count, pre, E, ctiles)).rows;
                 ok = all_of(wait_or_abort(&sh->acc_empty[b], acc_parity, a.wait_polls, &sh->abort, a.status, peer_abort));
                 tmem_fence_after();
                 const uint32_t idesc = kIdesc | (uint32_t)((rows + 31) / 32 * 4) << 17, d = tmem + b * kTileN;
                 for (int kb = 0; ok && kb < kblocks; ++kb) {
-                    ok = all_of(wait_or_abort(&sh->full[s], parity, a.wait_polls, &sh->abort, a.status, peer_abort));
+                    ok = in || all_of(wait_or_abort(&sh->full[s], parity, a.wait_polls, &sh->abort, a.status, peer_abort));
                     if (!ok) break;
-                    tmem_fence_after();
-                    if (elect_one()) {
-                        const uint32_t at = smem_u32(stages) + s * kStageBytes;
-                        const uint64_t da = operand_desc(at), db = operand_desc(at + kABytes);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)  // 32 bytes of K per instruction
-                            mma<kFp8>(d, da + j * 2, db + j * 2, idesc, kb > 0 || j > 0);
-                        mma_commit_both(&sh->empty[s]);
-                        if (kb == kblocks - 1) mma_commit_both(&sh->acc_full[b]);
-                    }
-                    __syncwarp();
+                    const int now = s;
                     if (++s == kStages) {
                         s = 0;
                         parity ^= 1;
                     }
+                    in = mbar_test_wait(&sh->full[s], parity);
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = base + now * kStageBytes;
+                        const uint64_t da = operand_desc(at), db = operand_desc(at + kABytes);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)  // 32 bytes of K per instruction
+                            mma<kFp8>(d, da + j * 2, db + j * 2, idesc, kb > 0 || j > 0);
+                        mma_commit_both(&sh->empty[now]);
+                        if (kb == kblocks - 1) mma_commit_both(&sh->acc_full[b]);
+                    }
+                    __syncwarp();
+                    in = all_of(in);
                 }
                 b ^= 1;
                 if (b == 0) acc_parity ^= 1;
@@ -394,18 +404,20 @@ template <bool kFp8, bool kSwiglu>
 cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
     const cuuint64_t es = kFp8 ? 1 : 2, K = a.K, N = a.N, E = a.g.E, halves = kSwiglu ? 2 : 1;
     const cuuint32_t step = kRowBytes / (cuuint32_t)es;
-    CUtensorMap mw, mb, ms;
+    CUtensorMap mw;
+    RowMaps mx;
     // w as [E][N/8][gate, up][8][K]
     const cuuint64_t wd[5] = {K, 8, halves, N / 8, E};
     const cuuint64_t wst[4] = {K * es, N * K * es, 8 * K * es, halves * N * K * es};
     const cuuint32_t wb[5] = {step, 8, (cuuint32_t)halves, (cuuint32_t)(kTileM / 8 / halves), 1};
     const cuuint64_t xd[2] = {K, (cuuint64_t)a.arena_rows};
     const cuuint64_t xst[1] = {(cuuint64_t)a.x_pitch};
-    const cuuint32_t xb[2] = {step, kBoxBig}, xs[2] = {step, kBoxSmall};
     const CUtensorMapDataType type = kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!encode_map(&mw, type, 5, a.w, wd, wst, wb) || !encode_map(&mb, type, 2, a.x, xd, xst, xb) ||
-        !encode_map(&ms, type, 2, a.x, xd, xst, xs))
-        return cudaErrorInvalidValue;
+    if (!encode_map(&mw, type, 5, a.w, wd, wst, wb)) return cudaErrorInvalidValue;
+    for (int i = 0; i < 3; ++i) {
+        const cuuint32_t xb[2] = {step, (cuuint32_t)box_rows(i)};
+        if (!encode_map(&mx.box[i], type, 2, a.x, xd, xst, xb)) return cudaErrorInvalidValue;
+    }
     const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared) + (size_t)a.g.E * 3 * 4;
     cudaError_t e = cudaFuncSetAttribute(expert_gemm_kernel<kFp8, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
@@ -414,7 +426,7 @@ cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t 
     const long long rows = (long long)a.g.R * a.g.T * a.g.k, chan = kSwiglu ? kTileM : 2 * kTileM;
     const long long most = ((rows < (long long)E ? rows : (long long)E) + rows / kTileN) * ((a.N + chan - 1) / chan);
     const int grid = 2 * (int)(most < p.num_sms / 2 ? most : p.num_sms / 2);
-    return launch_pdl(expert_gemm_kernel<kFp8, kSwiglu>, grid, kThreads, smem, s, mw, mb, ms, a);
+    return launch_pdl(expert_gemm_kernel<kFp8, kSwiglu>, grid, kThreads, smem, s, mw, mx, a);
 }
 
 }  // namespace
