@@ -13,7 +13,7 @@
 // rows, and the instruction reads both halves of the latter out of the two
 // shared memories.  In each block warp 0 feeds a ring of stages by TMA; warp 1 of the
 // first block issues the instructions into one of two TMEM accumulators;
-// warps 2-5 drain the other one (lane = channel, column = row), apply scales
+// warps 2-9 drain the other one (lane = channel, column = row), apply scales
 // and activation in fp32 and store bf16.
 //
 // SwiGLU: a block's tile holds the gate and the up weights of 64 channels in
@@ -21,13 +21,15 @@
 // of w), so the two halves of a channel sit eight TMEM lanes apart in the
 // same warp: one shuffle per two rows brings them together.
 #include <cuda_bf16.h>
+#include <stddef.h>
 
 #include "expert_common.cuh"
 
 namespace a2av {
 namespace {
 
-constexpr int kThreads = 192;       // producer warp, matrix warp, four epilogue warps
+constexpr int kEpiWarps = 8;        // two for each quarter of the TMEM lanes
+constexpr int kThreads = 64 + kEpiWarps * 32;  // after the producer warp and the matrix warp
 constexpr int kStages = 6;
 constexpr int kRowBytes = 128;      // K bytes per stage row: one 128-byte swizzle span
 constexpr int kTileM = 128;         // weight rows per block of a pair
@@ -39,14 +41,17 @@ constexpr int kStageBytes = kABytes + kBBytes;
 __host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : i == 1 ? 64 : 128; }
 constexpr int kBand = 8;            // row tiles of an expert that run with one channel tile in turn
 
-struct __align__(8) Shared {
+struct Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     uint32_t abort;
     uint32_t other_fills;  // of the ring, by the other block
-    int32_t warp_sum[8];
+    int32_t warp_sum[kThreads / 32];
+    alignas(16) float x_scale[kEpiWarps][kTileN / 2];  // of the expert rows an epilogue warp takes
 };
+
+static_assert(sizeof(Shared) % 16 == 0 && offsetof(Shared, x_scale) % 16 == 0, "the scales are read four at a time");
 
 // Shared-memory operand descriptor: K-major, 128-byte swizzle, eight-row
 // groups 1024 bytes apart.
@@ -101,14 +106,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr)
         : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -188,7 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh->acc_full[b], 1);
-            mbar_init(&sh->acc_empty[b], 8);  // four warps in each block
+            mbar_init(&sh->acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&sh->drain, 1);
         sh->abort = 0;
@@ -318,7 +323,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        const int quad = warp & 3;  // the TMEM lanes this warp may read
+        // 32 columns at a time, the two warps of a quarter in turn
+        const int quad = warp & 3, side = (warp - 2) >> 2;
+        float *const scales = sh->x_scale[warp - 2];
         uint32_t it = 0;
         const bool up = kSwiglu && (lane & 8);
         for (long long t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, ++it) {
@@ -329,22 +336,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                              (kSwiglu ? quad * 16 + (lane >> 4) * 8 + (lane & 7) : quad * 32 + lane);
             const bool store = chan < a.N;
             float ws = 1.0f;
-            if (kFp8 && store)
-                ws = __ldg(static_cast<const float *>(a.w_scale) + (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + chan);
-            // one answer for the warp: the TMEM loads below want all of its lanes
+            if (kFp8) {
+                if (store)
+                    ws = __ldg(static_cast<const float *>(a.w_scale) + (size_t)w.e * a.N * (kSwiglu ? 2 : 1) +
+                               (up ? a.N : 0) + chan);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // the rows' scales, behind their values
+                    const int r = i * 64 + side * 32 + lane;
+                    if (r < w.rows)
+                        scales[i * 32 + lane] =
+                            __ldg(reinterpret_cast<const float *>(a.x + (size_t)(w.row + r) * a.x_pitch + a.K));
+                }
+                __syncwarp();
+            }
             if (!all_of(wait_or_abort(&sh->acc_full[b], (it >> 1) & 1, a.wait_polls, &sh->abort, a.status, peer_abort)))
                 break;
             tmem_fence_after();
             uint16_t *y = a.y + (size_t)w.row * a.N + chan;
-            for (int c = 0; c < w.rows; c += 32) {
+            for (int c = side * 32; c < w.rows; c += 64) {
                 float v[32];
-                float xs = 1.0f;
-                if (kFp8 && c + lane < w.rows)  // the row's scale behind its values
-                    xs = __ldg(reinterpret_cast<const float *>(a.x + (size_t)(w.row + c + lane) * a.x_pitch + a.K));
                 tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + b * kTileN + c, v);
                 if (kFp8) {
+                    const float4 *xs = reinterpret_cast<const float4 *>(scales + (c >> 6) * 32);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= ws * __shfl_sync(0xffffffffu, xs, i);
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x4 = xs[i];
+                        v[i * 4] *= ws * x4.x;
+                        v[i * 4 + 1] *= ws * x4.y;
+                        v[i * 4 + 2] *= ws * x4.z;
+                        v[i * 4 + 3] *= ws * x4.w;
+                    }
                 }
                 if (kSwiglu) {
                     // of rows i, i+1 the gate lane finishes the first, the up lane the second
