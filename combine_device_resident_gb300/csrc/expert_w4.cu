@@ -34,8 +34,8 @@ struct Shared4 {
 __device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
     uint32_t v;
     asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w >> (4 * i)));  // (w & mask) | 128.0
-    const __nv_bfloat162 d =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __nv_bfloat162{__float2bfloat16(136.0f), __float2bfloat16(136.0f)});
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
+                                     __nv_bfloat162{__float2bfloat16(136.0f), __float2bfloat16(136.0f)});
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 
@@ -48,20 +48,31 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
 
+// Shared memory of the split form: the warps' rings, their partial sums, the barriers; then the experts' table.
+// Kernel and launch take it from here.
+template <int kMT>
+struct SplitLayout {
+    static constexpr int kRows = kMT * 16, kRing = kStages / kMT, kBoxBytes = kRows * 128;
+    static constexpr size_t kParts = (size_t)kWarps * kRing * kBoxBytes;                         // offsets
+    static constexpr size_t kShared = kParts + (size_t)kWarps * kRows * (kMaxRows + 1) * 4;
+    static constexpr size_t bytes(int E) { return 1024 + kShared + sizeof(Shared4) + (size_t)E * 12; }
+    static_assert(kShared % 8 == 0 && sizeof(Shared4) % 4 == 0, "alignment");
+};
+
 struct Item {
     int e, row, rows, block;
 };
 
 __device__ __forceinline__ Item item_at(long long t, const int32_t *start, const int32_t *count, const int32_t *pre,
-                                        int E, int blocks) {
+                                        int E, int blocks, int most) {
     Item w;
     w.e = expert_of(t, pre, E, blocks);
     const int in = (int)(t - (long long)pre[w.e] * blocks);
-    const int chunks = (count[w.e] + kMaxRows - 1) / kMaxRows;  // the chunks of one weight block follow each other
+    const int chunks = (count[w.e] + most - 1) / most;  // the chunks of one weight block follow each other
     w.block = in / chunks;
-    const int first = in % chunks * kMaxRows;
+    const int first = in % chunks * most;
     w.row = start[w.e] + first;
-    w.rows = min(kMaxRows, count[w.e] - first);
+    w.rows = min(most, count[w.e] - first);
     return w;
 }
 
@@ -129,12 +140,13 @@ __device__ __forceinline__ void accumulate(const uint32_t *box, const MatmulArgs
 template <int kMT, bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                 const MatmulArgs a) {
-    constexpr int kRows = kMT * 16, kBoxBytes = kRows * 128, kRing = kStages / kMT;
+    using L = SplitLayout<kMT>;
+    constexpr int kRows = L::kRows, kBoxBytes = L::kBoxBytes, kRing = L::kRing;
     constexpr int kChan = kSwiglu ? kRows / 2 : kRows;  // output channels per work item
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    float *parts = reinterpret_cast<float *>(ring + kWarps * kRing * kBoxBytes);  // [warp][kRows][kMaxRows + 1]
-    Shared4 *sh = reinterpret_cast<Shared4 *>(parts + kWarps * kRows * (kMaxRows + 1));
+    float *parts = reinterpret_cast<float *>(ring + L::kParts);  // [warp][kRows][kMaxRows + 1]
+    Shared4 *sh = reinterpret_cast<Shared4 *>(ring + L::kShared);
     const int E = a.g.E;
     int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
     int32_t *count = start + E;
@@ -167,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         }
         if (put_t >= items) return;
         if (lane == 0) {
-            const Item w = item_at(put_t, start, count, pre, E, blocks);
+            const Item w = item_at(put_t, start, count, pre, E, blocks, kMaxRows);
             uint64_t *bar = &sh->full[warp][put % kRing];
             mbar_arrive_expect_tx(bar, kBoxBytes);
             asm volatile(
@@ -183,12 +195,12 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 
     int i = 0;
     for (long long t = blockIdx.x; t < items; t += gridDim.x, ++i) {
-        const Item w = item_at(t, start, count, pre, E, blocks);
+        const Item w = item_at(t, start, count, pre, E, blocks, kMaxRows);
         float acc[kMT][4][4] = {};
         for (int span = (warp + i) % kWarps; ok && span < spans; span += kWarps) {
             const int s = got % kRing;
             const bool in = mbar_wait_bounded(&sh->full[warp][s], (got / kRing) & 1, a.wait_polls);
-            if (!all_of(in)) {
+            if (!__all_sync(0xffffffffu, in)) {
                 ok = false;
                 break;
             }
@@ -236,210 +248,278 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kRing], (got / kRing) & 1);
 }
 
-// ---- many work items: rows shared out among the warps -------------------------
+// ---- many work items: tensor memory ---------------------------------------------
 //
-// A producer warp fills a ring of stages with the weights' boxes (every
-// consumer warp's kMT*16 rows at once) and the expert rows' same span of K; x is then read
-// once per block instead of once per warp, and a consumer keeps whole sums.
-constexpr int kXPitch = kSpan * 2 + 64;  // a row of x in a stage; 64 more bytes spread two rows over all banks
+// One persistent block per SM; a work item is 128 weight rows of an expert and up to 16
+// of its rows.  Sixteen warps turn the words into bf16 pairs and store them
+// to tensor memory, which is where the fifth-generation matrix instruction
+// can take its A operand from: lane = weight row, column = two of K, the very
+// order in which a word gives its pairs, so a thread reads 16-byte pieces of its own
+// row and no dequantised weight touches shared memory.  Each group of K has its own
+// accumulator columns, and four more warps scale them into fp32 sums
+// in registers.  Per 128 of K ("chunk"): four warps fill one of four A buffers, one lane
+// issues eight instructions, and the accumulators go round four buffers with them.
+constexpr int kMaxCols = 16;                 // expert rows per work item: the instruction's N
+constexpr int kChunk = 128;                  // K per A buffer
+constexpr int kBufs = 4;                     // of A and accumulators, used together
+constexpr int kACols = kChunk / 2, kDCols = kChunk / 32 * kMaxCols;  // 32-bit columns: at most four groups a chunk
+constexpr int kTmemStages = 8;
+constexpr int kTileRows = 128;
+constexpr int kWBytes = kTileRows * 128, kXBox = kMaxCols * 128, kStage = kWBytes + kSpan / 64 * kXBox;
+constexpr int kIssuers = 2;                  // warps 1 and 2 issue the instructions, of every other chunk each
+static_assert(kIssuers == 2 && kBufs % kIssuers == 0, "an issuer takes one half of every stage");
+constexpr int kFirstDequant = 4, kFirstEpilogue = 20, kTmemThreads = 24 * 32;  // warp 0: loads
+static_assert(kBufs * (kACols + kDCols) <= 512, "tensor memory");
 
-template <int kW, int kMT, int kNT, bool kSwiglu, int kPer>
-__device__ __forceinline__ void stage_sums(const uint8_t *weights, const uint8_t *x, int words, const float *scale,
-                                           float (&acc)[kMT][4][4]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    constexpr int kChan = kW * kMT * (kSwiglu ? 8 : 16);
-#pragma unroll
-    for (int j0 = 0; j0 < 8; j0 += kPer) {
-        if (j0 >= words) break;
-        float part[kMT][kNT][4] = {};
-#pragma unroll
-        for (int j = j0; j < j0 + kPer; ++j) {
-            uint4 b[kNT];
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-                b[n] = *reinterpret_cast<const uint4 *>(x + (n * 8 + g) * kXPitch + j * 64 + t * 16);
-#pragma unroll
-            for (int m = 0; m < kMT; ++m) {
-                const int low = kSwiglu ? (warp * kMT + m) * 8 : (warp * kMT + m) * 16;
-                const int high = kSwiglu ? kChan + low : low + 8;
-                const uint32_t at = (j ^ g) * 16 + t * 4 + g * 128;
-                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(weights + low * 128 + at);
-                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(weights + high * 128 + at);
-                const uint32_t p0 = pair_of(w0, 0), p1 = pair_of(w0, 1), p2 = pair_of(w0, 2), p3 = pair_of(w0, 3);
-                const uint32_t q0 = pair_of(w1, 0), q1 = pair_of(w1, 1), q2 = pair_of(w1, 2), q3 = pair_of(w1, 3);
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                    mma16816(part[m][n], p0, q0, p1, q1, b[n].x, b[n].y);
-                    mma16816(part[m][n], p2, q2, p3, q3, b[n].z, b[n].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < kMT; ++m) {
-            const float s0 = scale[(j0 / kPer * kMT + m) * 2], s1 = scale[(j0 / kPer * kMT + m) * 2 + 1];
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                acc[m][n][0] = fmaf(s0, part[m][n][0], acc[m][n][0]);
-                acc[m][n][1] = fmaf(s0, part[m][n][1], acc[m][n][1]);
-                acc[m][n][2] = fmaf(s1, part[m][n][2], acc[m][n][2]);
-                acc[m][n][3] = fmaf(s1, part[m][n][3], acc[m][n][3]);
-            }
+struct SharedTmem {
+    uint64_t full[kTmemStages], empty[kTmemStages];
+    // ready: A is filled and the accumulators of four chunks ago are read; done: the instructions have ended
+    uint64_t ready[kBufs], done[kBufs], drain;
+    uint32_t tmem, abort;
+    int32_t warp_sum[kTmemThreads / 32];
+};
+constexpr size_t kTmemShared = (size_t)kTmemStages * kStage;  // offset behind the stages
+constexpr size_t tmem_smem_bytes(int E) { return 1024 + kTmemShared + sizeof(SharedTmem) + (size_t)E * 12; }
+
+// A position in a ring of n buffers and the parity of its current round.
+struct Ring {
+    int i = 0;
+    uint32_t parity;
+    __device__ explicit Ring(uint32_t p) : parity(p) {}
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            parity ^= 1;
         }
     }
-}
-
-struct SharedRows {
-    uint64_t full[4], empty[4];
-    uint32_t abort;
-    int32_t warp_sum[32];
 };
 
-// kPer: 32-wide steps per group of K.
-template <int kW, int kMT, bool kSwiglu, int kPer, int kRing>
-__global__ void __launch_bounds__((kW + 1) * 32, 2)
-    expert_w4_rows_kernel(const __grid_constant__ CUtensorMap map_w, const MatmulArgs a) {
-    constexpr int kRows = kW * kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows, kBlock = (kW + 1) * 32;
-    constexpr int kWBytes = kRows * 128, kStage = kWBytes + (kMaxRows * kXPitch + 1023) / 1024 * 1024;
+// Eight weights of a word as four bf16 pairs, k ascending.
+__device__ __forceinline__ void unpack_word(uint32_t w, uint32_t *p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pair_of(w, i);
+}
+
+// kPer: groups of a chunk.
+template <bool kSwiglu, int kPer>
+__global__ void __launch_bounds__(kTmemThreads, 1)
+    expert_w4_tmem_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                          const MatmulArgs a) {
+    constexpr int kChan = kSwiglu ? kTileRows / 2 : kTileRows;  // output channels per item
     extern __shared__ uint8_t raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    SharedRows *sh = reinterpret_cast<SharedRows *>(ring + kRing * kStage);
+    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    SharedTmem *sh = reinterpret_cast<SharedTmem *>(stages + kTmemShared);
     const int E = a.g.E;
     int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
     int32_t *count = start + E;
     int32_t *pre = count + E;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), quad = warp & 3;
     if (tid == 0) {
-        for (int s = 0; s < kRing; ++s) {
+        for (int s = 0; s < kTmemStages; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->empty[s], kW);
+            mbar_init(&sh->empty[s], 8 + kIssuers);  // the warps that read its words, the instructions that read its rows
         }
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&sh->ready[i], 8);  // four warps fill, four warps read
+            mbar_init(&sh->done[i], 1);
+        }
+        mbar_init(&sh->drain, kIssuers);
         sh->abort = 0;
         fence_mbar_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x));
     }
+    if (warp == 1) tmem_alloc_all(&sh->tmem);
     grid_dependency_wait();
-    const int total = place_experts<kBlock>(a, kMaxRows, start, count, pre, sh->warp_sum);  // ends in a barrier
+    tmem_fence_before();
+    const int total = place_experts<kTmemThreads>(a, kMaxCols, start, count, pre, sh->warp_sum);  // ends in a barrier
+    tmem_fence_after();
+    const uint32_t tmem = sh->tmem, d0 = tmem + kBufs * kACols;
     const int blocks = (a.N + kChan - 1) / kChan;
     const long long items = (long long)total * blocks;
     const int spans = (a.K + kSpan - 1) / kSpan;
+    // chunks of this block, all items; a span has two (what lies past K is zero in x)
+    const long long chunks = (long long)blockIdx.x < items ? ((items - 1 - blockIdx.x) / gridDim.x + 1) * spans * 2 : 0;
+    const long long polls = a.wait_polls;
 
-    if (warp == kW) {
-        int s = 0;
-        uint32_t round = 0;
+    if (warp == 0) {
+        Ring s(1);
+        uint32_t fills = 0;
         bool ok = true;
         for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
-            const Item w = item_at(t, start, count, pre, E, blocks);
-            const uint8_t *x = a.x + (size_t)(w.row + lane) * a.x_pitch;
+            const Item w = item_at(t, start, count, pre, E, blocks, kMaxCols);
+            const int row = __shfl_sync(0xffffffffu, w.row, 0), e = __shfl_sync(0xffffffffu, w.e, 0),
+                      block = __shfl_sync(0xffffffffu, w.block, 0);
             for (int span = 0; span < spans; ++span) {
-                if (round > 0) {
-                    const bool in = wait_or_abort(&sh->empty[s], (round - 1) & 1, a.wait_polls, &sh->abort, a.status);
-                    if (!all_of(in)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                uint8_t *stage = ring + s * kStage;
-                const uint32_t bytes = min(kSpan, a.K - span * kSpan) * 2;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh->full[s], kWBytes + w.rows * bytes);
+                ok = all_of(wait_or_abort(&sh->empty[s.i], s.parity, polls, &sh->abort, a.status));
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t at = smem_u32(stages) + s.i * kStage;
+                    uint64_t *bar = &sh->full[s.i];
+                    mbar_arrive_expect_tx(bar, kStage);
                     asm volatile(
-                        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-                        "%3, %4, %5}], [%6];" ::"r"(smem_u32(stage)),
-                        "l"(&map_w), "r"(span * (kSpan / 8)), "r"(w.block * kChan), "r"(0), "r"(w.e),
-                        "r"(smem_u32(&sh->full[s]))
+                        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                        "%3, %3, %4, %5}], [%6];" ::"r"(at),
+                        "l"(&map_w), "r"(span * (kSpan / 8)), "r"(0), "r"(block * (kChan / 8)), "r"(e),
+                        "r"(smem_u32(bar))
                         : "memory");
+#pragma unroll
+                    for (int i = 0; i < kSpan / 64; ++i)
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+                            "{%2, %3}], [%4];" ::"r"(at + kWBytes + i * kXBox),
+                            "l"(&map_x), "r"(span * kSpan + i * 64), "r"(row), "r"(smem_u32(bar))
+                            : "memory");
                 }
                 __syncwarp();
-                if (lane < w.rows)
-                    bulk_load(stage + kWBytes + lane * kXPitch, x + (size_t)span * kSpan * 2, bytes, &sh->full[s]);
-                if (++s == kRing) {
-                    s = 0;
-                    ++round;
-                }
+                s.next(kTmemStages);
+                ++fills;
             }
         }
-        if (lane == 0)  // every load that was issued lands before the block ends, also if the others gave up
-            for (int i = 0; i < kRing; ++i) {
-                const uint32_t fills = round + (i < s ? 1 : 0);
-                if (fills > 0) mbar_wait_bounded(&sh->full[i], (fills - 1) & 1);
+        // every load that was issued lands before the block ends, also if other warps gave up
+        for (int i = 0; i < kTmemStages && fills > 0; ++i, --fills) {
+            if (--s.i < 0) {
+                s.i = kTmemStages - 1;
+                s.parity ^= 1;
             }
-    } else {
-        constexpr int kGroups = 8 / kPer;  // groups of a stage
-        const int g = lane >> 2, q = lane & 3;
+            mbar_wait_bounded(&sh->full[s.i], s.parity ^ 1);
+        }
+    } else if (warp <= kIssuers) {
+        // One lane's issue of a chunk takes some 500 cycles from barrier to barrier, longer than its share of
+        // the weights takes to arrive: two warps take every other chunk, a half of a stage each.
+        constexpr uint32_t kIdesc =
+            1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kMaxCols >> 3) << 17 | (uint32_t)(kTileRows >> 4) << 24;
+        const int half = warp - 1;
+        Ring s(0), buf(0);
+        buf.i = half;
+        for (long long c = half; c < chunks; c += kIssuers) {
+            // (that the rows of x are there follows: the warps that filled A waited for the stage)
+            if (!all_of(wait_or_abort(&sh->ready[buf.i], buf.parity, polls, &sh->abort, a.status))) break;
+            tmem_fence_after();
+            if (elect_one()) {
+                const uint32_t rows = smem_u32(stages) + s.i * kStage + kWBytes + half * 2 * kXBox;
+                const uint32_t d = d0 + buf.i * kDCols, at = tmem + buf.i * kACols;
+#pragma unroll
+                for (int j = 0; j < kChunk / 16; ++j)
+                    mma_tmem(d + j / (8 / kPer) * kMaxCols, at + j * 8, operand_desc(rows + j / 4 * kXBox) + j % 4 * 2,
+                             kIdesc, j % (8 / kPer) != 0);
+                mma_commit_one(&sh->done[buf.i]);
+                mma_commit_one(&sh->empty[s.i]);
+            }
+            __syncwarp();
+            buf.next(kBufs);
+            buf.next(kBufs);
+            s.next(kTmemStages);
+        }
+        // the instructions that were issued end before tensor memory is freed
+        if (elect_one()) mma_commit_one(&sh->drain);
+        mbar_wait_bounded(&sh->drain, 0);
+    } else if (warp >= kFirstEpilogue) {
         const int groups = a.K / a.group;
-        int s = 0;
-        uint32_t round = 0;
+        const bool up = kSwiglu && (lane & 8);
+        Ring buf(0);
         bool ok = true;
+        if (lane == 0)
+            for (int i = 0; i < kBufs; ++i) mbar_arrive(&sh->ready[i]);  // nothing to read in the first round
         for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
-            const Item w = item_at(t, start, count, pre, E, blocks);
-            const uint16_t *from[kMT][2];
+            const Item w = item_at(t, start, count, pre, E, blocks, kMaxCols);
+            // swiglu: lanes 0-7 gate of channels 0-7, 8-15 their up, 16-23 gate of channels 8-15, ...
+            const int chan =
+                w.block * kChan + (kSwiglu ? quad * 16 + (lane >> 4) * 8 + (lane & 7) : quad * 32 + lane);
+            const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + min(chan, a.N - 1);
+            const uint16_t *from = static_cast<const uint16_t *>(a.w_scale) + row * groups;
+            float acc[kMaxCols] = {};
+            uint16_t next[kPer];
 #pragma unroll
-            for (int m = 0; m < kMT; ++m)
+            for (int i = 0; i < kPer; ++i) next[i] = i < groups ? __ldg(from + i) : 0;
+            for (int c = 0; c < spans * 2; ++c) {
+                float scale[kPer];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int chan = w.block * kChan + (kSwiglu ? (warp * kMT + m) * 8 : (warp * kMT + m) * 16 + h * 8) + g;
-                    const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (kSwiglu && h ? a.N : 0) + min(chan, a.N - 1);
-                    from[m][h] = static_cast<const uint16_t *>(a.w_scale) + row * groups;
+                for (int i = 0; i < kPer; ++i) {  // the next chunk's scales while this one's sums are waited for
+                    scale[i] = __uint_as_float((uint32_t)next[i] << 16);
+                    const int g = (c + 1) * kPer + i;
+                    next[i] = g < groups ? __ldg(from + g) : 0;
                 }
-            // the scales of a stage, one stage ahead
-            uint16_t next[kGroups * kMT * 2];
-            auto fetch = [&](int span) {
+                ok = all_of(wait_or_abort(&sh->done[buf.i], buf.parity, polls, &sh->abort, a.status));
+                if (!ok) break;
+                tmem_fence_after();
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i)
+                for (int i = 0; i < kPer; ++i) {
+                    float v[kMaxCols];
+                    tmem_ld16(d0 + ((uint32_t)(quad * 32) << 16) + buf.i * kDCols + i * kMaxCols, v);
+                    if (i == kPer - 1) {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh->ready[buf.i]);
+                    }
 #pragma unroll
-                    for (int m = 0; m < kMT; ++m)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int at = min(span * kGroups + i, groups - 1);
-                            next[(i * kMT + m) * 2 + h] = __ldg(from[m][h] + at);
-                        }
-            };
-            fetch(0);
-            float acc[kMT][4][4] = {};
-            for (int span = 0; span < spans; ++span) {
-                float scale[kGroups * kMT * 2];
-#pragma unroll
-                for (int i = 0; i < kGroups * kMT * 2; ++i) scale[i] = __uint_as_float((uint32_t)next[i] << 16);
-                fetch(min(span + 1, spans - 1));
-                const bool in = wait_or_abort(&sh->full[s], round & 1, a.wait_polls, &sh->abort, a.status);
-                if (!all_of(in)) {
-                    ok = false;
-                    break;
+                    for (int n = 0; n < kMaxCols; ++n) acc[n] = fmaf(scale[i], v[n], acc[n]);
                 }
-                const uint8_t *stage = ring + s * kStage;
-                const int words = min(kSpan, a.K - span * kSpan) / 32;
-                if (w.rows <= 8) stage_sums<kW, kMT, 1, kSwiglu, kPer>(stage, stage + kWBytes, words, scale, acc);
-                else if (w.rows <= 16) stage_sums<kW, kMT, 2, kSwiglu, kPer>(stage, stage + kWBytes, words, scale, acc);
-                else stage_sums<kW, kMT, 4, kSwiglu, kPer>(stage, stage + kWBytes, words, scale, acc);
-                __syncwarp();  // every lane has read the stage
-                if (lane == 0) mbar_arrive(&sh->empty[s]);
-                if (++s == kRing) {
-                    s = 0;
-                    ++round;
-                }
+                buf.next(kBufs);
             }
             if (!ok) break;
+            uint16_t *y = a.y + (size_t)w.row * a.N + chan;
+            if (kSwiglu) {
+                // of rows n, n+1 the gate lane finishes the first, the up lane the second
 #pragma unroll
-            for (int m = 0; m < kMT; ++m)
+                for (int n = 0; n < kMaxCols; n += 2) {
+                    const float other = __shfl_xor_sync(0xffffffffu, up ? acc[n] : acc[n + 1], 8);
+                    const float g = up ? other : acc[n], u = up ? acc[n + 1] : other;
+                    const int r = n + (up ? 1 : 0);
+                    const float out = __fdividef(g, 1.0f + __expf(-g)) * u;
+                    if (chan < a.N && r < w.rows)
+                        y[(size_t)r * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
+                }
+            } else if (chan < a.N) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int r = n * 8 + q * 2 + c;
-                        const int chan = w.block * kChan + (warp * kMT + m) * (kSwiglu ? 8 : 16) + g;
-                        if (r >= w.rows) continue;
-                        uint16_t *y = a.y + (size_t)(w.row + r) * a.N + chan;
-                        const float lo = acc[m][n][c], hi = acc[m][n][c + 2];
-                        if (kSwiglu) {
-                            if (chan < a.N)
-                                y[0] = __bfloat16_as_ushort(
-                                    __float2bfloat16_rn(__fdividef(lo, 1.0f + __expf(-lo)) * hi));
-                        } else {
-                            if (chan < a.N) y[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-                            if (chan + 8 < a.N) y[8] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-                        }
-                    }
+                for (int n = 0; n < kMaxCols; ++n)
+                    if (n < w.rows) y[(size_t)n * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[n]));
+            }
         }
+    } else if (warp >= kFirstDequant) {
+        // this warp's lanes: weight rows quad*32 + lane; its chunks: every fourth, always the same A buffer
+        const int mine = (warp - kFirstDequant) >> 2, row = quad * 32 + lane;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + mine * kACols;
+        Ring s(0);
+        s.i = mine >> 1;
+        uint32_t done_parity = 1;
+        for (long long c = mine; c < chunks; c += kBufs) {
+            if (!all_of(wait_or_abort(&sh->full[s.i], s.parity, polls, &sh->abort, a.status)) ||
+                !all_of(wait_or_abort(&sh->done[mine], done_parity, polls, &sh->abort, a.status)))
+                break;
+            tmem_fence_after();
+            const uint8_t *words = stages + s.i * kStage + row * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 64 of K: 32 columns
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at = (mine & 1) * 4 + h * 2 + i;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(words + ((at ^ (row & 7)) << 4));
+                    unpack_word(v.x, p + i * 16);
+                    unpack_word(v.y, p + i * 16 + 4);
+                    unpack_word(v.z, p + i * 16 + 8);
+                    unpack_word(v.w, p + i * 16 + 12);
+                }
+                tmem_st32(to + h * 32, p);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->empty[s.i]);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->ready[mine]);
+            done_parity ^= 1;
+            s.next(kTmemStages);  // four chunks on: two stages
+            s.next(kTmemStages);
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tmem_fence_after();
+        tmem_free_all(tmem);
     }
 }
 
@@ -452,28 +532,34 @@ cudaError_t map_words(CUtensorMap *m, const MatmulArgs &a, bool swiglu, int chan
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, a.w, dims, strides, box) ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int kW, int kMT, bool kSwiglu, int kPer, int kRing>
-cudaError_t launch_w4_rows(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
-    constexpr int kRows = kW * kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows;
-    constexpr int kStage = kRows * 128 + (kMaxRows * kXPitch + 1023) / 1024 * 1024;
-    CUtensorMap m;
-    cudaError_t e = map_words(&m, a, kSwiglu, kChan);
-    if (e != cudaSuccess) return e;
-    const auto kernel = expert_w4_rows_kernel<kW, kMT, kSwiglu, kPer, kRing>;
-    const size_t smem = 1024 + (size_t)kRing * kStage + sizeof(SharedRows) + (size_t)a.g.E * 3 * 4;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <bool kSwiglu, int kPer>
+cudaError_t launch_w4_tmem(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    constexpr int kChan = kSwiglu ? kTileRows / 2 : kTileRows;
+    const cuuint64_t halves = kSwiglu ? 2 : 1, row = (cuuint64_t)a.K / 2, N = a.N;
+    CUtensorMap mw, mx;
+    // w as [E][N/8][gate, up][8][K/8]
+    const cuuint64_t wd[5] = {(cuuint64_t)a.K / 8, 8, halves, N / 8, (cuuint64_t)a.g.E};
+    const cuuint64_t wst[4] = {row, N * row, 8 * row, halves * N * row};
+    const cuuint32_t wb[5] = {kSpan / 8, 8, (cuuint32_t)halves, kChan / 8, 1};
+    const cuuint64_t xd[2] = {(cuuint64_t)a.K, (cuuint64_t)a.arena_rows}, xst[1] = {(cuuint64_t)a.x_pitch};
+    const cuuint32_t xb[2] = {64, kMaxCols};
+    if (!encode_map(&mw, CU_TENSOR_MAP_DATA_TYPE_INT32, 5, a.w, wd, wst, wb) ||
+        !encode_map(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, xd, xst, xb))
+        return cudaErrorInvalidValue;
+    const auto kernel = expert_w4_tmem_kernel<kSwiglu, kPer>;
+    const size_t smem = tmem_smem_bytes(a.g.E);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.g.R * a.g.T * a.g.k;
-    const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxRows) * ((a.N + kChan - 1) / kChan);
-    const int grid = (int)(most < 2 * p.num_sms ? most : 2 * p.num_sms);
-    return launch_pdl(kernel, grid, (kW + 1) * 32, smem, s, m, a);
+    const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxCols) * ((a.N + kChan - 1) / kChan);
+    return launch_pdl(kernel, (int)(most < p.num_sms ? most : p.num_sms), kTmemThreads, smem, s, mw, mx, a);
 }
 
-template <int kW, int kMT, bool kSwiglu, int kRing>
-cudaError_t launch_w4_group(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
-    return a.group == 32   ? launch_w4_rows<kW, kMT, kSwiglu, 1, kRing>(p, a, s)
-           : a.group == 64 ? launch_w4_rows<kW, kMT, kSwiglu, 2, kRing>(p, a, s)
-                           : launch_w4_rows<kW, kMT, kSwiglu, 4, kRing>(p, a, s);
+template <bool kSwiglu>
+cudaError_t launch_w4_groups(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    return a.group == 32   ? launch_w4_tmem<kSwiglu, 4>(p, a, s)
+           : a.group == 64 ? launch_w4_tmem<kSwiglu, 2>(p, a, s)
+                           : launch_w4_tmem<kSwiglu, 1>(p, a, s);
 }
 
 template <int kMT, bool kSwiglu>
@@ -482,8 +568,7 @@ cudaError_t launch_w4(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s)
     CUtensorMap m;
     cudaError_t e = map_words(&m, a, kSwiglu, kChan);
     if (e != cudaSuccess) return e;
-    const size_t smem = 1024 + (size_t)kWarps * (kStages / kMT) * kRows * 128 + (size_t)kWarps * kRows * (kMaxRows + 1) * 4 +
-                        sizeof(Shared4) + (size_t)a.g.E * 3 * 4;
+    const size_t smem = SplitLayout<kMT>::bytes(a.g.E);
     e = cudaFuncSetAttribute(expert_w4_kernel<kMT, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
@@ -498,7 +583,7 @@ cudaError_t launch_w4(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s)
 cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s) {
     const long long rows = (long long)a.g.R * a.g.T * a.g.k, experts = rows < a.g.E ? rows : a.g.E;
     const bool wide = experts * (swiglu ? 2 : 1) * a.N / 128 >= 2 * p.num_sms;
-    if (wide) return swiglu ? launch_w4_group<8, 1, true, 3>(p, a, s) : launch_w4_group<8, 1, false, 3>(p, a, s);
+    if (wide) return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
     return swiglu ? launch_w4<1, true>(p, a, s) : launch_w4<1, false>(p, a, s);
 }
 

@@ -270,6 +270,20 @@ def test_w4_many_items():
     run_product("int4", counts, 512, 2056, False, group=32)["plan"].close()
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("group,K,N", [(32, 32, 2568), (32, 160, 2568), (64, 64, 2560), (64, 832, 2600), (128, 128, 2560),
+                                       (128, 1152, 2568)])
+def test_w4_many_items_of_every_group(group, K, N, swiglu):
+    counts = np.random.default_rng(group + K).integers(0, 4, (2, 64))
+    counts[0, 3], counts[1, 5], counts[0, 6] = 45, 17, 16  # more rows than a work item, one more, as many
+    run_product("int4", counts, K, N, swiglu, group=group, seed=K)["plan"].close()
+
+
+def test_w4_many_items_in_fixed_windows():
+    counts = np.random.default_rng(8).integers(0, 4, (4, 64))
+    run_product("int4", counts, 256, 2568, True, group=64, window_rows=70)["plan"].close()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "int4"])
 def test_all_experts_empty_and_most_experts(kind):
     r = run_product(kind, np.zeros((4, 16), int), 64, 64, False)
@@ -496,5 +510,23 @@ def test_waits_that_run_out_set_the_status(kind):
     assert plan.read_status() == 0
     for e, a, b in r["segs"]:
         ref, tol = product_ref(kind, r["x64"][a:b], r["w64"][e], None, True, 1024)
+        within(r["y"][a:b], ref, tol)
+    plan.close()
+
+
+@pytest.mark.parametrize("polls", [0, 1, 3])
+def test_waits_that_run_out_with_many_items(polls):
+    counts = np.random.default_rng(3).integers(0, 4, (2, 64))
+    r = run_product("int4", counts, 512, 2568, True, group=128)
+    plan = r["plan"]
+    plan.set_wait_limit(polls)
+    r["call"]()
+    assert plan.read_status(clear=True) in ((A.DEV_WAIT_TIMEOUT,) if polls == 0 else (0, A.DEV_WAIT_TIMEOUT))
+    plan.set_wait_limit(-1)
+    r["y"].fill_(CANARY)
+    r["call"]()
+    assert plan.read_status() == 0
+    for e, a, b in r["segs"]:
+        ref, tol = product_ref("int4", r["x64"][a:b], r["w64"][e], None, True, 512)
         within(r["y"][a:b], ref, tol)
     plan.close()
