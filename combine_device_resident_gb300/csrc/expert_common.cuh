@@ -133,7 +133,7 @@ __device__ __forceinline__ void mma_commit_one(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-// 16 columns of this warp's 32 lanes into registers, and 32 columns out of them.
+// 16 columns of this warp's 32 lanes into registers; eight columns of one value, and 32 columns, out of them.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
@@ -145,6 +145,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, uint32_t r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%1], {%0,%0,%0,%0,%0,%0,%0,%0};" ::"r"(r), "r"(addr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile(

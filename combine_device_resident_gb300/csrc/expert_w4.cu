@@ -30,10 +30,16 @@ struct Shared4 {
     int32_t warp_sum[kWarps];
 };
 
-// Bits i*4 and 16+i*4 of a word: k = 2i and 2i+1 as bf16, minus 8.
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
+// Bits i*4 and 16+i*4 of a word: 128 + q of k = 2i and 2i+1 as bf16.
+__device__ __forceinline__ uint32_t raw_pair(uint32_t w, int i) {
     uint32_t v;
     asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w >> (4 * i)));  // (w & mask) | 128.0
+    return v;
+}
+
+// The same minus 136: q - 8.
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
+    const uint32_t v = raw_pair(w, i);
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
                                      __nv_bfloat162{__float2bfloat16(136.0f), __float2bfloat16(136.0f)});
     return *reinterpret_cast<const uint32_t *>(&d);
@@ -251,79 +257,101 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 // ---- many work items: tensor memory ---------------------------------------------
 //
 // One persistent block per SM; a work item is 128 weight rows of an expert and up to 16
-// of its rows.  Sixteen warps turn the words into bf16 pairs and store them
-// to tensor memory, which is where the fifth-generation matrix instruction
-// can take its A operand from: lane = weight row, column = two of K, the very
+// of its rows.  Most warps turn the words into bf16 pairs and store them to
+// tensor memory, which is where the fifth-generation matrix instruction can
+// take its A operand from: lane = weight row, column = two of K, the very
 // order in which a word gives its pairs, so a thread reads 16-byte pieces of its own
-// row and no dequantised weight touches shared memory.  Each group of K has its own
-// accumulator columns, and four more warps scale them into fp32 sums
-// in registers.  Per 128 of K ("chunk"): four warps fill one of four A buffers, one lane
-// issues eight instructions, and the accumulators go round four buffers with them.
+// row and no unpacked weight touches shared memory.  (At N = 16 the instruction then takes 10
+// cycles, against 40 with A in shared memory.)  The pairs are 128 + q; a second
+// instruction with a constant A of -136 takes the 128 and the 8 off inside the
+// accumulator, exact products in fp32 sums.  Each group of K has its own
+// accumulator columns, and four warps scale them into fp32 sums in registers.
+//
+// The steps are short and the way round a buffer is long (barriers and latencies: some
+// 2000 cycles for a span of 256 of K, whose weights take 700 to arrive), so
+// each buffer has its own eight unpacking warps and its own issuing warp,
+// and there are as many buffers as tensor memory holds.  (A barrier's
+// parity tells a waiter only that the last phase is over: whoever waits for
+// a buffer has to see every phase of it.)
 constexpr int kMaxCols = 16;                 // expert rows per work item: the instruction's N
-constexpr int kChunk = 128;                  // K per A buffer
-constexpr int kBufs = 4;                     // of A and accumulators, used together
-constexpr int kACols = kChunk / 2, kDCols = kChunk / 32 * kMaxCols;  // 32-bit columns: at most four groups a chunk
-constexpr int kTmemStages = 8;
+constexpr int kACols = kSpan / 2, kZeroCols = 8;  // 32-bit columns of a span's A, and of the constant one
 constexpr int kTileRows = 128;
 constexpr int kWBytes = kTileRows * 128, kXBox = kMaxCols * 128, kStage = kWBytes + kSpan / 64 * kXBox;
-constexpr int kIssuers = 2;                  // warps 1 and 2 issue the instructions, of every other chunk each
-static_assert(kIssuers == 2 && kBufs % kIssuers == 0, "an issuer takes one half of every stage");
-constexpr int kFirstDequant = 4, kFirstEpilogue = 20, kTmemThreads = 24 * 32;  // warp 0: loads
-static_assert(kBufs * (kACols + kDCols) <= 512, "tensor memory");
+constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16, twice
+
+// For kPer groups of K per 128.
+template <int kPer>
+struct TmemForm {
+    static constexpr int kGroups = 2 * kPer, kDCols = kGroups * kMaxCols;  // of a span
+    static constexpr int kBufs = kPer == 1 ? 3 : 2, kStages = kPer == 1 ? 6 : 8;
+    static constexpr bool kSubtract = kPer == 4;  // no columns left for the constant A: q - 8 is unpacked
+    static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 8 * kBufs;  // warp 0 loads, 1 .. kBufs issue
+    static constexpr int kThreads = (kFirstSum + 4) * 32;
+    static constexpr int kZeroAt = kBufs * (kACols + kDCols);  // column
+    static_assert(kZeroAt + (kSubtract ? 0 : kZeroCols) <= 512, "tensor memory");
+    static_assert(kStages % kBufs == 0, "every waiter sees every phase of its stages");
+};
+constexpr int kMaxStages = 8, kMaxBufs = 3;
 
 struct SharedTmem {
-    uint64_t full[kTmemStages], empty[kTmemStages];
-    // ready: A is filled and the accumulators of four chunks ago are read; done: the instructions have ended
-    uint64_t ready[kBufs], done[kBufs], drain;
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    // ready: A is filled and the accumulators of a round ago are read; done: the instructions have ended
+    uint64_t ready[kMaxBufs], done[kMaxBufs], drain;
     uint32_t tmem, abort;
-    int32_t warp_sum[kTmemThreads / 32];
+    int32_t warp_sum[32];
 };
-constexpr size_t kTmemShared = (size_t)kTmemStages * kStage;  // offset behind the stages
-constexpr size_t tmem_smem_bytes(int E) { return 1024 + kTmemShared + sizeof(SharedTmem) + (size_t)E * 12; }
+constexpr size_t tmem_shared(int stages) { return (size_t)stages * kStage; }  // offset behind the stages
+constexpr size_t tmem_smem_bytes(int stages, int E) {
+    return 1024 + tmem_shared(stages) + sizeof(SharedTmem) + (size_t)E * 12;
+}
+static_assert(kStage % 1024 == 0 && tmem_smem_bytes(kMaxStages, kMaxExperts) <= 232448, "shared memory");
 
 // A position in a ring of n buffers and the parity of its current round.
 struct Ring {
     int i = 0;
     uint32_t parity;
     __device__ explicit Ring(uint32_t p) : parity(p) {}
-    __device__ __forceinline__ void next(int n) {
-        if (++i == n) {
-            i = 0;
+    __device__ __forceinline__ void next(int n, int steps = 1) {
+        i += steps;
+        if (i >= n) {
+            i -= n;
             parity ^= 1;
         }
     }
 };
 
 // Eight weights of a word as four bf16 pairs, k ascending.
+template <bool kSubtract>
 __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pair_of(w, i);
+    for (int i = 0; i < 4; ++i) p[i] = kSubtract ? pair_of(w, i) : raw_pair(w, i);
 }
 
-// kPer: groups of a chunk.
 template <bool kSwiglu, int kPer>
-__global__ void __launch_bounds__(kTmemThreads, 1)
+__global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
     expert_w4_tmem_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                           const MatmulArgs a) {
+    using F = TmemForm<kPer>;
     constexpr int kChan = kSwiglu ? kTileRows / 2 : kTileRows;  // output channels per item
+    constexpr int kBufs = F::kBufs, kDCols = F::kDCols, kGroups = F::kGroups;
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    SharedTmem *sh = reinterpret_cast<SharedTmem *>(stages + kTmemShared);
+    SharedTmem *sh = reinterpret_cast<SharedTmem *>(stages + tmem_shared(F::kStages));
     const int E = a.g.E;
     int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
     int32_t *count = start + E;
     int32_t *pre = count + E;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), quad = warp & 3;
     if (tid == 0) {
-        for (int s = 0; s < kTmemStages; ++s) {
+        for (int s = 0; s < F::kStages; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->empty[s], 8 + kIssuers);  // the warps that read its words, the instructions that read its rows
+            mbar_init(&sh->empty[s], 9);  // the eight warps that read its words, and the instructions that read its rows
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&sh->ready[i], 8);  // four warps fill, four warps read
+            mbar_init(&sh->ready[i], 12);  // eight warps fill, four read
             mbar_init(&sh->done[i], 1);
         }
-        mbar_init(&sh->drain, kIssuers);
+        mbar_init(&sh->drain, kBufs);
         sh->abort = 0;
         fence_mbar_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
@@ -332,14 +360,14 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
     if (warp == 1) tmem_alloc_all(&sh->tmem);
     grid_dependency_wait();
     tmem_fence_before();
-    const int total = place_experts<kTmemThreads>(a, kMaxCols, start, count, pre, sh->warp_sum);  // ends in a barrier
+    const int total = place_experts<F::kThreads>(a, kMaxCols, start, count, pre, sh->warp_sum);  // ends in a barrier
     tmem_fence_after();
-    const uint32_t tmem = sh->tmem, d0 = tmem + kBufs * kACols;
+    const uint32_t tmem = sh->tmem, d0 = tmem + kBufs * kACols, zero = tmem + F::kZeroAt;
     const int blocks = (a.N + kChan - 1) / kChan;
     const long long items = (long long)total * blocks;
     const int spans = (a.K + kSpan - 1) / kSpan;
-    // chunks of this block, all items; a span has two (what lies past K is zero in x)
-    const long long chunks = (long long)blockIdx.x < items ? ((items - 1 - blockIdx.x) / gridDim.x + 1) * spans * 2 : 0;
+    // spans of this block, all items (what lies past K is zero in x)
+    const long long mine = (long long)blockIdx.x < items ? ((items - 1 - blockIdx.x) / gridDim.x + 1) * spans : 0;
     const long long polls = a.wait_polls;
 
     if (warp == 0) {
@@ -372,53 +400,61 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
                             : "memory");
                 }
                 __syncwarp();
-                s.next(kTmemStages);
+                s.next(F::kStages);
                 ++fills;
             }
         }
         // every load that was issued lands before the block ends, also if other warps gave up
-        for (int i = 0; i < kTmemStages && fills > 0; ++i, --fills) {
+        for (int i = 0; i < F::kStages && fills > 0; ++i, --fills) {
             if (--s.i < 0) {
-                s.i = kTmemStages - 1;
+                s.i = F::kStages - 1;
                 s.parity ^= 1;
             }
             mbar_wait_bounded(&sh->full[s.i], s.parity ^ 1);
         }
-    } else if (warp <= kIssuers) {
-        // One lane's issue of a chunk takes some 500 cycles from barrier to barrier, longer than its share of
-        // the weights takes to arrive: two warps take every other chunk, a half of a stage each.
+    } else if (warp <= kBufs) {
         constexpr uint32_t kIdesc =
             1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kMaxCols >> 3) << 17 | (uint32_t)(kTileRows >> 4) << 24;
-        const int half = warp - 1;
-        Ring s(0), buf(0);
-        buf.i = half;
-        for (long long c = half; c < chunks; c += kIssuers) {
+        constexpr int kSteps = kSpan / 16, kPerGroup = kSteps / kGroups;
+        const int b = warp - 1;
+        const uint32_t at = tmem + b * kACols, d = d0 + b * kDCols;
+        Ring s(0);
+        s.i = b;
+        uint32_t parity = 0;
+        for (long long c = b; c < mine; c += kBufs) {
             // (that the rows of x are there follows: the warps that filled A waited for the stage)
-            if (!all_of(wait_or_abort(&sh->ready[buf.i], buf.parity, polls, &sh->abort, a.status))) break;
+            if (!all_of(wait_or_abort(&sh->ready[b], parity, polls, &sh->abort, a.status))) break;
             tmem_fence_after();
             if (elect_one()) {
-                const uint32_t rows = smem_u32(stages) + s.i * kStage + kWBytes + half * 2 * kXBox;
-                const uint32_t d = d0 + buf.i * kDCols, at = tmem + buf.i * kACols;
+                const uint32_t rows = smem_u32(stages) + s.i * kStage + kWBytes;
 #pragma unroll
-                for (int j = 0; j < kChunk / 16; ++j)
-                    mma_tmem(d + j / (8 / kPer) * kMaxCols, at + j * 8, operand_desc(rows + j / 4 * kXBox) + j % 4 * 2,
-                             kIdesc, j % (8 / kPer) != 0);
-                mma_commit_one(&sh->done[buf.i]);
+                for (int j = 0; j < kSteps; ++j) {
+                    const uint64_t bd = operand_desc(rows + j / 4 * kXBox) + j % 4 * 2;
+                    mma_tmem(d + j / kPerGroup * kMaxCols, at + j * 8, bd, kIdesc, j % kPerGroup != 0);
+                    if (!F::kSubtract) mma_tmem(d + j / kPerGroup * kMaxCols, zero, bd, kIdesc, true);
+                }
+                mma_commit_one(&sh->done[b]);
                 mma_commit_one(&sh->empty[s.i]);
             }
             __syncwarp();
-            buf.next(kBufs);
-            buf.next(kBufs);
-            s.next(kTmemStages);
+            parity ^= 1;
+            s.next(F::kStages, kBufs);
         }
         // the instructions that were issued end before tensor memory is freed
         if (elect_one()) mma_commit_one(&sh->drain);
         mbar_wait_bounded(&sh->drain, 0);
-    } else if (warp >= kFirstEpilogue) {
+    } else if (warp >= F::kFirstSum) {
         const int groups = a.K / a.group;
         const bool up = kSwiglu && (lane & 8);
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         Ring buf(0);
         bool ok = true;
+        if (!F::kSubtract) {
+            tmem_st8(zero + lanes, kMinus136);
+            tmem_wait_st();
+            tmem_fence_before();
+        }
+        __syncwarp();
         if (lane == 0)
             for (int i = 0; i < kBufs; ++i) mbar_arrive(&sh->ready[i]);  // nothing to read in the first round
         for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
@@ -429,32 +465,30 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
             const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + min(chan, a.N - 1);
             const uint16_t *from = static_cast<const uint16_t *>(a.w_scale) + row * groups;
             float acc[kMaxCols] = {};
-            uint16_t next[kPer];
+            uint16_t next[kGroups];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) next[i] = i < groups ? __ldg(from + i) : 0;
-            for (int c = 0; c < spans * 2; ++c) {
-                float scale[kPer];
+            for (int i = 0; i < kGroups; ++i) next[i] = i < groups ? __ldg(from + i) : 0;
+            for (int c = 0; c < spans; ++c) {
+                float scale[kGroups];
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {  // the next chunk's scales while this one's sums are waited for
+                for (int i = 0; i < kGroups; ++i) {  // the next span's scales while this one's sums are waited for
                     scale[i] = __uint_as_float((uint32_t)next[i] << 16);
-                    const int g = (c + 1) * kPer + i;
+                    const int g = (c + 1) * kGroups + i;
                     next[i] = g < groups ? __ldg(from + g) : 0;
                 }
                 ok = all_of(wait_or_abort(&sh->done[buf.i], buf.parity, polls, &sh->abort, a.status));
                 if (!ok) break;
                 tmem_fence_after();
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
+                for (int i = 0; i < kGroups; ++i) {
                     float v[kMaxCols];
-                    tmem_ld16(d0 + ((uint32_t)(quad * 32) << 16) + buf.i * kDCols + i * kMaxCols, v);
-                    if (i == kPer - 1) {
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh->ready[buf.i]);
-                    }
+                    tmem_ld16(d0 + lanes + buf.i * kDCols + i * kMaxCols, v);
 #pragma unroll
                     for (int n = 0; n < kMaxCols; ++n) acc[n] = fmaf(scale[i], v[n], acc[n]);
                 }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->ready[buf.i]);
                 buf.next(kBufs);
             }
             if (!ok) break;
@@ -476,16 +510,16 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
                     if (n < w.rows) y[(size_t)n * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[n]));
             }
         }
-    } else if (warp >= kFirstDequant) {
-        // this warp's lanes: weight rows quad*32 + lane; its chunks: every fourth, always the same A buffer
-        const int mine = (warp - kFirstDequant) >> 2, row = quad * 32 + lane;
-        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + mine * kACols;
+    } else if (warp >= F::kFirstUnpack) {
+        // this warp's lanes: weight rows quad*32 + lane, one half of every kBufs-th span
+        const int b = (warp - F::kFirstUnpack) >> 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + b * kACols + half * (kACols / 2);
         Ring s(0);
-        s.i = mine >> 1;
-        uint32_t done_parity = 1;
-        for (long long c = mine; c < chunks; c += kBufs) {
+        s.i = b;
+        uint32_t parity = 1;
+        for (long long c = b; c < mine; c += kBufs) {
             if (!all_of(wait_or_abort(&sh->full[s.i], s.parity, polls, &sh->abort, a.status)) ||
-                !all_of(wait_or_abort(&sh->done[mine], done_parity, polls, &sh->abort, a.status)))
+                !all_of(wait_or_abort(&sh->done[b], parity, polls, &sh->abort, a.status)))
                 break;
             tmem_fence_after();
             const uint8_t *words = stages + s.i * kStage + row * 128;
@@ -494,12 +528,12 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
                 uint32_t p[32];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int at = (mine & 1) * 4 + h * 2 + i;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(words + ((at ^ (row & 7)) << 4));
-                    unpack_word(v.x, p + i * 16);
-                    unpack_word(v.y, p + i * 16 + 4);
-                    unpack_word(v.z, p + i * 16 + 8);
-                    unpack_word(v.w, p + i * 16 + 12);
+                    const uint4 v =
+                        *reinterpret_cast<const uint4 *>(words + (((half * 4 + h * 2 + i) ^ (row & 7)) << 4));
+                    unpack_word<F::kSubtract>(v.x, p + i * 16);
+                    unpack_word<F::kSubtract>(v.y, p + i * 16 + 4);
+                    unpack_word<F::kSubtract>(v.z, p + i * 16 + 8);
+                    unpack_word<F::kSubtract>(v.w, p + i * 16 + 12);
                 }
                 tmem_st32(to + h * 32, p);
             }
@@ -508,10 +542,9 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->ready[mine]);
-            done_parity ^= 1;
-            s.next(kTmemStages);  // four chunks on: two stages
-            s.next(kTmemStages);
+            if (lane == 0) mbar_arrive(&sh->ready[b]);
+            parity ^= 1;
+            s.next(F::kStages, kBufs);
         }
     }
     __syncwarp();
@@ -547,12 +580,12 @@ cudaError_t launch_w4_tmem(const a2av_plan_s &p, const MatmulArgs &a, cudaStream
         !encode_map(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, xd, xst, xb))
         return cudaErrorInvalidValue;
     const auto kernel = expert_w4_tmem_kernel<kSwiglu, kPer>;
-    const size_t smem = tmem_smem_bytes(a.g.E);
+    const size_t smem = tmem_smem_bytes(TmemForm<kPer>::kStages, a.g.E);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.g.R * a.g.T * a.g.k;
     const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxCols) * ((a.N + kChan - 1) / kChan);
-    return launch_pdl(kernel, (int)(most < p.num_sms ? most : p.num_sms), kTmemThreads, smem, s, mw, mx, a);
+    return launch_pdl(kernel, (int)(most < p.num_sms ? most : p.num_sms), TmemForm<kPer>::kThreads, smem, s, mw, mx, a);
 }
 
 template <bool kSwiglu>
