@@ -467,9 +467,13 @@ bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *
         return found ? reinterpret_cast<EncodeFn>(f) : nullptr;
     }();
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    // Rows that start on 128-byte lines are fetched ahead in pairs of lines; rows that do not would bring lines
+    // in that belong to no box (8,168 rows of K = 1416: 125 us with, 111 us without; K = 1408: 85 us, 87 us).
+    const CUtensorMapL2promotion promotion =
+        strides[0] % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     return encode && encode(m, type, rank, const_cast<void *>(base), dims, strides, box, ones,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_expert_gemm(const a2av_plan_s &p, const MatmulArgs &a, bool fp8, bool swiglu, cudaStream_t s) {
