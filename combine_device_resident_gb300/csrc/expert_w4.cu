@@ -3,15 +3,11 @@
 //   y[r][n] = act( sum_g s[n][g] * sum_{k in g} (q[n][k] - 8) * x[r][k] )
 //
 // Bound by the weights' bytes (half a byte each), so everything is arranged
-// around streaming them: a block of eight warps takes 16 or 32 weight rows,
-// the warps share out K in spans of 256, and each warp keeps its own ring of
-// TMA boxes (32 rows x 128 bytes) in flight, across work items too.  A word of
-// eight 4-bit weights gives four bf16 pairs by a mask and an or each (q | 0x4300
-// is 128 + q) and an exact subtraction; the pairs are A fragments of the 16x8x16
-// matrix instruction, whose legacy form is the right one here: the product
-// needs 2*rows flops per weight, far below any tensor limit, and its operands
-// come out of registers.  Each group's sum is scaled in fp32, so no weight is
-// rounded.  The warps' partial sums meet in shared memory in a fixed order.
+// around streaming them; no weight is rounded, as each group's sum is scaled in
+// fp32.  A word of eight 4-bit weights gives four bf16 pairs by a mask and an
+// or each: q | 0x4300 is 128 + q.  There are two forms: one that shares K out among the
+// warps of a block, for calls with so few weight blocks that a block has to take
+// little, and one on tensor memory.
 #include <cuda_bf16.h>
 
 #include "expert_common.cuh"
@@ -21,8 +17,21 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kSpan = 256;     // K of a TMA box: 128 bytes of a weight row
-constexpr int kStages = 4;     // boxes of 16 weight rows in flight per warp (half as many of 32)
+constexpr int kStages = 4;     // boxes in flight per warp
 constexpr int kMaxRows = 32;   // expert rows per work item
+
+// ---- few work items: K shared out among the warps -------------------------------
+//
+// A block of eight warps takes 16 weight rows; each warp takes every eighth
+// span of 256 of K through its own ring of TMA boxes (16 rows x 128 bytes), in flight across
+// work items too.  The pairs, less 136, are A fragments of the 16x8x16 matrix instruction,
+// whose legacy form is the right one here: the product needs 2 * rows flops
+// per weight, far below any tensor limit, and its operands come out of
+// registers.  The warps' partial sums meet in shared memory in a fixed order.
+// With one row the call is a chain of latencies (launch, places, first box,
+// rows, joining): 9.5 us for 21 million weights.  Loading rows and scales a
+// span ahead cost more instructions than it hid (11.7 us).
+constexpr int kRows = 16, kBoxBytes = kRows * 128;
 
 struct Shared4 {
     uint64_t full[kWarps][kStages];
@@ -52,18 +61,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
-
-// Shared memory of the split form: the warps' rings, their partial sums, the barriers; then the experts' table.
-// Kernel and launch take it from here.
-template <int kMT>
-struct SplitLayout {
-    static constexpr int kRows = kMT * 16, kRing = kStages / kMT, kBoxBytes = kRows * 128;
-    static constexpr size_t kParts = (size_t)kWarps * kRing * kBoxBytes;                         // offsets
-    static constexpr size_t kShared = kParts + (size_t)kWarps * kRows * (kMaxRows + 1) * 4;
-    static constexpr size_t bytes(int E) { return 1024 + kShared + sizeof(Shared4) + (size_t)E * 12; }
-    static_assert(kShared % 8 == 0 && sizeof(Shared4) % 4 == 0, "alignment");
-};
+// Shared memory of this form: the warps' rings, their partial sums, the barriers; then the experts' table.
+constexpr size_t kSplitParts = (size_t)kWarps * kStages * kBoxBytes;  // offsets
+constexpr size_t kSplitShared = kSplitParts + (size_t)kWarps * kRows * (kMaxRows + 1) * 4;
+constexpr size_t split_smem_bytes(int E) { return 1024 + kSplitShared + sizeof(Shared4) + (size_t)E * 12; }
+static_assert(kSplitShared % 8 == 0 && sizeof(Shared4) % 4 == 0, "alignment");
 
 struct Item {
     int e, row, rows, block;
@@ -82,34 +84,26 @@ __device__ __forceinline__ Item item_at(long long t, const int32_t *start, const
     return w;
 }
 
-// One box: kRows weight rows x kSpan of K for kNT*8 expert rows, into acc.
-// Weight rows of tile m: `lower(m) + g` and `upper(m) + g`, g = lane / 4.
-template <int kMT, int kNT, bool kSwiglu>
-__device__ __forceinline__ void accumulate(const uint32_t *box, const MatmulArgs &a, const Item &w, int k0,
-                                           float (&acc)[kMT][4][4]) {
+// One box, 16 weight rows x kSpan of K, for kNT*8 expert rows, into acc.
+template <int kNT, bool kSwiglu>
+__device__ __forceinline__ void box_sums(const uint32_t *box, const MatmulArgs &a, const Item &w, int k0,
+                                         float (&acc)[4][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int words = min(kSpan, a.K - k0) / 32;  // 32-wide steps; K is a multiple of 32
     const int groups = a.K / a.group, per = a.group / 32;
     const uint16_t *x = reinterpret_cast<const uint16_t *>(a.x) + (size_t)w.row * a.K + k0 + t * 8;
-    const uint16_t *scale[kMT][2];
-    int low[kMT][2];
+    const uint16_t *scale[2];
 #pragma unroll
-    for (int m = 0; m < kMT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // swiglu: the lower rows are gates, the upper ones the same channels' ups
-            low[m][h] = kSwiglu ? h * 8 * kMT + m * 8 : m * 16 + h * 8;
-            const int chan = w.block * (kSwiglu ? 8 : 16) * kMT + (kSwiglu ? m * 8 : m * 16 + h * 8) + g;
-            const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (kSwiglu && h ? a.N : 0) + min(chan, a.N - 1);
-            scale[m][h] = static_cast<const uint16_t *>(a.w_scale) + row * groups;
-        }
+    for (int h = 0; h < 2; ++h) {
+        // swiglu: the lower eight rows are gates, the upper eight the same channels' ups
+        const int chan = w.block * (kSwiglu ? 8 : 16) + (kSwiglu ? 0 : h * 8) + g;
+        const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (kSwiglu && h ? a.N : 0) + min(chan, a.N - 1);
+        scale[h] = static_cast<const uint16_t *>(a.w_scale) + row * groups + k0 / a.group;
+    }
     for (int j0 = 0; j0 < words; j0 += per) {  // one group of K at a time
-        float part[kMT][kNT][4] = {};
-        float s[kMT][2];
-#pragma unroll
-        for (int m = 0; m < kMT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) s[m][h] = bf16_at(scale[m][h] + (k0 + j0 * 32) / a.group);
+        const float s0 = __uint_as_float((uint32_t)__ldg(scale[0]++) << 16);
+        const float s1 = __uint_as_float((uint32_t)__ldg(scale[1]++) << 16);
+        float part[kNT][4] = {};
 #pragma unroll 4
         for (int j = j0; j < j0 + per; ++j) {
             uint4 b[kNT];
@@ -117,48 +111,39 @@ __device__ __forceinline__ void accumulate(const uint32_t *box, const MatmulArgs
             for (int n = 0; n < kNT; ++n)
                 b[n] = n * 8 + g < w.rows ? __ldg(reinterpret_cast<const uint4 *>(x + (size_t)(n * 8 + g) * a.K + j * 32))
                                           : make_uint4(0, 0, 0, 0);
+            const uint32_t w0 = box[g * 32 + ((j ^ g) * 4 + t)], w1 = box[(8 + g) * 32 + ((j ^ g) * 4 + t)];
+            const uint32_t p0 = pair_of(w0, 0), p1 = pair_of(w0, 1), p2 = pair_of(w0, 2), p3 = pair_of(w0, 3);
+            const uint32_t q0 = pair_of(w1, 0), q1 = pair_of(w1, 1), q2 = pair_of(w1, 2), q3 = pair_of(w1, 3);
 #pragma unroll
-            for (int m = 0; m < kMT; ++m) {
-                const uint32_t w0 = box[(low[m][0] + g) * 32 + ((j ^ g) * 4 + t)];
-                const uint32_t w1 = box[(low[m][1] + g) * 32 + ((j ^ g) * 4 + t)];
-                const uint32_t p0 = pair_of(w0, 0), p1 = pair_of(w0, 1), p2 = pair_of(w0, 2), p3 = pair_of(w0, 3);
-                const uint32_t q0 = pair_of(w1, 0), q1 = pair_of(w1, 1), q2 = pair_of(w1, 2), q3 = pair_of(w1, 3);
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                    mma16816(part[m][n], p0, q0, p1, q1, b[n].x, b[n].y);
-                    mma16816(part[m][n], p2, q2, p3, q3, b[n].z, b[n].w);
-                }
+            for (int n = 0; n < kNT; ++n) {
+                mma16816(part[n], p0, q0, p1, q1, b[n].x, b[n].y);
+                mma16816(part[n], p2, q2, p3, q3, b[n].z, b[n].w);
             }
         }
 #pragma unroll
-        for (int m = 0; m < kMT; ++m)
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                acc[m][n][0] = fmaf(s[m][0], part[m][n][0], acc[m][n][0]);
-                acc[m][n][1] = fmaf(s[m][0], part[m][n][1], acc[m][n][1]);
-                acc[m][n][2] = fmaf(s[m][1], part[m][n][2], acc[m][n][2]);
-                acc[m][n][3] = fmaf(s[m][1], part[m][n][3], acc[m][n][3]);
-            }
+        for (int n = 0; n < kNT; ++n) {
+            acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
+            acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
+            acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
+            acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
+        }
     }
 }
 
-// kMT: 16-row weight tiles per work item.
-template <int kMT, bool kSwiglu>
+template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                 const MatmulArgs a) {
-    using L = SplitLayout<kMT>;
-    constexpr int kRows = L::kRows, kBoxBytes = L::kBoxBytes, kRing = L::kRing;
     constexpr int kChan = kSwiglu ? kRows / 2 : kRows;  // output channels per work item
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    float *parts = reinterpret_cast<float *>(ring + L::kParts);  // [warp][kRows][kMaxRows + 1]
-    Shared4 *sh = reinterpret_cast<Shared4 *>(ring + L::kShared);
+    float *parts = reinterpret_cast<float *>(ring + kSplitParts);  // [warp][kRows][kMaxRows + 1]
+    Shared4 *sh = reinterpret_cast<Shared4 *>(ring + kSplitShared);
     const int E = a.g.E;
     int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
     int32_t *count = start + E;
     int32_t *pre = count + E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < kWarps * kRing) mbar_init(&sh->full[tid / kRing][tid % kRing], 1);
+    if (tid < kWarps * kStages) mbar_init(&sh->full[tid / kStages][tid % kStages], 1);
     if (tid == 0) {
         sh->abort = 0;
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
@@ -170,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
     const long long items = (long long)total * blocks;
     const int spans = (a.K + kSpan - 1) / kSpan;
 
-    uint8_t *mine = ring + warp * kRing * kBoxBytes;
+    uint8_t *mine = ring + warp * kStages * kBoxBytes;
     // The warp's boxes in order: of item i of this block, spans (warp + i) % kWarps, + kWarps, ...; the
     // rotation evens out a K whose spans do not divide by the warps.
     long long put_t = blockIdx.x;
@@ -186,34 +171,31 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         if (put_t >= items) return;
         if (lane == 0) {
             const Item w = item_at(put_t, start, count, pre, E, blocks, kMaxRows);
-            uint64_t *bar = &sh->full[warp][put % kRing];
+            uint64_t *bar = &sh->full[warp][put % kStages];
             mbar_arrive_expect_tx(bar, kBoxBytes);
             asm volatile(
                 "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-                "%5}], [%6];" ::"r"(smem_u32(mine + put % kRing * kBoxBytes)),
+                "%5}], [%6];" ::"r"(smem_u32(mine + put % kStages * kBoxBytes)),
                 "l"(&map_w), "r"(put_span * (kSpan / 8)), "r"(w.block * kChan), "r"(0), "r"(w.e), "r"(smem_u32(bar))
                 : "memory");
         }
         put_span += kWarps;
         ++put;
     };
-    for (int i = 0; i < kRing; ++i) issue();
-
+    for (int i = 0; i < kStages; ++i) issue();
     int i = 0;
     for (long long t = blockIdx.x; t < items; t += gridDim.x, ++i) {
         const Item w = item_at(t, start, count, pre, E, blocks, kMaxRows);
-        float acc[kMT][4][4] = {};
+        float acc[4][4] = {};
         for (int span = (warp + i) % kWarps; ok && span < spans; span += kWarps) {
-            const int s = got % kRing;
-            const bool in = mbar_wait_bounded(&sh->full[warp][s], (got / kRing) & 1, a.wait_polls);
-            if (!__all_sync(0xffffffffu, in)) {
-                ok = false;
-                break;
-            }
-            const uint32_t *box = reinterpret_cast<const uint32_t *>(mine + s * kBoxBytes);
-            if (w.rows <= 8) accumulate<kMT, 1, kSwiglu>(box, a, w, span * kSpan, acc);
-            else if (w.rows <= 16) accumulate<kMT, 2, kSwiglu>(box, a, w, span * kSpan, acc);
-            else accumulate<kMT, 4, kSwiglu>(box, a, w, span * kSpan, acc);
+            const int at = got % kStages;
+            const bool in = mbar_wait_bounded(&sh->full[warp][at], (got / kStages) & 1, a.wait_polls);
+            ok = all_of(in);
+            if (!ok) break;
+            const uint32_t *box = reinterpret_cast<const uint32_t *>(mine + at * kBoxBytes);
+            if (w.rows <= 8) box_sums<1, kSwiglu>(box, a, w, span * kSpan, acc);
+            else if (w.rows <= 16) box_sums<2, kSwiglu>(box, a, w, span * kSpan, acc);
+            else box_sums<4, kSwiglu>(box, a, w, span * kSpan, acc);
             ++got;
             __syncwarp();  // every lane has read the box
             issue();
@@ -225,24 +207,20 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         const int g = lane >> 2, q = lane & 3;
         float *p = parts + warp * kRows * (kMaxRows + 1);
 #pragma unroll
-        for (int m = 0; m < kMT; ++m)
+        for (int n = 0; n < 4; ++n)
+            if (n * 8 < w.rows) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                if (n * 8 < w.rows) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        p[(m * 16 + (c >> 1) * 8 + g) * (kMaxRows + 1) + n * 8 + q * 2 + (c & 1)] = acc[m][n][c];
-                }
+                for (int c = 0; c < 4; ++c) p[((c >> 1) * 8 + g) * (kMaxRows + 1) + n * 8 + q * 2 + (c & 1)] = acc[n][c];
+            }
         __syncthreads();
         if (*(volatile uint32_t *)&sh->abort == 0)
             for (int o = tid; o < kChan * w.rows; o += kThreads) {
                 const int chan = o % kChan, r = o / kChan;
-                const int lower = kSwiglu ? chan / 8 * 16 + chan % 8 : chan;
                 float sum = 0.0f, up = 0.0f;
 #pragma unroll
                 for (int v = 0; v < kWarps; ++v) {
-                    sum += parts[(v * kRows + lower) * (kMaxRows + 1) + r];
-                    if (kSwiglu) up += parts[(v * kRows + lower + 8) * (kMaxRows + 1) + r];
+                    sum += parts[(v * kRows + chan) * (kMaxRows + 1) + r];
+                    if (kSwiglu) up += parts[(v * kRows + chan + 8) * (kMaxRows + 1) + r];
                 }
                 const float out = kSwiglu ? __fdividef(sum, 1.0f + __expf(-sum)) * up : sum;
                 const int n = w.block * kChan + chan;
@@ -251,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         __syncthreads();
     }
     if (!ok)  // given up: the boxes that were issued land before the block ends
-        for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kRing], (got / kRing) & 1);
+        for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kStages], (got / kStages) & 1);
 }
 
 // ---- many work items: tensor memory ---------------------------------------------
@@ -556,15 +534,6 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
     }
 }
 
-cudaError_t map_words(CUtensorMap *m, const MatmulArgs &a, bool swiglu, int chan) {
-    const cuuint64_t halves = swiglu ? 2 : 1, row = (cuuint64_t)a.K / 2;
-    // w as [E][gate, up][N][K/8]
-    const cuuint64_t dims[4] = {(cuuint64_t)a.K / 8, (cuuint64_t)a.N, halves, (cuuint64_t)a.g.E};
-    const cuuint64_t strides[3] = {row, a.N * row, halves * a.N * row};
-    const cuuint32_t box[4] = {kSpan / 8, (cuuint32_t)chan, (cuuint32_t)halves, 1};
-    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, a.w, dims, strides, box) ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <bool kSwiglu, int kPer>
 cudaError_t launch_w4_tmem(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
     constexpr int kChan = kSwiglu ? kTileRows / 2 : kTileRows;
@@ -595,20 +564,24 @@ cudaError_t launch_w4_groups(const a2av_plan_s &p, const MatmulArgs &a, cudaStre
                            : launch_w4_tmem<kSwiglu, 1>(p, a, s);
 }
 
-template <int kMT, bool kSwiglu>
-cudaError_t launch_w4(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
-    constexpr int kRows = kMT * 16, kChan = kSwiglu ? kRows / 2 : kRows;
+template <bool kSwiglu>
+cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
+    constexpr int kChan = kSwiglu ? kRows / 2 : kRows;
+    const cuuint64_t halves = kSwiglu ? 2 : 1, row = (cuuint64_t)a.K / 2;
     CUtensorMap m;
-    cudaError_t e = map_words(&m, a, kSwiglu, kChan);
-    if (e != cudaSuccess) return e;
-    const size_t smem = SplitLayout<kMT>::bytes(a.g.E);
-    e = cudaFuncSetAttribute(expert_w4_kernel<kMT, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    // w as [E][gate, up][N][K/8]
+    const cuuint64_t dims[4] = {(cuuint64_t)a.K / 8, (cuuint64_t)a.N, halves, (cuuint64_t)a.g.E};
+    const cuuint64_t strides[3] = {row, a.N * row, halves * a.N * row};
+    const cuuint32_t box[4] = {kSpan / 8, kChan, (cuuint32_t)halves, 1};
+    if (!encode_map(&m, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, a.w, dims, strides, box)) return cudaErrorInvalidValue;
+    const size_t smem = split_smem_bytes(a.g.E);
+    const cudaError_t e =
+        cudaFuncSetAttribute(expert_w4_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.g.R * a.g.T * a.g.k;
     const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxRows) * ((a.N + kChan - 1) / kChan);
     const int grid = (int)(most < 2 * p.num_sms ? most : 2 * p.num_sms);
-    return launch_pdl(expert_w4_kernel<kMT, kSwiglu>, grid, kThreads, smem, s, m, a);
+    return launch_pdl(expert_w4_kernel<kSwiglu>, grid, kThreads, smem, s, m, a);
 }
 
 }  // namespace
@@ -617,7 +590,7 @@ cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swi
     const long long rows = (long long)a.g.R * a.g.T * a.g.k, experts = rows < a.g.E ? rows : a.g.E;
     const bool wide = experts * (swiglu ? 2 : 1) * a.N / 128 >= 2 * p.num_sms;
     if (wide) return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
-    return swiglu ? launch_w4<1, true>(p, a, s) : launch_w4<1, false>(p, a, s);
+    return swiglu ? launch_w4_split<true>(p, a, s) : launch_w4_split<false>(p, a, s);
 }
 
 }  // namespace a2av
