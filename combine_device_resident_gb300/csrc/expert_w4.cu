@@ -305,6 +305,48 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t *p) {
     for (int i = 0; i < 4; ++i) p[i] = kSubtract ? pair_of(w, i) : raw_pair(w, i);
 }
 
+// The bf16 scales of groups at .. at + kGroups - 1 of a weight row, in pairs; zeros behind the last. In one load
+// where they lie aligned: the lanes' rows are apart, and each load of a warp takes a cycle per row.
+template <int kGroups>
+__device__ __forceinline__ void fetch_scales(uint32_t (&to)[kGroups / 2], const uint16_t *from, int at, int groups,
+                                             bool aligned) {
+#pragma unroll
+    for (int i = 0; i < kGroups / 2; ++i) to[i] = 0;
+    if (at >= groups) return;
+    if (aligned) {
+        if constexpr (kGroups == 2) {
+            to[0] = __ldg(reinterpret_cast<const uint32_t *>(from + at));
+        } else if constexpr (kGroups == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from + at));
+            to[0] = v.x, to[1] = v.y;
+        } else {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from + at));
+            to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+        if (at + i < groups) to[i / 2] |= (uint32_t)__ldg(from + at + i) << (i % 2 * 16);
+}
+
+// acc[n] += scale[i] * D_i[n] for the first kCols rows, kAtMost groups' columns at a time.
+template <int kCols, int kAtMost, int kGroups>
+__device__ __forceinline__ void add_groups(uint32_t d, const float (&scale)[kGroups], float (&acc)[kMaxCols]) {
+    constexpr int kAtOnce = kGroups < kAtMost ? kGroups : kAtMost;
+#pragma unroll
+    for (int i0 = 0; i0 < kGroups; i0 += kAtOnce) {
+        float v[kAtOnce][kCols];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) tmem_ld<kCols>(d + (i0 + i) * kMaxCols, v[i]);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) acc[n] = fmaf(scale[i0 + i], v[i][n], acc[n]);
+    }
+}
+
 template <bool kSwiglu, int kPer>
 __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
     expert_w4_tmem_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -425,6 +467,7 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
         const int groups = a.K / a.group;
         const bool up = kSwiglu && (lane & 8);
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const bool aligned = groups % kGroups == 0 && reinterpret_cast<uintptr_t>(a.w_scale) % 16 == 0;
         Ring buf(0);
         bool ok = true;
         if (!F::kSubtract) {
@@ -443,27 +486,26 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
             const size_t row = (size_t)w.e * a.N * (kSwiglu ? 2 : 1) + (up ? a.N : 0) + min(chan, a.N - 1);
             const uint16_t *from = static_cast<const uint16_t *>(a.w_scale) + row * groups;
             float acc[kMaxCols] = {};
-            uint16_t next[kGroups];
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) next[i] = i < groups ? __ldg(from + i) : 0;
+            uint32_t next[kGroups / 2];
+            fetch_scales<kGroups>(next, from, 0, groups, aligned);
             for (int c = 0; c < spans; ++c) {
                 float scale[kGroups];
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) {  // the next span's scales while this one's sums are waited for
-                    scale[i] = __uint_as_float((uint32_t)next[i] << 16);
-                    const int g = (c + 1) * kGroups + i;
-                    next[i] = g < groups ? __ldg(from + g) : 0;
+                for (int i = 0; i < kGroups; i += 2) {
+                    scale[i] = __uint_as_float(next[i / 2] << 16);
+                    scale[i + 1] = __uint_as_float(next[i / 2] & 0xffff0000u);
                 }
+                // the next span's scales while this one's sums are waited for
+                fetch_scales<kGroups>(next, from, (c + 1) * kGroups, groups, aligned);
                 ok = all_of(wait_or_abort(&sh->done[buf.i], buf.parity, polls, &sh->abort, a.status));
                 if (!ok) break;
                 tmem_fence_after();
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i) {
-                    float v[kMaxCols];
-                    tmem_ld16(d0 + lanes + buf.i * kDCols + i * kMaxCols, v);
-#pragma unroll
-                    for (int n = 0; n < kMaxCols; ++n) acc[n] = fmaf(scale[i], v[n], acc[n]);
-                }
+                // (with two groups a span there is little to leave out, and registers are few)
+                const uint32_t d = d0 + lanes + buf.i * kDCols;
+                if (kPer == 1) add_groups<16, 1>(d, scale, acc);
+                else if (w.rows <= 4) add_groups<4, 8>(d, scale, acc);
+                else if (w.rows <= 8) add_groups<8, 4>(d, scale, acc);
+                else add_groups<16, 2>(d, scale, acc);
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->ready[buf.i]);
