@@ -630,8 +630,11 @@ cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStrea
 
 cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s) {
     const long long rows = (long long)a.g.R * a.g.T * a.g.k, experts = rows < a.g.E ? rows : a.g.E;
-    const bool wide = experts * (swiglu ? 2 : 1) * a.N / 128 >= 2 * p.num_sms;
-    if (wide) return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
+    // Items of 128 weight rows the call can have: from a third of the SMs on, the form on tensor memory is the
+    // faster one (K = 5120, SwiGLU to 2048: one expert, 32 items, 14.6 us against 9.5; two, 64 items, 14.5 against
+    // 17.3; sixteen 40.6 against 96; K = 2048 to 5120: one expert, 40 items, 9.5 against 8.7).
+    const bool many = experts * (swiglu ? 2 : 1) * a.N / kTileRows >= p.num_sms / 3;
+    if (many) return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
     return swiglu ? launch_w4_split<true>(p, a, s) : launch_w4_split<false>(p, a, s);
 }
 
