@@ -36,13 +36,17 @@ constexpr int kTileM = 128;         // weight rows per block of a pair
 constexpr int kTileN = 256;         // expert rows per tile, at most
 constexpr int kABytes = kTileM * kRowBytes;
 constexpr int kBBytes = kTileN / 2 * kRowBytes;  // half of them in each block
-constexpr int kStageBytes = kABytes + kBBytes;
+// The ring: six stages for any tile; or, when no expert has more than 32 rows, ten whose row part holds just these:
+// such a call streams weights, and what an SM gets is what it has in flight.
+constexpr int kStageBytes = kABytes + kBBytes, kRingBytes = kStages * kStageBytes;
+constexpr int kFewRows = 32, kFewStageBytes = kABytes + kFewRows / 2 * kRowBytes, kFewStages = 10;
+static_assert(kFewStages * kFewStageBytes <= kRingBytes && kFewStageBytes % 1024 == 0, "one ring");
 // Rows of x a block loads at once: the first box that holds its share (128 at most).
 __host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : i == 1 ? 64 : 128; }
 constexpr int kBand = 8;            // row tiles of an expert that run with one channel tile in turn
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kFewStages], empty[kFewStages];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     uint32_t abort;
@@ -151,10 +155,10 @@ __device__ __forceinline__ Tile tile_at(long long t, const int32_t *start, const
     // An expert's row tiles are taken kBand at a time, every channel tile of
     // a band before the next band: the band's rows and the weights stay in L2
     // while they are used again.
-    const int in = (int)(t - (long long)pre[lo] * ctiles);
-    const int band = in / (kBand * ctiles);
+    const long long in = t - (long long)pre[lo] * ctiles;
+    const int band = (int)(in / (kBand * ctiles));
     const int wide = min(kBand, rt - band * kBand);
-    const int rem = in - band * kBand * ctiles;
+    const int rem = (int)(in - (long long)band * kBand * ctiles);
     Tile r;
     r.e = lo;
     r.ctile = rem / wide;
@@ -171,13 +175,17 @@ __device__ __forceinline__ Tile uniform(const Tile &t) {
                 __shfl_sync(0xffffffffu, t.ctile, 0)};
 }
 
+// Shared memory: the ring, the barriers, the experts' table.
+constexpr size_t smem_bytes(int E) { return 1024 + kRingBytes + sizeof(Shared) + (size_t)E * 12; }
+static_assert(smem_bytes(kMaxExperts) <= 232448, "shared memory");
+
 template <bool kFp8, bool kSwiglu>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x,
                        const MatmulArgs a) {
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    Shared *sh = reinterpret_cast<Shared *>(stages + kStages * kStageBytes);
+    Shared *sh = reinterpret_cast<Shared *>(stages + kRingBytes);
     const int E = a.g.E;
     int32_t *start = reinterpret_cast<int32_t *>(sh + 1);
     int32_t *count = start + E;
@@ -187,7 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t peer_abort = in_block(&sh->abort, rank ^ 1);
 
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kFewStages; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->empty[s], 1);
         }
@@ -212,6 +220,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     tmem_fence_before();
     const int total = place_experts<kThreads>(a, kTileN, start, count, pre, sh->warp_sum);  // ends in a barrier
+    bool more_rows = false;
+    for (int e = tid; e < E; e += kThreads) more_rows |= count[e] > kFewRows;
+    more_rows = __syncthreads_or(more_rows);
+    const int ring = more_rows ? kStages : kFewStages, stage_bytes = more_rows ? kStageBytes : kFewStageBytes;
     cluster_sync();  // the other block's barriers are set up, too
     tmem_fence_after();
 
@@ -247,13 +259,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                            a.status, peer_abort)))
                     return false;
                 const int s = put_s;
-                if (++put_s == kStages) {
+                if (++put_s == ring) {
                     put_s = 0;
                     put_parity ^= 1;
                 }
                 free = wait && a.wait_polls > 0 && mbar_test_wait(&sh->empty[put_s], put_parity);
                 if (elect_one()) {
-                    const uint32_t at = base + s * kStageBytes, bar = full0 + s * 8;
+                    const uint32_t at = base + s * stage_bytes, bar = full0 + s * 8;
                     if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], bytes);
                     tma_weights(at, &map_w, put_kb * kStep, block, w.e, bar);
                     tma_rows(at + kABytes, map, put_kb * kStep, row, bar);
@@ -269,9 +281,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         bool ok = produce(true, 0);
         // the arrivals on the last fills' barriers come from the first block: they are in before this one may end
-        for (int i = 0, s = put_s, par = put_parity; ok && i < kStages; ++i) {
+        for (int i = 0, s = put_s, par = put_parity; ok && i < ring; ++i) {
             ok = all_of(wait_or_abort(&sh->empty[s], par, a.wait_polls, &sh->abort, a.status, peer_abort));
-            if (++s == kStages) {
+            if (++s == ring) {
                 s = 0;
                 par ^= 1;
             }
@@ -296,14 +308,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = in || all_of(wait_or_abort(&sh->full[s], parity, a.wait_polls, &sh->abort, a.status, peer_abort));
                     if (!ok) break;
                     const int now = s;
-                    if (++s == kStages) {
+                    if (++s == ring) {
                         s = 0;
                         parity ^= 1;
                     }
                     in = mbar_test_wait(&sh->full[s], parity);
                     tmem_fence_after();
                     if (elect_one()) {
-                        const uint32_t at = base + now * kStageBytes;
+                        const uint32_t at = base + now * stage_bytes;
                         const uint64_t da = operand_desc(at), db = operand_desc(at + kABytes);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)  // 32 bytes of K per instruction
@@ -403,9 +415,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // them to land: the last fill of each stage.
         if (warp == 0) {
             produce(false, *(volatile uint32_t *)&sh->other_fills);
-            for (int i = 0; rank == 0 && i < kStages; ++i) {
+            for (int i = 0; rank == 0 && i < ring; ++i) {
                 if (--put_s < 0) {
-                    put_s = kStages - 1;
+                    put_s = ring - 1;
                     put_parity ^= 1;
                 }
                 if (fills-- > 0) mbar_wait_bounded(&sh->full[put_s], put_parity ^ 1);
@@ -439,7 +451,7 @@ cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t 
         const cuuint32_t xb[2] = {step, (cuuint32_t)box_rows(i)};
         if (!encode_map(&mx.box[i], type, 2, a.x, xd, xst, xb)) return cudaErrorInvalidValue;
     }
-    const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared) + (size_t)a.g.E * 3 * 4;
+    const size_t smem = smem_bytes(a.g.E);
     cudaError_t e = cudaFuncSetAttribute(expert_gemm_kernel<kFp8, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;

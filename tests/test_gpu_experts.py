@@ -253,6 +253,13 @@ def test_products(kind, shape, K, N, swiglu):
     run_product(kind, COUNTS[shape], K, N, swiglu, seed=K + N)["plan"].close()
 
 
+@pytest.mark.parametrize("most", [32, 33])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_either_ring(kind, most):
+    """Up to 32 rows an expert the stages are smaller and more; enough of K to go round both rings."""
+    run_product(kind, [[1, most, 0, 17, 5]], 2576, 264, True, seed=most)["plan"].close()
+
+
 @pytest.mark.parametrize("kind,K", [("bf16", 8), ("e4m3", 16), ("int4", 32)])
 def test_smallest_k(kind, K):
     run_product(kind, COUNTS["ragged"], K, 8, False)["plan"].close()
