@@ -552,6 +552,8 @@ a2av_status_t a2av_expert_matmul(a2av_plan_t p, const void *x, const void *w, co
     a.y = static_cast<uint16_t *>(y);
     a.status = p->status;
     a.arena_rows = rows;
+    const int64_t assignments = (int64_t)p->g.R * p->g.T * p->g.k;
+    a.rows_most = rows < assignments ? rows : assignments;
     a.x_pitch = (int64_t)pitch;
     a.wait_polls = p->wait_polls;
     a.K = K;

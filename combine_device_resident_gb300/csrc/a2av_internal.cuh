@@ -149,6 +149,7 @@ struct MatmulArgs {
     uint16_t *y;
     uint32_t *status;
     int64_t arena_rows, x_pitch, wait_polls;
+    int64_t rows_most;  // live rows there can be: the lesser of R*T*k and the arena
     int32_t K, N, group;
 };
 

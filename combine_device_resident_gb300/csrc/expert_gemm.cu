@@ -141,6 +141,8 @@ __device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap *m, 
 struct RowMaps {
     CUtensorMap box[3];
 };
+// Boxes a call can use: counts are cut to the arena, and an expert of up to kFewRows rows needs the first alone.
+__host__ __device__ inline int row_boxes(const MatmulArgs &a) { return a.arena_rows > kFewRows ? 3 : 1; }
 
 // One unit of work: rows [row, row + rows) of expert e times channel tile `ctile`.
 struct Tile {
@@ -214,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (tid == 64) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
-        for (int i = 0; i < 3; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x.box[i]));
+        for (int i = 0; i < row_boxes(a); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x.box[i]));
     }
     grid_dependency_wait();
 
@@ -447,16 +449,17 @@ cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t 
     const cuuint64_t xst[1] = {(cuuint64_t)a.x_pitch};
     const CUtensorMapDataType type = kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     if (!encode_map(&mw, type, 5, a.w, wd, wst, wb)) return cudaErrorInvalidValue;
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < row_boxes(a); ++i) {
         const cuuint32_t xb[2] = {step, (cuuint32_t)box_rows(i)};
         if (!encode_map(&mx.box[i], type, 2, a.x, xd, xst, xb)) return cudaErrorInvalidValue;
     }
     const size_t smem = smem_bytes(a.g.E);
-    cudaError_t e = cudaFuncSetAttribute(expert_gemm_kernel<kFp8, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e =
+        allow_smem(expert_gemm_kernel<kFp8, kSwiglu>, allowed, p.cfg.device, smem_bytes(kMaxExperts));
     if (e != cudaSuccess) return e;
     // at most this many tiles: each expert with rows begins one more than its rows fill
-    const long long rows = (long long)a.g.R * a.g.T * a.g.k, chan = kSwiglu ? kTileM : 2 * kTileM;
+    const long long rows = a.rows_most, chan = kSwiglu ? kTileM : 2 * kTileM;
     const long long most = ((rows < (long long)E ? rows : (long long)E) + rows / kTileN) * ((a.N + chan - 1) / chan);
     const int grid = 2 * (int)(most < p.num_sms / 2 ? most : p.num_sms / 2);
     return launch_pdl(expert_gemm_kernel<kFp8, kSwiglu>, grid, kThreads, smem, s, mw, mx, a);

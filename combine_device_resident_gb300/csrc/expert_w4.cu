@@ -592,9 +592,11 @@ cudaError_t launch_w4_tmem(const a2av_plan_s &p, const MatmulArgs &a, cudaStream
         return cudaErrorInvalidValue;
     const auto kernel = expert_w4_tmem_kernel<kSwiglu, kPer>;
     const size_t smem = tmem_smem_bytes(TmemForm<kPer>::kStages, a.g.E);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e =
+        allow_smem(kernel, allowed, p.cfg.device, tmem_smem_bytes(TmemForm<kPer>::kStages, kMaxExperts));
     if (e != cudaSuccess) return e;
-    const long long rows = (long long)a.g.R * a.g.T * a.g.k;
+    const long long rows = a.rows_most;
     const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxCols) * ((a.N + kChan - 1) / kChan);
     return launch_pdl(kernel, (int)(most < p.num_sms ? most : p.num_sms), TmemForm<kPer>::kThreads, smem, s, mw, mx, a);
 }
@@ -617,10 +619,10 @@ cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStrea
     const cuuint32_t box[4] = {kSpan / 8, kChan, (cuuint32_t)halves, 1};
     if (!encode_map(&m, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, a.w, dims, strides, box)) return cudaErrorInvalidValue;
     const size_t smem = split_smem_bytes(a.g.E);
-    const cudaError_t e =
-        cudaFuncSetAttribute(expert_w4_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(expert_w4_kernel<kSwiglu>, allowed, p.cfg.device, split_smem_bytes(kMaxExperts));
     if (e != cudaSuccess) return e;
-    const long long rows = (long long)a.g.R * a.g.T * a.g.k;
+    const long long rows = a.rows_most;
     const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxRows) * ((a.N + kChan - 1) / kChan);
     const int grid = (int)(most < 2 * p.num_sms ? most : 2 * p.num_sms);
     return launch_pdl(expert_w4_kernel<kSwiglu>, grid, kThreads, smem, s, m, a);
@@ -629,7 +631,7 @@ cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStrea
 }  // namespace
 
 cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s) {
-    const long long rows = (long long)a.g.R * a.g.T * a.g.k, experts = rows < a.g.E ? rows : a.g.E;
+    const long long rows = a.rows_most, experts = rows < a.g.E ? rows : a.g.E;
     // Items of 128 weight rows the call can have: from a third of the SMs on, the form on tensor memory is the
     // faster one (K = 5120, SwiGLU to 2048: one expert, 32 items, 14.6 us against 9.5; two, 64 items, 14.5 against
     // 17.3; sixteen 40.6 against 96; K = 2048 to 5120: one expert, 40 items, 9.5 against 8.7).
