@@ -523,12 +523,12 @@ a2av_status_t a2av_expert_matmul(a2av_plan_t p, const void *x, const void *w, co
     if (p->g.epr > 1 && !aligned(splits->recv_expert_offsets, 4))
         return refuse("a2av_expert_matmul: recv_expert_offsets is needed");
     if (N < 8 || N % 8 || N > a2av::kMaxWidth)
-        return refuse("a2av_expert_matmul: N must be a multiple of 8, at most 2^20");
+        return refuse("a2av_expert_matmul: N must be a multiple of 8, at most 2^18");
     if (weight_type == A2AV_W_INT4 && group != 32 && group != 64 && group != 128)
         return refuse("a2av_expert_matmul: group must be 32, 64 or 128");
     const int32_t unit = weight_type == A2AV_W_BF16 ? 8 : weight_type == A2AV_W_E4M3 ? 16 : group;
     if (K < unit || K % unit || K > a2av::kMaxWidth)
-        return refuse("a2av_expert_matmul: K must be a multiple of 8 (bf16), 16 (e4m3) or the group (int4), at most 2^20");
+        return refuse("a2av_expert_matmul: K must be a multiple of 8 (bf16), 16 (e4m3) or the group (int4), at most 2^18");
     const int64_t rows = a2av_recv_arena_rows(&p->cfg);
     const bool swiglu = activation == A2AV_ACT_SWIGLU;
     const size_t pitch = weight_type == A2AV_W_E4M3 ? (size_t)K + 16 : (size_t)K * 2;

@@ -19,7 +19,7 @@ constexpr int kMaxRanks = 64;
 constexpr int kMaxExperts = 2048;
 constexpr int kMaxTopk = 32;
 constexpr int kMaxNormRow = 32768;    // row length of the norm: one block holds the row
-constexpr int kMaxWidth = 1 << 20;    // K and N of the experts' products
+constexpr int kMaxWidth = 1 << 18;    // K and N of the experts' products (a tensor map's strides end at 2^40 bytes)
 
 // Status bit set when a bounded wait gives up (should never happen: every wait
 // in these kernels is on copies this CTA issued itself).

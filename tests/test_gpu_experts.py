@@ -329,6 +329,20 @@ def test_nan_stays_in_its_row_and_expert(kind):
     r["plan"].close()
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_nan_stays_in_its_row_with_many_items(group):
+    r = run_product("int4", [[5, 40, 0, 20]], 256, 3600, False, group=group)
+    clean = r["y"].clone()
+    r["x"][7, 3] = float("nan")
+    r["x"][9, 30] = float("inf")
+    r["call"]()
+    torch.cuda.synchronize()
+    assert torch.isnan(r["y"][7]).all() and not torch.isfinite(r["y"][9]).any()
+    keep = [i for i in range(65) if i not in (7, 9)]
+    assert torch.equal(r["y"][keep], clean[keep])
+    r["plan"].close()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "int4"])
 def test_infinite_sums_and_large_gates(kind):
     # gates far out on both sides: silu is 0 or the gate itself, never NaN
