@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 //
 // The steps are short and the way round a buffer is long (barriers and latencies: some
 // 2000 cycles for a span of 256 of K, whose weights take 700 to arrive), so
-// each buffer has its own eight unpacking warps and its own issuing warp,
+// each buffer has its own four unpacking warps and its own issuing warp (eight
+// warps with half a span each: 569 us against 535 on 1,024 rows, the waits being per warp),
 // and there are as many buffers as tensor memory holds.  (A barrier's
 // parity tells a waiter only that the last phase is over: whoever waits for
 // a buffer has to see every phase of it.)
@@ -263,7 +264,7 @@ struct TmemForm {
     static constexpr int kGroups = 2 * kPer, kDCols = kGroups * kMaxCols;  // of a span
     static constexpr int kBufs = kPer == 1 ? 3 : 2, kStages = kPer == 1 ? 6 : 8;
     static constexpr bool kSubtract = kPer == 4;  // no columns left for the constant A: q - 8 is unpacked
-    static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 8 * kBufs;  // warp 0 loads, 1 .. kBufs issue
+    static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kBufs;  // warp 0 loads, 1 .. kBufs issue
     static constexpr int kThreads = (kFirstSum + 4) * 32;
     static constexpr int kZeroAt = kBufs * (kACols + kDCols);  // column
     static_assert(kZeroAt + (kSubtract ? 0 : kZeroCols) <= 512, "tensor memory");
@@ -365,10 +366,10 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < F::kStages; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->empty[s], 9);  // the eight warps that read its words, and the instructions that read its rows
+            mbar_init(&sh->empty[s], 5);  // the four warps that read its words, and the instructions that read its rows
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&sh->ready[i], 12);  // eight warps fill, four read
+            mbar_init(&sh->ready[i], 8);  // four warps fill, four read
             mbar_init(&sh->done[i], 1);
         }
         mbar_init(&sh->drain, kBufs);
@@ -531,9 +532,9 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
             }
         }
     } else if (warp >= F::kFirstUnpack) {
-        // this warp's lanes: weight rows quad*32 + lane, one half of every kBufs-th span
-        const int b = (warp - F::kFirstUnpack) >> 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
-        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + b * kACols + half * (kACols / 2);
+        // this warp's lanes: weight rows quad*32 + lane of every kBufs-th span
+        const int b = (warp - F::kFirstUnpack) >> 2, row = quad * 32 + lane;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + b * kACols;
         Ring s(0);
         s.i = b;
         uint32_t parity = 1;
@@ -544,12 +545,12 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
             tmem_fence_after();
             const uint8_t *words = stages + s.i * kStage + row * 128;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 64 of K: 32 columns
+            for (int h = 0; h < 4; ++h) {  // 64 of K: 32 columns
                 uint32_t p[32];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint4 v =
-                        *reinterpret_cast<const uint4 *>(words + (((half * 4 + h * 2 + i) ^ (row & 7)) << 4));
+                        *reinterpret_cast<const uint4 *>(words + (((h * 2 + i) ^ (row & 7)) << 4));
                     unpack_word<F::kSubtract>(v.x, p + i * 16);
                     unpack_word<F::kSubtract>(v.y, p + i * 16 + 4);
                     unpack_word<F::kSubtract>(v.z, p + i * 16 + 8);
