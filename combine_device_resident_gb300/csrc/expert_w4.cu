@@ -274,8 +274,8 @@ constexpr int kMaxStages = 8, kMaxBufs = 3;
 
 struct SharedTmem {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    // ready: A is filled and the accumulators of a round ago are read; done: the instructions have ended
-    uint64_t ready[kMaxBufs], done[kMaxBufs], drain;
+    // ready: a half of A is filled (and the accumulators of a round ago are read); done: the instructions have ended
+    uint64_t ready[2][kMaxBufs], done[kMaxBufs], drain;
     uint32_t tmem, abort;
     int32_t warp_sum[32];
 };
@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
             mbar_init(&sh->empty[s], 5);  // the four warps that read its words, and the instructions that read its rows
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&sh->ready[i], 8);  // four warps fill, four read
+            mbar_init(&sh->ready[0][i], 8);  // four warps fill, four read
+            mbar_init(&sh->ready[1][i], 4);
             mbar_init(&sh->done[i], 1);
         }
         mbar_init(&sh->drain, kBufs);
@@ -444,20 +445,28 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
         uint32_t parity = 0;
         for (long long c = b; c < mine; c += kBufs) {
             // (that the rows of x are there follows: the warps that filled A waited for the stage)
-            if (!all_of(wait_or_abort(&sh->ready[b], parity, polls, &sh->abort, a.status))) break;
-            tmem_fence_after();
-            if (elect_one()) {
-                const uint32_t rows = smem_u32(stages) + s.i * kStage + kWBytes;
+            bool ok = true;
 #pragma unroll
-                for (int j = 0; j < kSteps; ++j) {
-                    const uint64_t bd = operand_desc(rows + j / 4 * kXBox) + j % 4 * 2;
-                    mma_tmem(d + j / kPerGroup * kMaxCols, at + j * 8, bd, kIdesc, j % kPerGroup != 0);
-                    if (!F::kSubtract) mma_tmem(d + j / kPerGroup * kMaxCols, zero, bd, kIdesc, true);
+            for (int half = 0; half < 2; ++half) {  // the first half's instructions run while the second is unpacked
+                ok = ok && all_of(wait_or_abort(&sh->ready[half][b], parity, polls, &sh->abort, a.status));
+                if (!ok) break;
+                tmem_fence_after();
+                if (elect_one()) {
+                    const uint32_t rows = smem_u32(stages) + s.i * kStage + kWBytes;
+#pragma unroll
+                    for (int j = half * (kSteps / 2); j < (half + 1) * (kSteps / 2); ++j) {
+                        const uint64_t bd = operand_desc(rows + j / 4 * kXBox) + j % 4 * 2;
+                        mma_tmem(d + j / kPerGroup * kMaxCols, at + j * 8, bd, kIdesc, j % kPerGroup != 0);
+                        if (!F::kSubtract) mma_tmem(d + j / kPerGroup * kMaxCols, zero, bd, kIdesc, true);
+                    }
+                    if (half == 1) {
+                        mma_commit_one(&sh->done[b]);
+                        mma_commit_one(&sh->empty[s.i]);
+                    }
                 }
-                mma_commit_one(&sh->done[b]);
-                mma_commit_one(&sh->empty[s.i]);
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
             parity ^= 1;
             s.next(F::kStages, kBufs);
         }
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0)
-            for (int i = 0; i < kBufs; ++i) mbar_arrive(&sh->ready[i]);  // nothing to read in the first round
+            for (int i = 0; i < kBufs; ++i) mbar_arrive(&sh->ready[0][i]);  // nothing to read in the first round
         for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
             const Item w = item_at(t, start, count, pre, E, blocks, kMaxCols);
             // swiglu: lanes 0-7 gate of channels 0-7, 8-15 their up, 16-23 gate of channels 8-15, ...
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
                 else add_groups<16, 2>(d, scale, acc);
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->ready[buf.i]);
+                if (lane == 0) mbar_arrive(&sh->ready[0][buf.i]);
                 buf.next(kBufs);
             }
             if (!ok) break;
@@ -557,13 +566,17 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
                     unpack_word<F::kSubtract>(v.w, p + i * 16 + 12);
                 }
                 tmem_st32(to + h * 32, p);
+                if (h == 3) {
+                    __syncwarp();  // every lane has its words
+                    if (lane == 0) mbar_arrive(&sh->empty[s.i]);
+                }
+                if (h % 2 == 1) {
+                    tmem_wait_st();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->ready[h / 2][b]);
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->empty[s.i]);
-            tmem_wait_st();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->ready[b]);
             parity ^= 1;
             s.next(F::kStages, kBufs);
         }
