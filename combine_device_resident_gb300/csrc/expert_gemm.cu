@@ -3,10 +3,12 @@
 //   y[r][n] = act( sum_k x[r][k] * w[e(r)][n][k] ),  the rows of expert e = rows [start_e, start_e + count_e)
 //
 // with start and count read on the device from the split arrays.  The weights
-// are the M side of the matrix instruction (128 channels per tile) and an
-// expert's rows the N side: N may be any multiple of 16 up to 256, so a group
-// of c rows costs ceil(c/16)*16 columns, not a multiple of 128, and a group of
-// a few rows streams the weights once with a narrow instruction.
+// are the M side of the matrix instruction (256 rows per tile) and an
+// expert's rows the N side: N may be any multiple of 32 up to 256, so a group
+// of c rows costs ceil(c/32)*32 columns, not a multiple of 128, and a group of
+// a few rows streams the weights once with a narrow instruction.  Many rows:
+// bound by the tensor pipe (90% active; 8 x 1,024 rows, 5120 -> 2 x 2048: 197-205 us,
+// 1.68-1.75 PFLOP/s); few: by the weights' bytes (16 experts with a row each: 76 us, 5.8 TB/s).
 //
 // One persistent pair of blocks per two SMs (a cluster, cta_group::2): each
 // block loads its 128 of the tile's 256 weight rows and half of its expert
@@ -37,7 +39,8 @@ constexpr int kTileN = 256;         // expert rows per tile, at most
 constexpr int kABytes = kTileM * kRowBytes;
 constexpr int kBBytes = kTileN / 2 * kRowBytes;  // half of them in each block
 // The ring: six stages for any tile; or, when no expert has more than 32 rows, ten whose row part holds just these:
-// such a call streams weights, and what an SM gets is what it has in flight.
+// such a call streams weights, and what an SM gets is what it has in flight (16 experts with a row each: 76 us
+// against 83 with the six).
 constexpr int kStageBytes = kABytes + kBBytes, kRingBytes = kStages * kStageBytes;
 constexpr int kFewRows = 32, kFewStageBytes = kABytes + kFewRows / 2 * kRowBytes, kFewStages = 10;
 static_assert(kFewStages * kFewStageBytes <= kRingBytes && kFewStageBytes % 1024 == 0, "one ring");
@@ -164,11 +167,12 @@ __device__ __forceinline__ Tile tile_at(long long t, const int32_t *start, const
     Tile r;
     r.e = lo;
     r.ctile = rem / wide;
-    // even shares, multiples of 32 rows (the last one takes what is left)
+    // even shares, multiples of 32 rows; the last one takes what is left, which is a row at least: rounding up adds at
+    // most 31 rows to a share, and nothing to the share of more than seven tiles (their mean is above 224, share 256)
     const int share = ((n + rt - 1) / rt + 31) / 32 * 32;
     const int first = (band * kBand + rem % wide) * share;
     r.row = start[lo] + first;
-    r.rows = max(0, min(share, n - first));
+    r.rows = min(share, n - first);
     return r;
 }
 
@@ -331,10 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 b ^= 1;
                 if (b == 0) acc_parity ^= 1;
             }
-            if (!ok) {  // given up: let the instructions that were issued end before TMEM is freed
-                if (elect_one()) mma_commit(&sh->drain);
-                mbar_wait_bounded(&sh->drain, 0);
-            }
+            // every instruction that was issued ends before TMEM is freed, also where an epilogue gave up
+            if (elect_one()) mma_commit(&sh->drain);
+            mbar_wait_bounded(&sh->drain, 0);
         }
     } else {
         // 32 columns at a time, the two warps of a quarter in turn
@@ -440,7 +443,7 @@ cudaError_t launch_gemm(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t 
     const cuuint64_t es = kFp8 ? 1 : 2, K = a.K, N = a.N, E = a.g.E, halves = kSwiglu ? 2 : 1;
     const cuuint32_t step = kRowBytes / (cuuint32_t)es;
     CUtensorMap mw;
-    RowMaps mx;
+    RowMaps mx{};
     // w as [E][N/8][gate, up][8][K]
     const cuuint64_t wd[5] = {K, 8, halves, N / 8, E};
     const cuuint64_t wst[4] = {K * es, N * K * es, 8 * K * es, halves * N * K * es};

@@ -23,13 +23,14 @@ constexpr int kMaxRows = 32;   // expert rows per work item
 // ---- few work items: K shared out among the warps -------------------------------
 //
 // A block of eight warps takes 16 weight rows; each warp takes every eighth
-// span of 256 of K through its own ring of TMA boxes (16 rows x 128 bytes), in flight across
-// work items too.  The pairs, less 136, are A fragments of the 16x8x16 matrix instruction,
+// span of 256 of K through its own ring of TMA boxes (16 rows x 128 bytes).
+// The pairs, less 136, are A fragments of the 16x8x16 matrix instruction,
 // whose legacy form is the right one here: the product needs 2 * rows flops
 // per weight, far below any tensor limit, and its operands come out of
 // registers.  The warps' partial sums meet in shared memory in a fixed order.
 // With one row the call is a chain of latencies (launch, places, first box,
-// rows, joining): 9.5 us for 21 million weights.  Loading rows and scales a
+// rows, joining): 8.0 us for 21 million weights (9.5 with a loop over items
+// in the kernel, which no call needs).  Loading rows and scales a
 // span ahead cost more instructions than it hid (11.7 us).
 constexpr int kRows = 16, kBoxBytes = kRows * 128;
 
@@ -152,25 +153,16 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
     grid_dependency_wait();
     const int total = place_experts<kThreads>(a, kMaxRows, start, count, pre, sh->warp_sum);  // ends in a barrier
     const int blocks = (a.N + kChan - 1) / kChan;
-    const long long items = (long long)total * blocks;
+    if (blockIdx.x >= (long long)total * blocks) return;
     const int spans = (a.K + kSpan - 1) / kSpan;
+    const Item w = item_at(blockIdx.x, start, count, pre, E, blocks, kMaxRows);
 
     uint8_t *mine = ring + warp * kStages * kBoxBytes;
-    // The warp's boxes in order: of item i of this block, spans (warp + i) % kWarps, + kWarps, ...; the
-    // rotation evens out a K whose spans do not divide by the warps.
-    long long put_t = blockIdx.x;
-    int put_i = 0, put_span = warp;
-    uint32_t put = 0, got = 0;  // boxes issued and consumed
+    int put_span = warp, put = 0, got = 0;  // boxes issued and consumed
     bool ok = true;
     auto issue = [&] {  // the next box of this warp, if there is one
-        while (put_t < items && put_span >= spans) {
-            put_t += gridDim.x;
-            ++put_i;
-            put_span = (warp + put_i) % kWarps;
-        }
-        if (put_t >= items) return;
+        if (put_span >= spans) return;
         if (lane == 0) {
-            const Item w = item_at(put_t, start, count, pre, E, blocks, kMaxRows);
             uint64_t *bar = &sh->full[warp][put % kStages];
             mbar_arrive_expect_tx(bar, kBoxBytes);
             asm volatile(
@@ -183,51 +175,45 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
         ++put;
     };
     for (int i = 0; i < kStages; ++i) issue();
-    int i = 0;
-    for (long long t = blockIdx.x; t < items; t += gridDim.x, ++i) {
-        const Item w = item_at(t, start, count, pre, E, blocks, kMaxRows);
-        float acc[4][4] = {};
-        for (int span = (warp + i) % kWarps; ok && span < spans; span += kWarps) {
-            const int at = got % kStages;
-            const bool in = mbar_wait_bounded(&sh->full[warp][at], (got / kStages) & 1, a.wait_polls);
-            ok = all_of(in);
-            if (!ok) break;
-            const uint32_t *box = reinterpret_cast<const uint32_t *>(mine + at * kBoxBytes);
-            if (w.rows <= 8) box_sums<1, kSwiglu>(box, a, w, span * kSpan, acc);
-            else if (w.rows <= 16) box_sums<2, kSwiglu>(box, a, w, span * kSpan, acc);
-            else box_sums<4, kSwiglu>(box, a, w, span * kSpan, acc);
-            ++got;
-            __syncwarp();  // every lane has read the box
-            issue();
-        }
-        if (!ok && lane == 0) {
-            sh->abort = 1;
-            atomicOr(a.status, kDevWaitTimeout);
-        }
-        const int g = lane >> 2, q = lane & 3;
-        float *p = parts + warp * kRows * (kMaxRows + 1);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-            if (n * 8 < w.rows) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) p[((c >> 1) * 8 + g) * (kMaxRows + 1) + n * 8 + q * 2 + (c & 1)] = acc[n][c];
-            }
-        __syncthreads();
-        if (*(volatile uint32_t *)&sh->abort == 0)
-            for (int o = tid; o < kChan * w.rows; o += kThreads) {
-                const int chan = o % kChan, r = o / kChan;
-                float sum = 0.0f, up = 0.0f;
-#pragma unroll
-                for (int v = 0; v < kWarps; ++v) {
-                    sum += parts[(v * kRows + chan) * (kMaxRows + 1) + r];
-                    if (kSwiglu) up += parts[(v * kRows + chan + 8) * (kMaxRows + 1) + r];
-                }
-                const float out = kSwiglu ? __fdividef(sum, 1.0f + __expf(-sum)) * up : sum;
-                const int n = w.block * kChan + chan;
-                if (n < a.N) a.y[(size_t)(w.row + r) * a.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
-            }
-        __syncthreads();
+    float acc[4][4] = {};
+    for (int span = warp; span < spans; span += kWarps) {
+        const int at = got % kStages;
+        ok = all_of(mbar_wait_bounded(&sh->full[warp][at], (got / kStages) & 1, a.wait_polls));
+        if (!ok) break;
+        const uint32_t *box = reinterpret_cast<const uint32_t *>(mine + at * kBoxBytes);
+        if (w.rows <= 8) box_sums<1, kSwiglu>(box, a, w, span * kSpan, acc);
+        else if (w.rows <= 16) box_sums<2, kSwiglu>(box, a, w, span * kSpan, acc);
+        else box_sums<4, kSwiglu>(box, a, w, span * kSpan, acc);
+        ++got;
+        __syncwarp();  // every lane has read the box
+        issue();
     }
+    if (!ok && lane == 0) {
+        sh->abort = 1;
+        atomicOr(a.status, kDevWaitTimeout);
+    }
+    const int g = lane >> 2, q = lane & 3;
+    float *p = parts + warp * kRows * (kMaxRows + 1);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        if (n * 8 < w.rows) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[((c >> 1) * 8 + g) * (kMaxRows + 1) + n * 8 + q * 2 + (c & 1)] = acc[n][c];
+        }
+    __syncthreads();
+    if (*(volatile uint32_t *)&sh->abort == 0)
+        for (int o = tid; o < kChan * w.rows; o += kThreads) {
+            const int chan = o % kChan, r = o / kChan;
+            float sum = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                sum += parts[(v * kRows + chan) * (kMaxRows + 1) + r];
+                if (kSwiglu) up += parts[(v * kRows + chan + 8) * (kMaxRows + 1) + r];
+            }
+            const float out = kSwiglu ? __fdividef(sum, 1.0f + __expf(-sum)) * up : sum;
+            const int n = w.block * kChan + chan;
+            if (n < a.N) a.y[(size_t)(w.row + r) * a.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
+        }
     if (!ok)  // given up: the boxes that were issued land before the block ends
         for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kStages], (got / kStages) & 1);
 }
@@ -248,10 +234,12 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 // The steps are short and the way round a buffer is long (barriers and latencies: some
 // 2000 cycles for a span of 256 of K, whose weights take 700 to arrive), so
 // each buffer has its own four unpacking warps and its own issuing warp (eight
-// warps with half a span each: 569 us against 535 on 1,024 rows, the waits being per warp),
-// and there are as many buffers as tensor memory holds.  (A barrier's
-// parity tells a waiter only that the last phase is over: whoever waits for
-// a buffer has to see every phase of it.)
+// warps with half a span each: 569 us against 535 on 1,024 rows, the waits
+// being per warp), and there are as many buffers as tensor memory holds.  (A
+// barrier's parity tells a waiter only that the last phase is over: whoever
+// waits for a buffer has to see every phase of it.)  1,024 rows on 256
+// experts, K = 7168, SwiGLU to 2048: 526 us, 4.8 TB/s of weights; next to HBM the ALU
+// pipe bounds it (65%), as seven of an unpacked word's operations run there at half rate.
 constexpr int kMaxCols = 16;                 // expert rows per work item: the instruction's N
 constexpr int kACols = kSpan / 2, kZeroCols = 8;  // 32-bit columns of a span's A, and of the constant one
 constexpr int kTileRows = 128;
@@ -262,7 +250,7 @@ constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16, twice
 template <int kPer>
 struct TmemForm {
     static constexpr int kGroups = 2 * kPer, kDCols = kGroups * kMaxCols;  // of a span
-    static constexpr int kBufs = kPer == 1 ? 3 : 2, kStages = kPer == 1 ? 6 : 8;
+    static constexpr int kBufs = kPer == 1 ? 3 : 2, kStages = kPer == 1 ? 6 : 8;  // (a multiple of the buffers)
     static constexpr bool kSubtract = kPer == 4;  // no columns left for the constant A: q - 8 is unpacked
     static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kBufs;  // warp 0 loads, 1 .. kBufs issue
     static constexpr int kThreads = (kFirstSum + 4) * 32;
@@ -444,8 +432,7 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
         s.i = b;
         uint32_t parity = 0;
         for (long long c = b; c < mine; c += kBufs) {
-            // (that the rows of x are there follows: the warps that filled A waited for the stage)
-            bool ok = true;
+            bool ok = all_of(wait_or_abort(&sh->full[s.i], s.parity, polls, &sh->abort, a.status));  // the rows
 #pragma unroll
             for (int half = 0; half < 2; ++half) {  // the first half's instructions run while the second is unpacked
                 ok = ok && all_of(wait_or_abort(&sh->ready[half][b], parity, polls, &sh->abort, a.status));
@@ -622,6 +609,12 @@ cudaError_t launch_w4_groups(const a2av_plan_s &p, const MatmulArgs &a, cudaStre
                            : launch_w4_tmem<kSwiglu, 1>(p, a, s);
 }
 
+// the most items of the split form that the call's rows can make
+long long split_items(const MatmulArgs &a, bool swiglu) {
+    const long long rows = a.rows_most, chans = swiglu ? kRows / 2 : kRows;
+    return ((rows < a.g.E ? rows : a.g.E) + rows / kMaxRows) * ((a.N + chans - 1) / chans);
+}
+
 template <bool kSwiglu>
 cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStream_t s) {
     constexpr int kChan = kSwiglu ? kRows / 2 : kRows;
@@ -636,21 +629,20 @@ cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStrea
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(expert_w4_kernel<kSwiglu>, allowed, p.cfg.device, split_smem_bytes(kMaxExperts));
     if (e != cudaSuccess) return e;
-    const long long rows = a.rows_most;
-    const long long most = ((rows < a.g.E ? rows : a.g.E) + rows / kMaxRows) * ((a.N + kChan - 1) / kChan);
-    const int grid = (int)(most < 2 * p.num_sms ? most : 2 * p.num_sms);
-    return launch_pdl(expert_w4_kernel<kSwiglu>, grid, kThreads, smem, s, m, a);
+    // (the caller has seen to it that there are no more items than blocks that fit at once)
+    return launch_pdl(expert_w4_kernel<kSwiglu>, (int)split_items(a, kSwiglu), kThreads, smem, s, m, a);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s) {
-    const long long rows = a.rows_most, experts = rows < a.g.E ? rows : a.g.E;
-    // Items of 128 weight rows the call can have: from a third of the SMs on, the form on tensor memory is the
-    // faster one (K = 5120, SwiGLU to 2048: one expert, 32 items, 14.6 us against 9.5; two, 64 items, 14.5 against
-    // 17.3; sixteen 40.6 against 96; K = 2048 to 5120: one expert, 40 items, 9.5 against 8.7).
-    const bool many = experts * (swiglu ? 2 : 1) * a.N / kTileRows >= p.num_sms / 3;
-    if (many) return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
+    // The split form while all its items (16 weight rows each) are resident at once, two to an SM; when some would have
+    // to wait for a turn the form on tensor memory is the faster one.  One row to 4096 (256 items): K = 2048 5.9 us
+    // split, 7.8 on tensor memory, 4096 8.6 and 11.3, 8192 14.3 and 18.1; to 5120 (320 items), K = 2048: 9.7 and 7.9;
+    // to 6144: K = 1024 8.9 and 6.2, 8192 25 and 18.  K = 5120, SwiGLU to 2048: one expert 7.9 and 13.1, two 15.1 and
+    // 13.4, sixteen 92 and 36.
+    if (split_items(a, swiglu) > 2 * p.num_sms)
+        return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
     return swiglu ? launch_w4_split<true>(p, a, s) : launch_w4_split<false>(p, a, s);
 }
 
