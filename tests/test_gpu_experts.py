@@ -291,6 +291,22 @@ def test_w4_many_items_in_fixed_windows():
     run_product("int4", counts, 256, 2568, True, group=64, window_rows=70)["plan"].close()
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("group,K", [(32, 8224), (64, 10304), (128, 18432)])
+def test_w4_few_items_of_long_rows(group, K, swiglu):
+    """K past what a warp's boxes in flight hold (four of 256, eight warps), so that every ring goes round."""
+    run_product("int4", [[1, 5, 0, 40]], K, 72, swiglu, group=group, seed=K)["plan"].close()
+
+
+@pytest.mark.parametrize("items", [-1, 0, 1])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_w4_around_the_change_of_form(swiglu, items):
+    """One expert whose items of 16 weight rows just fit on the SMs, two each, and one less and more."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    N = (2 * sms + items) * (8 if swiglu else 16)
+    run_product("int4", [[3]], 288, N, swiglu, seed=N)["plan"].close()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "int4"])
 def test_all_experts_empty_and_most_experts(kind):
     r = run_product(kind, np.zeros((4, 16), int), 64, 64, False)
