@@ -29,8 +29,8 @@ constexpr int kMaxRows = 32;   // expert rows per work item
 // per weight, far below any tensor limit, and its operands come out of
 // registers.  The warps' partial sums meet in shared memory in a fixed order.
 // With one row the call is a chain of latencies (launch, places, first box,
-// rows, joining): 8.0 us for 21 million weights (9.5 with a loop over items
-// in the kernel, which no call needs).  Loading rows and scales a
+// rows, joining): 8.1 us for 21 million weights.  (9.5 with the next item's
+// boxes asked for during this one's: two items of a block are rare.)  Loading rows and scales a
 // span ahead cost more instructions than it hid (11.7 us).
 constexpr int kRows = 16, kBoxBytes = kRows * 128;
 
@@ -153,55 +153,58 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
     grid_dependency_wait();
     const int total = place_experts<kThreads>(a, kMaxRows, start, count, pre, sh->warp_sum);  // ends in a barrier
     const int blocks = (a.N + kChan - 1) / kChan;
-    if (blockIdx.x >= (long long)total * blocks) return;
+    const long long items = (long long)total * blocks;
     const int spans = (a.K + kSpan - 1) / kSpan;
-    const Item w = item_at(blockIdx.x, start, count, pre, E, blocks, kMaxRows);
-
     uint8_t *mine = ring + warp * kStages * kBoxBytes;
-    int put_span = warp, put = 0, got = 0;  // boxes issued and consumed
+    int put = 0, got = 0;  // boxes issued and consumed
     bool ok = true;
-    auto issue = [&] {  // the next box of this warp, if there is one
-        if (put_span >= spans) return;
-        if (lane == 0) {
-            uint64_t *bar = &sh->full[warp][put % kStages];
-            mbar_arrive_expect_tx(bar, kBoxBytes);
-            asm volatile(
-                "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-                "%5}], [%6];" ::"r"(smem_u32(mine + put % kStages * kBoxBytes)),
-                "l"(&map_w), "r"(put_span * (kSpan / 8)), "r"(w.block * kChan), "r"(0), "r"(w.e), "r"(smem_u32(bar))
-                : "memory");
+    // (one item a block, unless the splits hold more rows than the plan's tokens make)
+    for (long long t = blockIdx.x; t < items; t += gridDim.x) {
+        const Item w = item_at(t, start, count, pre, E, blocks, kMaxRows);
+        int put_span = warp;
+        auto issue = [&] {  // the next box of this warp, if there is one
+            if (put_span >= spans) return;
+            if (lane == 0) {
+                uint64_t *bar = &sh->full[warp][put % kStages];
+                mbar_arrive_expect_tx(bar, kBoxBytes);
+                asm volatile(
+                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+                    "%5}], [%6];" ::"r"(smem_u32(mine + put % kStages * kBoxBytes)),
+                    "l"(&map_w), "r"(put_span * (kSpan / 8)), "r"(w.block * kChan), "r"(0), "r"(w.e),
+                    "r"(smem_u32(bar))
+                    : "memory");
+            }
+            put_span += kWarps;
+            ++put;
+        };
+        for (int i = 0; i < kStages; ++i) issue();
+        float acc[4][4] = {};
+        for (int span = warp; ok && span < spans; span += kWarps) {
+            const int at = got % kStages;
+            ok = all_of(mbar_wait_bounded(&sh->full[warp][at], (got / kStages) & 1, a.wait_polls));
+            if (!ok) break;
+            const uint32_t *box = reinterpret_cast<const uint32_t *>(mine + at * kBoxBytes);
+            if (w.rows <= 8) box_sums<1, kSwiglu>(box, a, w, span * kSpan, acc);
+            else if (w.rows <= 16) box_sums<2, kSwiglu>(box, a, w, span * kSpan, acc);
+            else box_sums<4, kSwiglu>(box, a, w, span * kSpan, acc);
+            ++got;
+            __syncwarp();  // every lane has read the box
+            issue();
         }
-        put_span += kWarps;
-        ++put;
-    };
-    for (int i = 0; i < kStages; ++i) issue();
-    float acc[4][4] = {};
-    for (int span = warp; span < spans; span += kWarps) {
-        const int at = got % kStages;
-        ok = all_of(mbar_wait_bounded(&sh->full[warp][at], (got / kStages) & 1, a.wait_polls));
-        if (!ok) break;
-        const uint32_t *box = reinterpret_cast<const uint32_t *>(mine + at * kBoxBytes);
-        if (w.rows <= 8) box_sums<1, kSwiglu>(box, a, w, span * kSpan, acc);
-        else if (w.rows <= 16) box_sums<2, kSwiglu>(box, a, w, span * kSpan, acc);
-        else box_sums<4, kSwiglu>(box, a, w, span * kSpan, acc);
-        ++got;
-        __syncwarp();  // every lane has read the box
-        issue();
-    }
-    if (!ok && lane == 0) {
-        sh->abort = 1;
-        atomicOr(a.status, kDevWaitTimeout);
-    }
-    const int g = lane >> 2, q = lane & 3;
-    float *p = parts + warp * kRows * (kMaxRows + 1);
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-        if (n * 8 < w.rows) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) p[((c >> 1) * 8 + g) * (kMaxRows + 1) + n * 8 + q * 2 + (c & 1)] = acc[n][c];
+        if (!ok && lane == 0) {
+            sh->abort = 1;
+            atomicOr(a.status, kDevWaitTimeout);
         }
-    __syncthreads();
-    if (*(volatile uint32_t *)&sh->abort == 0)
+        const int g = lane >> 2, q = lane & 3;
+        float *p = parts + warp * kRows * (kMaxRows + 1);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (n * 8 < w.rows) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) p[((c >> 1) * 8 + g) * (kMaxRows + 1) + n * 8 + q * 2 + (c & 1)] = acc[n][c];
+            }
+        __syncthreads();
+        if (*(volatile uint32_t *)&sh->abort) break;  // the same for every thread: nobody sets it before the next item
         for (int o = tid; o < kChan * w.rows; o += kThreads) {
             const int chan = o % kChan, r = o / kChan;
             float sum = 0.0f, up = 0.0f;
@@ -214,8 +217,10 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
             const int n = w.block * kChan + chan;
             if (n < a.N) a.y[(size_t)(w.row + r) * a.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
         }
-    if (!ok)  // given up: the boxes that were issued land before the block ends
-        for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kStages], (got / kStages) & 1);
+        __syncthreads();  // the sums are read
+    }
+    // given up: the boxes that were issued land before the block ends
+    for (; got < put; ++got) mbar_wait_bounded(&sh->full[warp][got % kStages], (got / kStages) & 1);
 }
 
 // ---- many work items: tensor memory ---------------------------------------------
@@ -629,7 +634,7 @@ cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStrea
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(expert_w4_kernel<kSwiglu>, allowed, p.cfg.device, split_smem_bytes(kMaxExperts));
     if (e != cudaSuccess) return e;
-    // (the caller has seen to it that there are no more items than blocks that fit at once)
+    // (the caller has seen to it that so many blocks fit at once)
     return launch_pdl(expert_w4_kernel<kSwiglu>, (int)split_items(a, kSwiglu), kThreads, smem, s, m, a);
 }
 

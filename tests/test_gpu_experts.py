@@ -298,6 +298,16 @@ def test_w4_few_items_of_long_rows(group, K, swiglu):
     run_product("int4", [[1, 5, 0, 40]], K, 72, swiglu, group=group, seed=K)["plan"].close()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int4"])
+@pytest.mark.parametrize("N", [72, 5128])
+def test_more_live_rows_than_the_plan_has_tokens(kind, N, monkeypatch):
+    """Splits of another plan's dispatch: every live row is computed, whatever the launch was sized for."""
+    counts = np.array([[70, 0, 21, 1]])
+    monkeypatch.setitem(globals(), "plan_for", lambda c, order, rows: A.Plan(
+        1, 4, 1, 64, 1, device=DEV, window_mode="fixed", window_rows=rows, recv_order=order))
+    run_product(kind, counts, 544, N, False, window_rows=96, seed=N)["plan"].close()
+
+
 @pytest.mark.parametrize("items", [-1, 0, 1])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_w4_around_the_change_of_form(swiglu, items):
