@@ -135,8 +135,7 @@ __device__ __forceinline__ void mma_commit_one(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-// kCols columns of this warp's 32 lanes into registers, which hold them after tmem_wait_ld; eight columns of one
-// value, and 32 columns, out of them.
+// kCols columns of this warp's 32 lanes into registers, which hold them after tmem_wait_ld; 32 columns out of them.
 template <int kCols>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[kCols]) {
     static_assert(kCols == 4 || kCols == 8 || kCols == 16, "columns");
@@ -163,10 +162,6 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[kLoads][kCols]) {
     for (int i = 0; i < kLoads; ++i)
 #pragma unroll
         for (int n = 0; n < kCols; ++n) asm volatile("" : "+f"(v[i][n]));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, uint32_t r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%1], {%0,%0,%0,%0,%0,%0,%0,%0};" ::"r"(r), "r"(addr)
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile(

@@ -5,7 +5,10 @@
 // Bound by the weights' bytes (half a byte each), so everything is arranged
 // around streaming them; no weight is rounded, as each group's sum is scaled in
 // fp32.  A word of eight 4-bit weights gives four bf16 pairs by a mask and an
-// or each: q | 0x4300 is 128 + q.  There are two forms: one that shares K out among the
+// or each: q | 0x4300 is 128 + q, and 136 less is q - 8, exactly.  The 136 comes off before the
+// product: behind it, every partial sum would carry 136 times the row's values and round
+// to that, so that an activation of 1e4 on a weight of zero costs a bf16 step.  There are two
+// forms: one that shares K out among the
 // warps of a block, for calls with so few weight blocks that a block has to take
 // little, and one on tensor memory.
 #include <cuda_bf16.h>
@@ -40,16 +43,10 @@ struct Shared4 {
     int32_t warp_sum[kWarps];
 };
 
-// Bits i*4 and 16+i*4 of a word: 128 + q of k = 2i and 2i+1 as bf16.
-__device__ __forceinline__ uint32_t raw_pair(uint32_t w, int i) {
+// Bits i*4 and 16+i*4 of a word: q - 8 of k = 2i and 2i+1 as bf16.
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
     uint32_t v;
     asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w >> (4 * i)));  // (w & mask) | 128.0
-    return v;
-}
-
-// The same minus 136: q - 8.
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
-    const uint32_t v = raw_pair(w, i);
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
                                      __nv_bfloat162{__float2bfloat16(136.0f), __float2bfloat16(136.0f)});
     return *reinterpret_cast<const uint32_t *>(&d);
@@ -231,9 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 // take its A operand from: lane = weight row, column = two of K, the very
 // order in which a word gives its pairs, so a thread reads 16-byte pieces of its own
 // row and no unpacked weight touches shared memory.  (At N = 16 the instruction then takes 10
-// cycles, against 40 with A in shared memory.)  The pairs are 128 + q; a second
-// instruction with a constant A of -136 takes the 128 and the 8 off inside the
-// accumulator, exact products in fp32 sums.  Each group of K has its own
+// cycles, against 40 with A in shared memory.)  Each group of K has its own
 // accumulator columns, and four warps scale them into fp32 sums in registers.
 //
 // The steps are short and the way round a buffer is long (barriers and latencies: some
@@ -243,24 +238,22 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 // being per warp), and there are as many buffers as tensor memory holds.  (A
 // barrier's parity tells a waiter only that the last phase is over: whoever
 // waits for a buffer has to see every phase of it.)  1,024 rows on 256
-// experts, K = 7168, SwiGLU to 2048: 526 us, 4.8 TB/s of weights; next to HBM the ALU
+// experts, K = 7168, SwiGLU to 2048: 540 us, 4.6 TB/s of weights (525 with the 136 taken off by
+// a second instruction, see above); next to HBM the ALU
 // pipe bounds it (65%), as seven of an unpacked word's operations run there at half rate.
 constexpr int kMaxCols = 16;                 // expert rows per work item: the instruction's N
-constexpr int kACols = kSpan / 2, kZeroCols = 8;  // 32-bit columns of a span's A, and of the constant one
+constexpr int kACols = kSpan / 2;            // 32-bit columns of a span's A
 constexpr int kTileRows = 128;
 constexpr int kWBytes = kTileRows * 128, kXBox = kMaxCols * 128, kStage = kWBytes + kSpan / 64 * kXBox;
-constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16, twice
 
 // For kPer groups of K per 128.
 template <int kPer>
 struct TmemForm {
     static constexpr int kGroups = 2 * kPer, kDCols = kGroups * kMaxCols;  // of a span
     static constexpr int kBufs = kPer == 1 ? 3 : 2, kStages = kPer == 1 ? 6 : 8;  // (a multiple of the buffers)
-    static constexpr bool kSubtract = kPer == 4;  // no columns left for the constant A: q - 8 is unpacked
     static constexpr int kFirstUnpack = 4, kFirstSum = kFirstUnpack + 4 * kBufs;  // warp 0 loads, 1 .. kBufs issue
     static constexpr int kThreads = (kFirstSum + 4) * 32;
-    static constexpr int kZeroAt = kBufs * (kACols + kDCols);  // column
-    static_assert(kZeroAt + (kSubtract ? 0 : kZeroCols) <= 512, "tensor memory");
+    static_assert(kBufs * (kACols + kDCols) <= 512, "tensor memory");
     static_assert(kStages % kBufs == 0, "every waiter sees every phase of its stages");
 };
 constexpr int kMaxStages = 8, kMaxBufs = 3;
@@ -293,10 +286,9 @@ struct Ring {
 };
 
 // Eight weights of a word as four bf16 pairs, k ascending.
-template <bool kSubtract>
 __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = kSubtract ? pair_of(w, i) : raw_pair(w, i);
+    for (int i = 0; i < 4; ++i) p[i] = pair_of(w, i);
 }
 
 // The bf16 scales of groups at .. at + kGroups - 1 of a weight row, in pairs; zeros behind the last. In one load
@@ -377,7 +369,7 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
     tmem_fence_before();
     const int total = place_experts<F::kThreads>(a, kMaxCols, start, count, pre, sh->warp_sum);  // ends in a barrier
     tmem_fence_after();
-    const uint32_t tmem = sh->tmem, d0 = tmem + kBufs * kACols, zero = tmem + F::kZeroAt;
+    const uint32_t tmem = sh->tmem, d0 = tmem + kBufs * kACols;
     const int blocks = (a.N + kChan - 1) / kChan;
     const long long items = (long long)total * blocks;
     const int spans = (a.K + kSpan - 1) / kSpan;
@@ -449,7 +441,6 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
                     for (int j = half * (kSteps / 2); j < (half + 1) * (kSteps / 2); ++j) {
                         const uint64_t bd = operand_desc(rows + j / 4 * kXBox) + j % 4 * 2;
                         mma_tmem(d + j / kPerGroup * kMaxCols, at + j * 8, bd, kIdesc, j % kPerGroup != 0);
-                        if (!F::kSubtract) mma_tmem(d + j / kPerGroup * kMaxCols, zero, bd, kIdesc, true);
                     }
                     if (half == 1) {
                         mma_commit_one(&sh->done[b]);
@@ -472,12 +463,6 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
         const bool aligned = groups % kGroups == 0 && reinterpret_cast<uintptr_t>(a.w_scale) % 16 == 0;
         Ring buf(0);
         bool ok = true;
-        if (!F::kSubtract) {
-            tmem_st8(zero + lanes, kMinus136);
-            tmem_wait_st();
-            tmem_fence_before();
-        }
-        __syncwarp();
         if (lane == 0)
             for (int i = 0; i < kBufs; ++i) mbar_arrive(&sh->ready[0][i]);  // nothing to read in the first round
         for (long long t = blockIdx.x; ok && t < items; t += gridDim.x) {
@@ -550,12 +535,11 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
                 uint32_t p[32];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint4 v =
-                        *reinterpret_cast<const uint4 *>(words + (((h * 2 + i) ^ (row & 7)) << 4));
-                    unpack_word<F::kSubtract>(v.x, p + i * 16);
-                    unpack_word<F::kSubtract>(v.y, p + i * 16 + 4);
-                    unpack_word<F::kSubtract>(v.z, p + i * 16 + 8);
-                    unpack_word<F::kSubtract>(v.w, p + i * 16 + 12);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(words + (((h * 2 + i) ^ (row & 7)) << 4));
+                    unpack_word(v.x, p + i * 16);
+                    unpack_word(v.y, p + i * 16 + 4);
+                    unpack_word(v.z, p + i * 16 + 8);
+                    unpack_word(v.w, p + i * 16 + 12);
                 }
                 tmem_st32(to + h * 32, p);
                 if (h == 3) {

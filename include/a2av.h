@@ -379,8 +379,9 @@ a2av_status_t a2av_quantize_rows(a2av_plan_t plan, const void *x, int32_t K, con
  * A2AV_ACT_SWIGLU; weights and scales as for weight_type above.
  *   A2AV_W_BF16: K % 8 == 0; w_scale NULL.
  *   A2AV_W_E4M3: K % 16 == 0; the sum is scaled by w_scale[e][n] and the row's scale.
- *   A2AV_W_INT4: `group` is 32, 64 or 128 and K % group == 0; each group's sum is scaled in
- *                fp32; for few rows per expert (decode): weights are unpacked again for every
+ *   A2AV_W_INT4: `group` is 32, 64 or 128 and K % group == 0; each group's sum of
+ *                (q - 8) * x is taken and scaled in fp32 (and so has to lie in its
+ *                range, before the scale); for few rows per expert (decode): weights are unpacked again for every
  *                16 rows of an expert (32 in calls of few weight rows).
  * N % 8 == 0; K and N at most 2^18; x, w and y 16-byte aligned; y overlaps neither x nor w.
  * [Figure 13: the received tokens go on to their experts; the pages do not
