@@ -94,6 +94,14 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, lo
     return false;
 }
 
+// g / (1 + exp(-g)) * u.  The power is exp(-|g|), at most 1, so that the divisor lies between 1 and 2: with exp(-g) it
+// grows past 2^126 at gates below -87.3, where the fast division gives 0.  Both are the fast forms, some
+// (5 + 1.2 |g|) * 2^-23 off, far below the bf16 the result is rounded to.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g >= 0.0f ? g : g * e, 1.0f + e) * u;
+}
+
 // One answer for the warp.
 __device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
 

@@ -391,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 8);
                         const float g = up ? other : v[i], u = up ? v[i + 1] : other;
                         const int row = c + i + (up ? 1 : 0);
-                        const float out = __fdividef(g, 1.0f + __expf(-g)) * u;
+                        const float out = swiglu(g, u);
                         if (store && row < w.rows)
                             y[(size_t)row * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
                     }

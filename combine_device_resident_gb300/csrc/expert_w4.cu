@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
                 sum += parts[(v * kRows + chan) * (kMaxRows + 1) + r];
                 if (kSwiglu) up += parts[(v * kRows + chan + 8) * (kMaxRows + 1) + r];
             }
-            const float out = kSwiglu ? __fdividef(sum, 1.0f + __expf(-sum)) * up : sum;
+            const float out = kSwiglu ? swiglu(sum, up) : sum;
             const int n = w.block * kChan + chan;
             if (n < a.N) a.y[(size_t)(w.row + r) * a.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
         }
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
                     const float other = __shfl_xor_sync(0xffffffffu, up ? acc[n] : acc[n + 1], 8);
                     const float g = up ? other : acc[n], u = up ? acc[n + 1] : other;
                     const int r = n + (up ? 1 : 0);
-                    const float out = __fdividef(g, 1.0f + __expf(-g)) * u;
+                    const float out = swiglu(g, u);
                     if (chan < a.N && r < w.rows)
                         y[(size_t)r * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
                 }

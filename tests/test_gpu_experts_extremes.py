@@ -95,3 +95,73 @@ def test_w4_infinite_rows(N, group):
     for e, a, b in segs:
         rows = [r for r in range(a, b) if r not in (2, 30)]
         within(y[rows], *product_ref("int4", x[rows].double(), w64[e], ws, False, K))
+
+
+# ---- the activation far out ------------------------------------------------------------
+
+FORMS = [("bf16", 8), ("e4m3", 8), ("int4", 8), ("int4", 3600)]  # 4-bit weights: either form, by the width
+
+
+def gated(kind, N, gates, up):
+    """y [len(gates)][N] of one expert whose gate is gates[r] in row r and whose up is `up`, both exact."""
+    n, K = len(gates), 64
+    plan = A.Plan(1, 1, n, 64, 1, device=DEV, recv_order="expert")
+    sp, _ = layout(plan, np.array([[n]]))
+    x = torch.zeros(n, K, device=DEV)
+    x[:, 0], x[:, 1] = torch.tensor(gates, device=DEV), up
+    w = torch.zeros(1, 2 * N, K, device=DEV)
+    w[0, :N, 0], w[0, N:, 1] = 1.0, 1.0
+    y = torch.full((n, N), CANARY, device=DEV, dtype=torch.bfloat16)
+    if kind == "bf16":
+        plan.expert_matmul(x.bfloat16(), w.bfloat16(), sp, y, activation="swiglu")
+    elif kind == "e4m3":  # a scale of 8 for the row holds a gate and an up of up to 3584 in steps of theirs
+        rows8 = plan.new_rows8(n, K)
+        q, s = A.rows8_parts(rows8)
+        s.fill_(8.0)
+        q.copy_((x / 8.0).to(torch.float8_e4m3fn))
+        assert torch.equal(q.float() * 8.0, x)
+        plan.expert_matmul(rows8, w.to(torch.float8_e4m3fn), sp, y, w_scale=torch.ones(1, 2 * N, device=DEV),
+                           activation="swiglu")
+    else:
+        words = torch.zeros(1, 2 * N, K // 8, dtype=torch.int32, device=DEV)
+        words[...] = -0x77777778  # eight eights: weights of zero
+        words[0, :N, 0] += 1        # k = 0: 9 - 8
+        words[0, N:, 0] += 1 << 16  # k = 1
+        assert torch.equal(A.unpack_weights_w4(words, torch.ones(1, 2 * N, 1, device=DEV)), w)
+        plan.expert_matmul_w4(x.bfloat16(), words, torch.ones(1, 2 * N, 1, device=DEV, dtype=torch.bfloat16), sp, y,
+                              activation="swiglu")
+    torch.cuda.synchronize()
+    assert plan.read_status() == 0
+    plan.close()
+    return y
+
+
+@pytest.mark.parametrize("kind,N", FORMS)
+def test_gates_far_out(kind, N):
+    """silu is g exp(g) there, down to where bf16 ends: fp32's exp and division are (8 + 2|g|) * 2^-23 off, half a step
+    of a bf16 below its smallest normal is 2^-134, and below fp32's the power is a step of 2^-149 off, times g and the
+    up."""
+    gates = [-72.0, -80.0, -88.0, -96.0, -104.0, 72.0, 88.0, 96.0, 104.0, 2048.0, -2048.0, 8.0, -8.0, 0.0]
+    y = gated(kind, N, gates, 64.0).double()
+    g = torch.tensor(gates, device=DEV, dtype=torch.float64)
+    ref = (g / (1.0 + torch.exp(-g)) * 64.0).unsqueeze(-1).expand_as(y)
+    rel = (BF + (8 + 2 * g.abs()) * 2.0 ** -23).unsqueeze(-1)
+    within(y, ref, ref.abs() * rel + 2.0 ** -134 + ((g.abs() + 2) * 64 * 2.0 ** -149).unsqueeze(-1))
+
+
+@pytest.mark.parametrize("kind,N", [f for f in FORMS if f[0] != "e4m3"])  # 8-bit rows hold no such pair exactly
+def test_overflowing_sums_stay_infinite(kind, N):
+    """A product past fp32 is an infinity of its sign, not a NaN (gate 2048, up 2^126)."""
+    big = 2.0 ** 126
+    y = gated(kind, N, [2048.0, -2048.0, 8.0, -1.0], big).double()
+    assert (y[0] == float("inf")).all() and (y[1] == 0).all() and (y[2] == float("inf")).all()
+    ref = torch.full((N,), -1.0 / (1.0 + np.exp(1.0)) * big, dtype=torch.float64, device=DEV)
+    within(y[3], ref, ref.abs() * (BF + 10 * 2.0 ** -23))
+
+
+@pytest.mark.parametrize("kind,N", FORMS)
+def test_a_large_gate_is_the_gate(kind, N):
+    y = gated(kind, N, [704.0, 960.0, 112.0, -112.0], 8.0).double()
+    for row, want in ((0, 704.0 * 8), (1, 960.0 * 8), (2, 112.0 * 8)):
+        within(y[row], torch.full_like(y[row], want), torch.full_like(y[row], want * (BF + 2.0 ** -20)))
+    assert (y[3].abs() < 1e-37).all()
