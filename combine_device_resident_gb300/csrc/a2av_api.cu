@@ -535,7 +535,11 @@ a2av_status_t a2av_expert_matmul(a2av_plan_t p, const void *x, const void *w, co
     const size_t w_bytes = (size_t)p->g.E * N * (swiglu ? 2 : 1) * K /
                            (weight_type == A2AV_W_INT4 ? 2 : 1) * (weight_type == A2AV_W_BF16 ? 2 : 1);
     const size_t y_bytes = (size_t)rows * N * 2;
-    if (overlap(y, y_bytes, x, (size_t)rows * pitch) || overlap(y, y_bytes, w, w_bytes))
+    const size_t scale_bytes = !scaled ? 0
+                               : (size_t)p->g.E * N * (swiglu ? 2 : 1) *
+                                     (weight_type == A2AV_W_INT4 ? (size_t)(K / group) * 2 : 4);
+    if (overlap(y, y_bytes, x, (size_t)rows * pitch) || overlap(y, y_bytes, w, w_bytes) ||
+        (scaled && overlap(y, y_bytes, w_scale, scale_bytes)))
         return refuse("a2av_expert_matmul: y overlaps an input");
     DeviceGuard guard(p->cfg.device);
     if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");

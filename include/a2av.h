@@ -383,7 +383,7 @@ a2av_status_t a2av_quantize_rows(a2av_plan_t plan, const void *x, int32_t K, con
  *                (q - 8) * x is taken and scaled in fp32 (and so has to lie in its
  *                range, before the scale); for few rows per expert (decode): weights are unpacked again for every
  *                16 rows of an expert (32 in calls of few weight rows).
- * N % 8 == 0; K and N at most 2^18; x, w and y 16-byte aligned; y overlaps neither x nor w.
+ * N % 8 == 0; K and N at most 2^18; x, w and y 16-byte aligned; y overlaps none of x, w and w_scale.
  * [Figure 13: the received tokens go on to their experts; the pages do not
  * define the experts.] */
 a2av_status_t a2av_expert_matmul(a2av_plan_t plan, const void *x, const void *w, const void *w_scale, void *y,

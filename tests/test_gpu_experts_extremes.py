@@ -165,3 +165,32 @@ def test_a_large_gate_is_the_gate(kind, N):
     for row, want in ((0, 704.0 * 8), (1, 960.0 * 8), (2, 112.0 * 8)):
         within(y[row], torch.full_like(y[row], want), torch.full_like(y[row], want * (BF + 2.0 ** -20)))
     assert (y[3].abs() < 1e-37).all()
+
+
+# ---- refusals --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["e4m3", "int4"])
+@pytest.mark.parametrize("at", ["first", "last"])
+def test_output_over_the_weights_scales_is_refused(kind, at):
+    """The scales are read while other blocks store y."""
+    plan = A.Plan(1, 2, 16, 64, 1, device=DEV, recv_order="expert")
+    sp, _ = layout(plan, np.array([[9, 7]]))
+    K, N, rows = 64, 32, plan.arena_rows
+    size = 2 * N * (4 if kind == "e4m3" else K // 32 * 2)
+    buf = torch.zeros(size + rows * N * 2, dtype=torch.uint8, device=DEV)
+    # y covers the first or the last 16 bytes of the scales
+    y0 = buf.numel() - rows * N * 2 if at == "last" else 0
+    y = buf[y0:y0 + rows * N * 2].view(torch.bfloat16).view(rows, N)
+    s0 = y0 - size + 16 if at == "last" else rows * N * 2 - 16
+    scales = buf[s0:s0 + size]
+    if kind == "e4m3":
+        w = torch.zeros(2, N, K, device=DEV).to(torch.float8_e4m3fn)
+        call = lambda: plan.expert_matmul(plan.new_rows8(rows, K), w, sp, y, w_scale=scales.view(torch.float32).view(2, N))
+    else:
+        w = torch.zeros(2, N, K // 8, dtype=torch.int32, device=DEV)
+        x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+        call = lambda: plan.expert_matmul_w4(x, w, scales.view(torch.bfloat16).view(2, N, K // 32), sp, y)
+    with pytest.raises(A.A2avError, match="overlaps"):
+        call()
+    assert plan.launches == 0
+    plan.close()
