@@ -213,17 +213,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sh->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    }
     if (tid == 64) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
         for (int i = 0; i < row_boxes(a); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x.box[i]));
     }
     grid_dependency_wait();
 
+    // Tensor memory is taken after the wait: the kernel before may take its own late, and this one may start early.
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
     tmem_fence_before();
     const int total = place_experts<kThreads>(a, kTileN, start, count, pre, sh->warp_sum);  // ends in a barrier
     bool more_rows = false;

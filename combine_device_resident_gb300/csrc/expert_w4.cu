@@ -364,8 +364,9 @@ __global__ void __launch_bounds__(TmemForm<kPer>::kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w));
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x));
     }
-    if (warp == 1) tmem_alloc_all(&sh->tmem);
     grid_dependency_wait();
+    // Tensor memory is taken after the wait: the kernel before may take its own late, and this one may start early.
+    if (warp == 1) tmem_alloc_all(&sh->tmem);
     tmem_fence_before();
     const int total = place_experts<F::kThreads>(a, kMaxCols, start, count, pre, sh->warp_sum);  // ends in a barrier
     tmem_fence_after();

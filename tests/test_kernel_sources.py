@@ -1,0 +1,24 @@
+"""Orders in the kernels' sources that no run can show without hanging."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "combine_device_resident_gb300", "csrc")
+
+
+def kernels():
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith(".cu"):
+            for body in open(os.path.join(CSRC, name)).read().split("__global__")[1:]:
+                yield name, re.search(r"(\w+_kernel)\(", body).group(1), body
+
+
+def test_tensor_memory_is_taken_after_the_dependency_wait():
+    """A kernel that starts early and takes tensor memory before it waits can leave its predecessor, whose blocks may
+    take theirs later, without any: each would wait for the other."""
+    found = []
+    for name, kernel, body in kernels():
+        alloc = min((body.find(t) for t in ("tcgen05.alloc", "tmem_alloc_all(") if t in body), default=-1)
+        if alloc >= 0:
+            found.append(kernel)
+            assert 0 <= body.find("grid_dependency_wait();") < alloc, (name, kernel)
+    assert sorted(found) == ["expert_gemm_kernel", "expert_w4_tmem_kernel"]
