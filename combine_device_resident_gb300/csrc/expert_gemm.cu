@@ -418,7 +418,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Given up (both blocks know: the flag is set in both before this
         // barrier).  The block that is behind issues the loads the other has
         // issued, so that every fill is whole, and the first block waits for
-        // them to land: the last fill of each stage.
+        // them to land: the last fill of each stage.  And the second block waits
+        // for what the first one's instructions still send to its barriers: one
+        // more arrival, behind theirs.
         if (warp == 0) {
             produce(false, *(volatile uint32_t *)&sh->other_fills);
             for (int i = 0; rank == 0 && i < ring; ++i) {
@@ -429,6 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (fills-- > 0) mbar_wait_bounded(&sh->full[put_s], put_parity ^ 1);
                 else break;
             }
+        } else if (warp == 1) {
+            if (rank == 0 && elect_one()) mma_commit_both(&sh->drain);
+            mbar_wait_bounded(&sh->drain, rank ^ 1);  // the first block's second phase, the other's first
         }
         __syncwarp();
         cluster_sync();

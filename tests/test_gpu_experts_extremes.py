@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import combine_device_resident_gb300 as A
-from tests.test_gpu_experts import BF, CANARY, DEV, gen, layout, normal, plan_for, product_ref, within
+from tests.test_gpu_experts import BF, CANARY, DEV, gen, layout, normal, plan_for, product_ref, run_product, within
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,36 @@ def test_output_over_the_weights_scales_is_refused(kind, at):
         call()
     assert plan.launches == 0
     plan.close()
+
+
+# ---- waits that run out ----------------------------------------------------------------
+
+def gives_up_in_order(r, polls, K, swiglu):
+    """With few polls a call ends, right or with its status bit; the next one, with the default, is right."""
+    plan = r["plan"]
+    plan.set_wait_limit(polls)
+    for _ in range(3):
+        r["call"]()
+        status = plan.read_status(clear=True)
+        assert status == A.DEV_WAIT_TIMEOUT or (polls > 0 and status == 0)
+    plan.set_wait_limit(-1)
+    r["y"].fill_(CANARY)
+    r["call"]()
+    assert plan.read_status() == 0
+    for e, a, b in r["segs"]:
+        within(r["y"][a:b], *product_ref(None, r["x64"][a:b], r["w64"][e], None, swiglu, K))
+    plan.close()
+
+
+@pytest.mark.parametrize("polls", [0, 1, 2, 3, 10, 100])
+@pytest.mark.parametrize("counts", [[[0, 1030, 3, 2305]], [[1, 32, 0, 17]]], ids=["six stages", "ten stages"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_pairs_give_up_in_order(kind, counts, polls):
+    """Rings that go round, blocks of a pair that stop at different fills."""
+    gives_up_in_order(run_product(kind, counts, 2576, 264, True, seed=polls), polls, 2576, True)
+
+
+@pytest.mark.parametrize("polls", [0, 1, 2, 3, 10])
+@pytest.mark.parametrize("K,swiglu", [(18432, False), (1024, True)])
+def test_the_4bit_split_form_gives_up_in_order(K, swiglu, polls):
+    gives_up_in_order(run_product("int4", [[1, 5, 0, 40]], K, 72, swiglu, group=64, seed=polls), polls, K, swiglu)
