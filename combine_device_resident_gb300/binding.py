@@ -9,10 +9,9 @@ library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
-
-import torch
 
 from . import build as _build
 
@@ -212,17 +211,29 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-# The current stream's handle by device ordinal: torch's own short way where it has one (making a
-# Stream object takes longer than a small kernel).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+@functools.cache
+def _torch():
+    """torch, which the package imports without.  (An import statement takes about as long as a check of an argument;
+    this, in the calls where that counts, does not.)"""
+    import torch
+
+    return torch
+
+
+def _raw_stream(index):
+    """The current stream's handle by device ordinal: torch's own short way where it has one (making a
+    Stream object takes longer than a small kernel)."""
+    torch = _torch()
+    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return short(index) if short else torch.cuda.current_stream(index).cuda_stream
 
 
 def _width(t, name):
-    """Length of a tensor's last dimension."""
-    if not isinstance(t, torch.Tensor) or t.dim() < 1:
+    """Length of a tensor's last dimension (what else it has to be, ``_p`` checks)."""
+    shape = getattr(t, "shape", None)
+    if not shape:
         raise A2avError(f"{name} must be a torch tensor with at least one dimension")
-    return t.shape[-1]
+    return shape[-1]
 
 
 class Plan:
@@ -413,6 +424,8 @@ class Plan:
     def new_rows8(self, rows, K):
         """Zeroed 8-bit rows [rows][K+16] (uint8; `rows` a number or a leading
         shape): K e4m3 values, the fp32 scale, padding (``rows8_parts``)."""
+        import torch
+
         lead = (int(rows),) if isinstance(rows, int) else tuple(rows)
         return torch.zeros(lead + (int(K) + ROW8_TAIL,), dtype=torch.uint8, device=self.device)
 
@@ -420,6 +433,7 @@ class Plan:
         """Root-mean-square norm of x (+ residual) over H, times `weight`
         (a2av_rms_norm): into y (bf16) and/or rows8 (8-bit rows [R][T][H+16]),
         the sum into residual_out (which may be x or residual itself)."""
+        torch = _torch()
         bf16, shape, p = torch.bfloat16, (self.R, self.T, self.H), self._p
         rc = self.lib.a2av_rms_norm(
             self.handle, p(x, bf16, shape, "x"), None if residual is None else p(residual, bf16, shape, "residual"),
@@ -433,6 +447,7 @@ class Plan:
 
     def quantize_rows(self, x, splits: Splits, rows8, stream=None):
         """8-bit rows of the live rows of an arena x [arena_rows][K] (a2av_quantize_rows)."""
+        torch = _torch()
         K = _width(x, "x")
         rc = self.lib.a2av_quantize_rows(
             self.handle, self._p(x, torch.bfloat16, (self.arena_rows, K), "x"), K, self._sp(splits),
@@ -446,6 +461,7 @@ class Plan:
         w [E][Nw][K] bf16 with x bf16 [arena_rows][K], or float8_e4m3fn with
         w_scale fp32 [E][Nw] and x 8-bit rows [arena_rows][K+16]; y bf16
         [arena_rows][N].  activation "swiglu": Nw = 2N, gate rows then up rows."""
+        torch = _torch()
         K = _width(w, "w")
         if w.dtype is torch.float8_e4m3fn:
             kind, dtype, xp = W_E4M3, w.dtype, self._p(x, torch.uint8, (self.arena_rows, K + ROW8_TAIL), "x")
@@ -458,6 +474,7 @@ class Plan:
     def expert_matmul_w4(self, x, w4, w_scale, splits: Splits, y, activation=None, stream=None):
         """``expert_matmul`` with 4-bit weights, for few rows per expert: w4 int32
         [E][Nw][K/8], w_scale bf16 [E][Nw][K/group] (``pack_weights_w4``), x bf16."""
+        torch = _torch()
         K = _width(w4, "w4") * 8
         groups = max(1, _width(w_scale, "w_scale"))
         if K % groups:
@@ -467,6 +484,7 @@ class Plan:
                      splits, y, activation, stream)
 
     def _matmul(self, x, w, w_dtype, K, w_width, kind, group, w_scale, splits, y, activation, stream):
+        torch = _torch()
         act = ACTIVATIONS.get(activation, -1)
         if act < 0:
             raise A2avError(f"activation must be None or 'swiglu', got {activation!r}")
@@ -479,8 +497,9 @@ class Plan:
             _check(self.lib, rc, "a2av_expert_matmul")
 
     def _p(self, t, dtype, shape, name):
-        """Device pointer of a tensor that is as it has to be; else ``_t`` says what is wrong."""
-        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+        """Device pointer of a tensor that is as it has to be; else ``_t`` says what is wrong.  (A torch
+        dtype is one object, which nothing but a tensor has for its own.)"""
+        if (getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous()
                 and t.device == self.device):
             return t.data_ptr()
         return self._t(t, dtype, shape, name)
