@@ -10,17 +10,20 @@ from .binding import ROW8_TAIL, A2avError
 # takes two neighbours out as the two halves of a register.
 W4_SHIFTS = (0, 16, 4, 20, 8, 24, 12, 28)
 E4M3_MAX = 448.0
+ZERO_ROW = 1e-30  # as in the 8-bit rows the kernels write
 
 
 def quantize_weights(w):
-    """(float8_e4m3fn [..][K], fp32 scale [..]) of w [..][K]: scale = max|w| / 448 per row."""
+    """(float8_e4m3fn [..][K], fp32 scale [..]) of w [..][K]: scale = max|w| / 448 per row; a row whose
+    maximum is below 1e-30 is zeros with scale 0 (448 / max|w| has to lie in fp32's range)."""
     import torch
 
     w = w.float()
     a = w.abs().amax(-1)
-    inv = torch.where(a > 0, E4M3_MAX / a, torch.zeros_like(a))
+    zero = a < ZERO_ROW  # false for NaN
+    inv = torch.where(zero, 0.0, E4M3_MAX / a)
     q = (w * inv.unsqueeze(-1)).clamp_(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
-    return q, a / E4M3_MAX
+    return q, torch.where(zero, 0.0, a / E4M3_MAX)
 
 
 def pack_weights_w4(w, group: int = 128):
