@@ -47,6 +47,7 @@ class MoeBlock:
 
         self.w_norm = (1.0 + normal(H, std=0.1)).to(torch.bfloat16)
         self.w_router = normal(E, H, std=H ** -0.5).to(torch.bfloat16)
+        self.router32 = self.w_router.float().T             # what its product takes, laid out once
         w_in, w_out = normal(E, 2 * F, H, std=H ** -0.5), normal(E, H, F, std=F ** -0.5)
         self.s_in = self.s_out = None
         if form == "bf16":
@@ -66,11 +67,13 @@ class MoeBlock:
         arena = self.plan.arena_rows
         bf = dict(dtype=torch.bfloat16, device=dev)
         self.y = torch.empty(R, T, H, **bf)                 # normed tokens: the router reads them, and the bf16 experts
+        self.y32 = torch.empty(R * T, H, dtype=torch.float32, device=dev)  # the same for the router's product
         self.rows8 = self.plan.new_rows8((R, T), H) if form == "8bit" else None
         self.logits = torch.empty(R, T, E, dtype=torch.float32, device=dev)
         self.topk = torch.empty(R, T, k, dtype=torch.int32, device=dev)
         self.gate = torch.empty(R, T, k, dtype=torch.float32, device=dev)
-        self.recv, self.slot_map, self.out = self.rows_plan.new_buffers()
+        self.recv = torch.empty(arena, self.rows_plan.H, **bf)
+        self.slot_map = torch.empty(R, T, k, dtype=torch.int32, device=dev)
         self.out = torch.empty(R, T, H, **bf)
         self.inner = torch.empty(arena, F, **bf)
         self.inner8 = self.plan.new_rows8(arena, F) if form == "8bit" else None
@@ -81,8 +84,8 @@ class MoeBlock:
         block's residual stream)."""
         p, rows = self.plan, self.rows_plan
         p.rms_norm(x, self.w_norm, y=self.y, rows8=self.rows8, residual=residual, residual_out=residual, eps=self.eps)
-        torch.matmul(self.y.view(-1, self.H).float(), self.w_router.float().T,
-                     out=self.logits.view(-1, self.E))      # the router's own projection, a plain library product
+        self.y32.copy_(self.y.view(-1, self.H))
+        torch.mm(self.y32, self.router32, out=self.logits.view(-1, self.E))  # the router's projection, a library product
         p.route(self.logits, self.topk, self.gate)
         sent = self.y if self.form != "8bit" else self.rows8.view(torch.bfloat16)
         rows.dispatch(sent, self.topk, self.splits, self.recv, self.slot_map)
