@@ -350,6 +350,10 @@ enum {
  *                            and e4m3_rne(v * (448 / max|v|)); a row whose maximum is
  *                            below 1e-30 is all zero with scale 0; a NaN or an infinity
  *                            anywhere in a row makes its scale NaN or infinite.
+ * Squares and their sum are fp32: a finite row whose squares sum to 2^128 or
+ * more (one value of 1.8e19) gives zeros, and with eps = 0 a row whose squares
+ * vanish (values below 2.6e-23, zeros) gives infinities or NaN; in between,
+ * with eps = 0 and values below 1e-19, the squares lose digits.
  * x, residual, residual_out bf16 [R][T][H], weight bf16 [H]; at least one of
  * y and rows8; y and rows8 overlap nothing else.  H <= 32768, and H % 16 == 0
  * for rows8 (then 16-byte aligned).  Tokens that take no part

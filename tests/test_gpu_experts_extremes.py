@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import combine_device_resident_gb300 as A
-from tests.test_gpu_experts import BF, CANARY, DEV, gen, layout, normal, plan_for, product_ref, run_product, within
+from tests.test_gpu_experts import (BF, CANARY, DEV, check_rows8, gen, layout, norm_ref, normal, plan_for, product_ref,
+                                    run_product, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -227,3 +228,55 @@ def test_pairs_give_up_in_order(kind, counts, polls):
 @pytest.mark.parametrize("K,swiglu", [(18432, False), (1024, True)])
 def test_the_4bit_split_form_gives_up_in_order(K, swiglu, polls):
     gives_up_in_order(run_product("int4", [[1, 5, 0, 40]], K, 72, swiglu, group=64, seed=polls), polls, K, swiglu)
+
+
+# ---- the norm's smallest and largest rows ------------------------------------------------
+
+def both_norms(x, w, eps):
+    """(y, rows8) of rows x [n][H]."""
+    n, H = x.shape
+    plan = A.Plan(1, 1, n, H, 1, device=DEV)
+    y, rows8 = torch.full((1, n, H), CANARY, device=DEV, dtype=torch.bfloat16), plan.new_rows8((1, n), H).fill_(0xA5)
+    plan.rms_norm(x.unsqueeze(0), w, y=y, rows8=rows8, eps=eps)
+    torch.cuda.synchronize()
+    plan.close()
+    return y[0], rows8[0]
+
+
+@pytest.mark.parametrize("H", [256, 512, 7168])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_of_rows_with_subnormal_squares(H, eps):
+    """Rows of 1e-20: a square is 71,000 steps of fp32's smallest, so it and the mean are half a step off each, 2^-16 of
+    the value together, half of that in the root; the rest is 2^-18."""
+    x = torch.full((3, H), 1e-20, device=DEV)
+    x[1, ::2] *= -1
+    x[2] = 1.0
+    x, w = x.bfloat16(), (normal(gen(H), H) * 0.1 + 1).bfloat16()
+    y, rows8 = both_norms(x, w, eps)
+    _, v = norm_ref(x, None, w, eps)
+    within(y, v, v.abs() * (BF + 2.0 ** -17 + 2.0 ** -18) + 1e-38)
+    check_rows8(rows8, v, 2.0 ** -17 + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("H", [256, 512, 7168])
+def test_norm_of_rows_at_the_end_of_the_range(H):
+    """Squares up to 2^128 are right; past it the row is zeros, in y and in 8 bits, as the header says; with eps = 0 rows
+    without a square have no norm."""
+    g = gen(H)
+    x = normal(g, 4, H)
+    x[0, 3] = 1.8e19   # its square is 3.2e38
+    x[1, 3] = 1.9e19   # 3.6e38, past 2^128
+    x[2] = 0.0
+    x[3] *= 1e15
+    x, w = x.bfloat16(), torch.ones(H, device=DEV, dtype=torch.bfloat16)
+    y, rows8 = both_norms(x, w, 1e-6)
+    _, v = norm_ref(x, None, w, 1e-6)
+    for row in (0, 2, 3):
+        within(y[row], v[row], v[row].abs() * (BF + 2.0 ** -18) + 1e-38)
+        if row != 2:
+            check_rows8(rows8[row:row + 1], v[row:row + 1], 2.0 ** -18)
+    for row in (1, 2):
+        q, s = A.rows8_parts(rows8[row:row + 1])
+        assert (y[row] == 0).all() and (q.float() == 0).all() and s == 0
+    y, rows8 = both_norms(x, w, 0.0)
+    assert torch.isnan(y[2]).all() and torch.isnan(A.rows8_parts(rows8[2:3])[1]).all()
