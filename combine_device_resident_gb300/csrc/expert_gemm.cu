@@ -60,13 +60,6 @@ struct Shared {
 
 static_assert(sizeof(Shared) % 16 == 0 && offsetof(Shared, x_scale) % 16 == 0, "the scales are read four at a time");
 
-// Shared-memory operand descriptor: K-major, 128-byte swizzle, eight-row
-// groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
-}
-
 template <bool kFp8>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     const uint32_t acc = accumulate ? 1u : 0u;
@@ -104,8 +97,6 @@ __device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // 32 columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {

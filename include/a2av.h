@@ -397,8 +397,8 @@ a2av_status_t a2av_expert_matmul(a2av_plan_t plan, const void *x, const void *w,
 /* Diagnostic hook for the failure path of the bounded waits (not part of
  * the method).  The TMA pack (default), the TMA combine
  * (A2AV_FLAG_COMBINE_TMA), the lane-per-token router (a2av_route's
- * default) and the experts' products (a2av_expert_matmul with bf16 or 8-bit
- * weights) wait on mbarriers for the bulk copies (and matrix
+ * default) and the experts' products (a2av_expert_matmul with any weight
+ * type) wait on mbarriers for the bulk copies (and matrix
  * instructions) they issued themselves; each wait gives up after a bounded number of polls, sets
  * A2AV_DEV_WAIT_TIMEOUT in the status word and ends the CTA in order (it
  * first lets every copy it issued land, with the full bound).  This call sets
