@@ -8,7 +8,8 @@
 // of c rows costs ceil(c/32)*32 columns, not a multiple of 128, and a group of
 // a few rows streams the weights once with a narrow instruction.  Many rows:
 // bound by the tensor pipe (90% active; 8 x 1,024 rows, 5120 -> 2 x 2048: 197-205 us,
-// 1.68-1.75 PFLOP/s); few: by the weights' bytes (16 experts with a row each: 76 us, 5.8 TB/s).
+// 1.68-1.75 PFLOP/s); few: by the weights' bytes (16 rows over 16 experts, about
+// ten of them live: 76 us, 420 MB at 5.5 TB/s).
 //
 // One persistent pair of blocks per two SMs (a cluster, cta_group::2): each
 // block loads its 128 of the tile's 256 weight rows and half of its expert
@@ -39,7 +40,7 @@ constexpr int kTileN = 256;         // expert rows per tile, at most
 constexpr int kABytes = kTileM * kRowBytes;
 constexpr int kBBytes = kTileN / 2 * kRowBytes;  // half of them in each block
 // The ring: six stages for any tile; or, when no expert has more than 32 rows, ten whose row part holds just these:
-// such a call streams weights, and what an SM gets is what it has in flight (16 experts with a row each: 76 us
+// such a call streams weights, and what an SM gets is what it has in flight (16 rows over 16 experts: 76 us
 // against 83 with the six).
 constexpr int kStageBytes = kABytes + kBBytes, kRingBytes = kStages * kStageBytes;
 constexpr int kFewRows = 32, kFewStageBytes = kABytes + kFewRows / 2 * kRowBytes, kFewStages = 10;
@@ -96,24 +97,6 @@ __device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// 32 columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr)
-        : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Loads into this block's shared memory that count on a barrier of the pair's first block (`bar`).
@@ -363,8 +346,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_fence_after();
             uint16_t *y = a.y + (size_t)w.row * a.N + chan;
             for (int c = side * 32; c < w.rows; c += 64) {
-                float v[32];
-                tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + b * kTileN + c, v);
+                float got[1][32];
+                tmem_ld<32>(tmem + ((uint32_t)(quad * 32) << 16) + b * kTileN + c, got[0]);
+                tmem_wait_ld(got);
+                float(&v)[32] = got[0];
                 if (kFp8) {
                     const float4 *xs = reinterpret_cast<const float4 *>(scales + (c >> 6) * 32);
 #pragma unroll

@@ -22,3 +22,14 @@ def test_tensor_memory_is_taken_after_the_dependency_wait():
             found.append(kernel)
             assert 0 <= body.find("grid_dependency_wait();") < alloc, (name, kernel)
     assert sorted(found) == ["expert_gemm_kernel", "expert_w4_tmem_kernel"]
+
+
+def test_tensor_memory_loads_are_used_after_their_wait():
+    """The registers of an asynchronous load are no operands of the wait, so a compiler may use them before it, unless they
+    pass through a statement behind it: one function waits, and passes them on."""
+    for name in sorted(os.listdir(CSRC)):
+        text = open(os.path.join(CSRC, name)).read()
+        waits = [m.end() for m in re.finditer(r"tcgen05\.wait::ld", text)]
+        assert len(waits) == (name == "expert_common.cuh"), name
+        for at in waits:
+            assert re.search(r'asm volatile\("" : "\+[fr]"\(v', text[at:text.index("\n}", at)]), name
