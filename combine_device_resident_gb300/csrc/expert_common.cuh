@@ -122,7 +122,6 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-
 // All of tensor memory for this block (a whole warp calls these).
 __device__ __forceinline__ void tmem_alloc_all(uint32_t *to) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(to)) : "memory");
@@ -205,7 +204,7 @@ cudaError_t allow_smem(Kernel kernel, std::atomic<uint64_t> &done, int device, s
     return e;
 }
 
-// A 128-byte-swizzled tensor map with zeros outside; the reason of a failure in the last error.
+// A 128-byte-swizzled tensor map with zeros outside; false where the driver has no such function or refuses.
 bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
                 const cuuint64_t *strides, const cuuint32_t *box);
 
