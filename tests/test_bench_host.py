@@ -96,3 +96,10 @@ def test_tokens_and_hidden_options_scale_the_workload():
     w = bench.resolve_workload(a)
     assert (w.T, w.H, w.window_rows) == (16, W.WORKLOADS[3].H, W.WORKLOADS[3].R * 16 * W.WORKLOADS[3].k)
     assert bench.resolve_workload(bench.parse_args([])) == W.WORKLOADS[bench.DEFAULT_WORKLOAD]
+
+
+def test_traffic_records_are_of_the_present_sources():
+    # A change of the hashed sources (the shared headers among them) without new counters drops the record from the
+    # benchmark's line in silence.
+    w5 = "r32-e256-t2048-h7168-top8-hot0-zipf1.1-softmax"
+    assert bench.ncu_traffic("pack", w5) and bench.ncu_traffic("combine", w5)
