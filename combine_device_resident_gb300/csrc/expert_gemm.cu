@@ -7,8 +7,8 @@
 // expert's rows the N side: N may be any multiple of 32 up to 256, so a group
 // of c rows costs ceil(c/32)*32 columns, not a multiple of 128, and a group of
 // a few rows streams the weights once with a narrow instruction.  Many rows:
-// bound by the tensor pipe (90% active; 8 x 1,024 rows, 5120 -> 2 x 2048: 197-205 us,
-// 1.68-1.75 PFLOP/s); few: by the weights' bytes (16 rows over 16 experts, about
+// bound by the tensor pipe (90% active; 8 x 1,024 rows, 5120 -> 2 x 2048: 195-205 us,
+// 1.68-1.76 PFLOP/s); few: by the weights' bytes (16 rows over 16 experts, about
 // ten of them live: 76 us, 420 MB at 5.5 TB/s).
 //
 // One persistent pair of blocks per two SMs (a cluster, cta_group::2): each
@@ -468,7 +468,7 @@ bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *
     }();
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     // Rows that start on 128-byte lines are fetched ahead in pairs of lines; rows that do not would bring lines
-    // in that belong to no box (8,168 rows of K = 1416: 125 us with, 111 us without; K = 1408: 85 us, 87 us).
+    // in that belong to no box (8,168 rows of K = 1416: 125 us with, 111 us without, 119 at most on other boxes; K = 1408: 85 us, 87 us).
     const CUtensorMapL2promotion promotion =
         strides[0] % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     return encode && encode(m, type, rank, const_cast<void *>(base), dims, strides, box, ones,

@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 // being per warp), and there are as many buffers as tensor memory holds.  (A
 // barrier's parity tells a waiter only that the last phase is over: whoever
 // waits for a buffer has to see every phase of it.)  1,024 rows on 256
-// experts, K = 7168, SwiGLU to 2048: 540 us, 4.6 TB/s of weights (525 with the 136 taken off by
-// a second instruction, see above); next to HBM the ALU
-// pipe bounds it (65%), as seven of an unpacked word's operations run there at half rate.
+// experts, K = 7168, SwiGLU to 2048: 540-556 us, 4.5-4.6 TB/s of weights (525 with the 136 taken
+// off by a second instruction, see above).  No unit is full (256 rows on 32 experts: the ALU pipe 61%, which takes seven of
+// an unpacked word's eleven operations, issue 65%, HBM 59%); what is left is the way round a buffer.
 constexpr int kMaxCols = 16;                 // expert rows per work item: the instruction's N
 constexpr int kACols = kSpan / 2;            // 32-bit columns of a span's A
 constexpr int kTileRows = 128;
@@ -628,9 +628,9 @@ cudaError_t launch_w4_split(const a2av_plan_s &p, const MatmulArgs &a, cudaStrea
 cudaError_t launch_expert_w4(const a2av_plan_s &p, const MatmulArgs &a, bool swiglu, cudaStream_t s) {
     // The split form while all its items (16 weight rows each) are resident at once, two to an SM; when some would have
     // to wait for a turn the form on tensor memory is the faster one.  One row to 4096 (256 items): K = 2048 5.9 us
-    // split, 7.8 on tensor memory, 4096 8.6 and 11.3, 8192 14.3 and 18.1; to 5120 (320 items), K = 2048: 9.7 and 7.9;
-    // to 6144: K = 1024 8.9 and 6.2, 8192 25 and 18.  K = 5120, SwiGLU to 2048: one expert 7.9 and 13.1, two 15.1 and
-    // 13.4, sixteen 92 and 36.
+    // split, 8.3 on tensor memory, 4096 8.6 and 12.2, 8192 14.1 and 20.3; to 5120 (320 items), K = 2048: 9.7 and 8.3;
+    // to 6144: K = 1024 8.9 and 6.2, 8192 25 and 20.  K = 5120, SwiGLU to 2048: one expert 8.1 and 13.0, two 15.3 and
+    // 13.3, sixteen 93 and 37.
     if (split_items(a, swiglu) > 2 * p.num_sms)
         return swiglu ? launch_w4_groups<true>(p, a, s) : launch_w4_groups<false>(p, a, s);
     return swiglu ? launch_w4_split<true>(p, a, s) : launch_w4_split<false>(p, a, s);
