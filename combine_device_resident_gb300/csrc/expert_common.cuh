@@ -204,7 +204,7 @@ cudaError_t allow_smem(Kernel kernel, std::atomic<uint64_t> &done, int device, s
     return e;
 }
 
-// A 128-byte-swizzled tensor map with zeros outside; false where the driver has no such function or refuses.
+// A 128-byte-swizzled tensor map with zeros outside; false where the CUDA driver has no such function or refuses.
 bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
                 const cuuint64_t *strides, const cuuint32_t *box);
 

@@ -468,7 +468,7 @@ bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *
     }();
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     // Rows that start on 128-byte lines are fetched ahead in pairs of lines; rows that do not would bring lines
-    // in that belong to no box (8,168 rows of K = 1416: 125 us with, 111 us without, 119 at most on other boxes; K = 1408: 85 us, 87 us).
+    // in that belong to no box (8,168 rows of K = 1416: 125 us with, 111-119 us without; K = 1408: 85 us, 87 us).
     const CUtensorMapL2promotion promotion =
         strides[0] % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     return encode && encode(m, type, rank, const_cast<void *>(base), dims, strides, box, ones,
