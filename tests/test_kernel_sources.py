@@ -15,21 +15,22 @@ def kernels():
 def test_tensor_memory_is_taken_after_the_dependency_wait():
     """A kernel that starts early and takes tensor memory before it waits can leave its predecessor, whose blocks may
     take theirs later, without any: each would wait for the other."""
-    found = []
+    found = set()
     for name, kernel, body in kernels():
         alloc = min((body.find(t) for t in ("tcgen05.alloc", "tmem_alloc_all(") if t in body), default=-1)
         if alloc >= 0:
-            found.append(kernel)
+            found.add(kernel)
             assert 0 <= body.find("grid_dependency_wait();") < alloc, (name, kernel)
-    assert sorted(found) == ["expert_gemm_kernel", "expert_w4_tmem_kernel"]
+    assert found >= {"expert_gemm_kernel", "expert_w4_tmem_kernel"}
 
 
 def test_tensor_memory_loads_are_used_after_their_wait():
     """The registers of an asynchronous load are no operands of the wait, so a compiler may use them before it, unless they
-    pass through a statement behind it: one function waits, and passes them on."""
+    pass through a statement behind it, in the same function."""
+    found = 0
     for name in sorted(os.listdir(CSRC)):
         text = open(os.path.join(CSRC, name)).read()
-        waits = [m.end() for m in re.finditer(r"tcgen05\.wait::ld", text)]
-        assert len(waits) == (name == "expert_common.cuh"), name
-        for at in waits:
-            assert re.search(r'asm volatile\("" : "\+[fr]"\(v', text[at:text.index("\n}", at)]), name
+        for wait in re.finditer(r"tcgen05\.wait::ld", text):
+            found += 1
+            assert re.search(r'asm volatile\("" : "\+[fr]"', text[wait.end():text.index("\n}", wait.end())]), name
+    assert found
