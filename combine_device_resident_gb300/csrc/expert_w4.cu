@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const __grid_con
 // being per warp), and there are as many buffers as tensor memory holds.  (A
 // barrier's parity tells a waiter only that the last phase is over: whoever
 // waits for a buffer has to see every phase of it.)  1,024 rows on 256
-// experts, K = 7168, SwiGLU to 2048: 540-556 us, 4.5-4.6 TB/s of weights (525 with the 136 taken
+// experts, K = 7168, SwiGLU to 2048: 540-574 us, 4.4-4.6 TB/s of weights (525-564 with the 136 taken
 // off by a second instruction, see above).  No unit is full (256 rows on 32 experts: the ALU pipe 61%, which takes seven of
 // an unpacked word's eleven operations, issue 65%, HBM 59%); what is left is the way round a buffer.
 constexpr int kMaxCols = 16;                 // expert rows per work item: the instruction's N
