@@ -22,6 +22,7 @@ from .binding import (  # noqa: F401
     ORDER_EXPERT,
     ORDER_SOURCE,
     Plan,
+    RouteRule,
     Splits,
     load_library,
     library_path,

@@ -38,6 +38,8 @@ W_BF16 = 0  # weight types of the experts' products
 W_E4M3 = 1
 W_INT4 = 2
 ACTIVATIONS = {None: 0, "none": 0, "swiglu": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GATE_NONE, GATE_CHANNEL, GATE_RANK, GATE_TOKEN = 0, 1, 2, 3
 ROW8_TAIL = 16  # bytes behind the values of an 8-bit row: the fp32 scale and padding
 
 # Every function the header declares, for load checks.
@@ -48,7 +50,8 @@ EXPORTED = [
     "a2av_status_string", "a2av_last_error", "a2av_dispatch_static",
     "a2av_dispatch_padded", "a2av_pack_padded", "a2av_exchange_padded", "a2av_set_active_tokens",
     "a2av_route", "a2av_route_splits", "a2av_set_wait_limit", "a2av_rms_norm", "a2av_quantize_rows",
-    "a2av_expert_matmul",
+    "a2av_expert_matmul", "a2av_route_scores", "a2av_route_scores_grad", "a2av_combine_grad", "a2av_block_norm",
+    "a2av_norm_scratch_bytes", "a2av_block_norm_grad",
 ]
 
 
@@ -81,6 +84,29 @@ class SplitsPtrs(ctypes.Structure):
 
 class A2avError(RuntimeError):
     pass
+
+
+class RouteRule(ctypes.Structure):
+    """How ``Plan.route_scores`` chooses experts and what their gates are (a2av_route_rule_t).
+
+    ``score`` "softmax" (over all experts) or "sigmoid"; ``groups`` of consecutive experts, of which a token
+    may choose from ``groups_kept`` (None: all), valued by their best choice or the sum of their two best
+    (``group_best`` 1 or 2); ``renormalize``: gates divided by their sum; ``scale``: a factor of the gates."""
+
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    def __init__(self, score="softmax", groups=1, groups_kept=None, group_best=1, renormalize=True, scale=1.0):
+        if score not in SCORES:
+            raise A2avError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+        kept = groups if groups_kept is None else groups_kept
+        super().__init__(SCORES[score], int(groups), int(kept), int(group_best), int(bool(renormalize)), float(scale))
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("gate_kind", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -152,6 +178,19 @@ def load_library(path: Optional[str] = None):
     L.a2av_quantize_rows.restype = i32
     L.a2av_expert_matmul.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, spp, vp]
     L.a2av_expert_matmul.restype = i32
+    rulep, normp = ctypes.POINTER(RouteRule), ctypes.POINTER(BlockNormArgs)
+    L.a2av_route_scores.argtypes = [vp, rulep, vp, vp, vp, vp, vp]
+    L.a2av_route_scores.restype = i32
+    L.a2av_route_scores_grad.argtypes = [vp, rulep, vp, vp, vp, vp, vp]
+    L.a2av_route_scores_grad.restype = i32
+    L.a2av_combine_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+    L.a2av_combine_grad.restype = i32
+    L.a2av_block_norm.argtypes = [vp, normp, vp, vp, vp, vp, vp, vp]
+    L.a2av_block_norm.restype = i32
+    L.a2av_norm_scratch_bytes.argtypes = [vp]
+    L.a2av_norm_scratch_bytes.restype = ctypes.c_int64
+    L.a2av_block_norm_grad.argtypes = [vp, normp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.a2av_block_norm_grad.restype = i32
     if path is None:
         _lib = L
     return L
@@ -495,6 +534,113 @@ class Plan:
             self._s(stream))
         if rc:
             _check(self.lib, rc, "a2av_expert_matmul")
+
+    # ---- the router by scores, the gradients, the norms around a block ----------------
+    def _rule(self, rule):
+        if not isinstance(rule, RouteRule):
+            raise A2avError("rule must be a RouteRule")
+        return rule
+
+    def route_scores(self, logits, topk_idx, gate_w, rule: RouteRule, bias=None, stream=None):
+        """Experts and gates of fp32 logits [R][T][E] by ``rule`` (a2av_route_scores); ``bias`` fp32 [E]
+        takes part in the choice alone."""
+        torch = _torch()
+        f32, p, per = torch.float32, self._p, (self.R, self.T, self.k)
+        rc = self.lib.a2av_route_scores(
+            self.handle, self._rule(rule), p(logits, f32, (self.R, self.T, self.E), "logits"),
+            None if bias is None else p(bias, f32, (self.E,), "bias"), p(topk_idx, torch.int32, per, "topk_idx"),
+            p(gate_w, f32, per, "gate_w"), self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_route_scores")
+
+    def route_scores_grad(self, logits, topk_idx, d_gate, d_logits, rule: RouteRule, stream=None):
+        """d_logits fp32 [R][T][E] from the gradient of ``route_scores``' gates (a2av_route_scores_grad)."""
+        torch = _torch()
+        f32, p, per, each = torch.float32, self._p, (self.R, self.T, self.k), (self.R, self.T, self.E)
+        rc = self.lib.a2av_route_scores_grad(
+            self.handle, self._rule(rule), p(logits, f32, each, "logits"), p(topk_idx, torch.int32, per, "topk_idx"),
+            p(d_gate, f32, per, "d_gate"), p(d_logits, f32, each, "d_logits"), self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_route_scores_grad")
+
+    def combine_grad(self, d_out, y, gate_w, slot_map, d_y=None, d_gate=None, stream=None):
+        """Gradients of ``combine`` (a2av_combine_grad): d_y [arena_rows][H] bf16, live rows only (may be y
+        itself), and/or d_gate fp32 [R][T][k].  y may be None without d_gate, gate_w without d_y."""
+        torch = _torch()
+        bf16, p, per, arena = torch.bfloat16, self._p, (self.R, self.T, self.k), (self.arena_rows, self.H)
+        rc = self.lib.a2av_combine_grad(
+            self.handle, p(d_out, bf16, (self.R, self.T, self.H), "d_out"), None if y is None else p(y, bf16, arena, "y"),
+            None if gate_w is None else p(gate_w, torch.float32, per, "gate_w"),
+            p(slot_map, torch.int32, per, "slot_map"), None if d_y is None else p(d_y, bf16, arena, "d_y"),
+            None if d_gate is None else p(d_gate, torch.float32, per, "d_gate"), self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_combine_grad")
+
+    def _gate_kind(self, gate):
+        if gate is None:
+            return GATE_NONE
+        dim = getattr(gate, "ndim", 0)
+        if dim not in (1, 2, 3):
+            raise A2avError("gate must be a tensor [H], [R][H] or [R][T][H]")
+        return dim
+
+    def _gate_shape(self, kind):
+        return ((self.H,), (self.R, self.H), (self.R, self.T, self.H))[kind - 1]
+
+    def _block_norm_args(self, post_weight, gate, weight, residual_scale, branch_scale, eps):
+        bf16, p, kind = _torch().bfloat16, self._p, self._gate_kind(gate)
+        return kind, BlockNormArgs(
+            None if post_weight is None else p(post_weight, bf16, (self.H,), "post_weight"),
+            None if gate is None else p(gate, bf16, self._gate_shape(kind), "gate"),
+            None if weight is None else p(weight, bf16, (self.H,), "weight"), kind, residual_scale, branch_scale, eps)
+
+    def block_norm(self, x, residual, residual_out=None, weight=None, y=None, rows8=None, post_weight=None, gate=None,
+                   residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None):
+        """Between two blocks (a2av_block_norm): x, what a block gave, normed by ``post_weight``, times ``gate``
+        ([H], [R][H] or [R][T][H]) and ``branch_scale``, plus ``residual_scale`` * residual, into residual_out
+        (which may be x or residual itself); that normed by ``weight`` into y (bf16) and/or rows8 (8-bit rows)."""
+        torch = _torch()
+        bf16, shape, p = torch.bfloat16, (self.R, self.T, self.H), self._p
+        _, args = self._block_norm_args(post_weight, gate, weight, residual_scale, branch_scale, eps)
+        rc = self.lib.a2av_block_norm(
+            self.handle, args, p(x, bf16, shape, "x"), p(residual, bf16, shape, "residual"),
+            None if residual_out is None else p(residual_out, bf16, shape, "residual_out"),
+            None if y is None else p(y, bf16, shape, "y"),
+            None if rows8 is None else p(rows8, torch.uint8, (self.R, self.T, self.H + ROW8_TAIL), "rows8"),
+            self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_block_norm")
+
+    def new_norm_scratch(self):
+        """Scratch of ``block_norm_grad`` for this plan (uint8, uninitialised); one per call in flight."""
+        torch = _torch()
+        return torch.empty(int(self.lib.a2av_norm_scratch_bytes(self.handle)), dtype=torch.uint8, device=self.device)
+
+    def block_norm_grad(self, x, residual, d_x, d_residual, weight=None, d_y=None, d_residual_out=None,
+                        post_weight=None, gate=None, d_weight=None, d_post_weight=None, d_gate=None, scratch=None,
+                        residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None):
+        """Gradients of ``block_norm`` from d_y and/or d_residual_out (a2av_block_norm_grad): d_x and d_residual
+        bf16 [R][T][H] (which may be d_y and d_residual_out themselves), the weights' in fp32, d_gate fp32 as gate's
+        shape, or bf16 for a gate [R][T][H].  ``scratch``: ``new_norm_scratch``, where a summed gradient is asked for."""
+        torch = _torch()
+        bf16, f32, shape, p = torch.bfloat16, torch.float32, (self.R, self.T, self.H), self._p
+        kind, args = self._block_norm_args(post_weight, gate, weight, residual_scale, branch_scale, eps)
+        if d_gate is not None:
+            if kind == GATE_NONE:
+                raise A2avError("d_gate needs gate")
+            d_gate = p(d_gate, bf16 if kind == GATE_TOKEN else f32, self._gate_shape(kind), "d_gate")
+        if scratch is not None:
+            scratch = p(scratch, torch.uint8, (int(self.lib.a2av_norm_scratch_bytes(self.handle)),), "scratch")
+        rc = self.lib.a2av_block_norm_grad(
+            self.handle, args, p(x, bf16, shape, "x"), p(residual, bf16, shape, "residual"),
+            None if d_y is None else p(d_y, bf16, shape, "d_y"),
+            None if d_residual_out is None else p(d_residual_out, bf16, shape, "d_residual_out"),
+            p(d_x, bf16, shape, "d_x"), p(d_residual, bf16, shape, "d_residual"),
+            None if d_weight is None else p(d_weight, f32, (self.H,), "d_weight"),
+            None if d_post_weight is None else p(d_post_weight, f32, (self.H,), "d_post_weight"),
+            d_gate, scratch, self._s(stream))
+        if rc:
+            _check(self.lib, rc, "a2av_block_norm_grad")
 
     def _p(self, t, dtype, shape, name):
         """Device pointer of a tensor that is as it has to be; else ``_t`` says what is wrong.  (A torch

@@ -9,6 +9,7 @@
 #include <new>
 
 #include "a2av_internal.cuh"
+#include "block_ops.cuh"
 
 namespace {
 
@@ -58,6 +59,94 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 
 size_t row_bytes(const a2av_plan_s *p) { return (size_t)p->g.H * 2; }
 size_t tokens(const a2av_plan_s *p) { return (size_t)p->g.R * p->g.T; }
+
+struct Span {
+    const void *p;
+    size_t n;
+    const void *may_be;  // an input this output may be itself
+};
+
+// Whether an output overlaps an input (other than the one it may be) or another output.
+template <int O, int I>
+bool clash(const Span (&out)[O], const Span (&in)[I]) {
+    for (int o = 0; o < O; ++o) {
+        if (!out[o].p) continue;
+        for (int i = 0; i < I; ++i)
+            if (in[i].p && !(out[o].p == in[i].p && out[o].may_be == in[i].p) &&
+                overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+                return true;
+        for (int q = 0; q < o; ++q)
+            if (out[q].p && overlap(out[o].p, out[o].n, out[q].p, out[q].n)) return true;
+    }
+    return false;
+}
+
+bool finite(float v) { return v - v == 0.0f; }
+
+a2av_status_t refuse_call(const char *call, const char *why) {
+    snprintf(g_last_error, sizeof g_last_error, "%s: %s", call, why);
+    return A2AV_ERR_INVALID_ARG;
+}
+
+// Null where the rule can be followed for this plan, else what is wrong with it.
+const char *rule_fault(const a2av_plan_s *p, const a2av_route_rule_t *r) {
+    if (!r) return "rule is null";
+    if (r->score != A2AV_SCORE_SOFTMAX && r->score != A2AV_SCORE_SIGMOID) return "unknown score";
+    if (r->groups < 1 || r->groups > a2av::kMaxGroups || p->g.E % r->groups) return "groups must divide E, at most 64";
+    if (r->groups_kept < 1 || r->groups_kept > r->groups) return "groups_kept must lie in 1..groups";
+    if (r->group_best != 1 && r->group_best != 2) return "group_best must be 1 or 2";
+    if (r->group_best > p->g.E / r->groups) return "group_best exceeds a group's experts";
+    if (r->renormalize != 0 && r->renormalize != 1) return "renormalize must be 0 or 1";
+    if (!finite(r->scale)) return "scale must be finite";
+    if (p->g.k > r->groups_kept * (p->g.E / r->groups)) return "k distinct experts need k <= groups_kept * E / groups";
+    return nullptr;
+}
+
+void score_args(a2av_plan_s *p, const a2av_route_rule_t *r, const float *logits, a2av::ScoreArgs &a) {
+    memset(&a, 0, sizeof a);
+    a.g = p->g;
+    a.num_tokens = p->num_tokens;
+    a.logits = logits;
+    a.status = p->status;
+    a.sigmoid = r->score == A2AV_SCORE_SIGMOID;
+    a.groups = r->groups;
+    a.kept = r->groups_kept;
+    a.best = r->group_best;
+    a.renorm = r->renormalize;
+    a.scale = r->scale;
+}
+
+// What both of the block norm's calls refuse in their weights; null where nothing.
+const char *block_norm_fault(const a2av_block_norm_t *n) {
+    if (!n) return "args is null";
+    if ((uintptr_t)n->post_weight % 16 || (uintptr_t)n->gate % 16 || (uintptr_t)n->weight % 16)
+        return "a misaligned weight";
+    if (n->gate_kind < A2AV_GATE_NONE || n->gate_kind > A2AV_GATE_TOKEN) return "unknown gate_kind";
+    if ((n->gate != nullptr) != (n->gate_kind != A2AV_GATE_NONE)) return "gate and gate_kind do not go together";
+    if (!(n->eps >= 0.0f)) return "eps must not be negative";
+    if (!finite(n->residual_scale) || !finite(n->branch_scale)) return "the scales must be finite";
+    return nullptr;
+}
+
+size_t gate_bytes(const a2av_plan_s *p, int32_t kind) {
+    return row_bytes(p) * (kind == A2AV_GATE_TOKEN ? tokens(p) : kind == A2AV_GATE_RANK ? (size_t)p->g.R : 1);
+}
+
+void block_norm_args(const a2av_plan_s *p, const a2av_block_norm_t *n, const void *x, const void *residual,
+                     a2av::BlockNormArgs &a) {
+    memset(&a, 0, sizeof a);
+    a.g = p->g;
+    a.num_tokens = p->num_tokens;
+    a.x = static_cast<const uint16_t *>(x);
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.post = static_cast<const uint16_t *>(n->post_weight);
+    a.gate = static_cast<const uint16_t *>(n->gate);
+    a.weight = static_cast<const uint16_t *>(n->weight);
+    a.gate_kind = n->gate_kind;
+    a.residual_scale = n->residual_scale;
+    a.branch_scale = n->branch_scale;
+    a.eps = n->eps;
+}
 
 }  // namespace
 
@@ -569,6 +658,161 @@ a2av_status_t a2av_expert_matmul(a2av_plan_t p, const void *x, const void *w, co
     if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
     p->launches += 1;
     return A2AV_OK;
+}
+
+a2av_status_t a2av_route_scores(a2av_plan_t p, const a2av_route_rule_t *rule, const float *logits, const float *bias,
+                                int32_t *topk_idx, float *gate_w, void *stream) {
+    static const char *const call = "a2av_route_scores";
+    if (!p || !aligned(logits, 4) || (uintptr_t)bias % 4 || !aligned(topk_idx, 4) || !aligned(gate_w, 4))
+        return refuse_call(call, "a null or misaligned pointer");
+    if (const char *why = rule_fault(p, rule)) return refuse_call(call, why);
+    const size_t nk = tokens(p) * p->g.k * 4;
+    const Span in[2] = {{logits, tokens(p) * p->g.E * 4}, {bias, (size_t)p->g.E * 4}};
+    const Span out[2] = {{topk_idx, nk}, {gate_w, nk}};
+    if (clash(out, in)) return refuse_call(call, "an output overlaps another tensor");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    a2av::ScoreArgs a;
+    score_args(p, rule, logits, a);
+    a.bias = bias;
+    a.idx = topk_idx;
+    a.gate = gate_w;
+    cudaError_t e = a2av::launch_route_scores(*p, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "score router kernel launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
+a2av_status_t a2av_route_scores_grad(a2av_plan_t p, const a2av_route_rule_t *rule, const float *logits,
+                                     const int32_t *topk_idx, const float *d_gate, float *d_logits, void *stream) {
+    static const char *const call = "a2av_route_scores_grad";
+    if (!p || !aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(d_gate, 4) || !aligned(d_logits, 4))
+        return refuse_call(call, "a null or misaligned pointer");
+    if (const char *why = rule_fault(p, rule)) return refuse_call(call, why);
+    const size_t nl = tokens(p) * p->g.E * 4, nk = tokens(p) * p->g.k * 4;
+    const Span in[3] = {{logits, nl}, {topk_idx, nk}, {d_gate, nk}};
+    const Span out[1] = {{d_logits, nl}};
+    if (clash(out, in)) return refuse_call(call, "d_logits overlaps an input");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    a2av::ScoreArgs a;
+    score_args(p, rule, logits, a);
+    a.idx = const_cast<int32_t *>(topk_idx);
+    a.d_gate = d_gate;
+    a.d_logits = d_logits;
+    cudaError_t e = a2av::launch_route_scores_grad(*p, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "score router gradient launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
+a2av_status_t a2av_combine_grad(a2av_plan_t p, const void *d_out, const void *y, const float *gate_w,
+                                const int32_t *slot_map, void *d_y, float *d_gate, void *stream) {
+    static const char *const call = "a2av_combine_grad";
+    if (!p || !aligned(d_out, 16) || !aligned(slot_map, 4) || (uintptr_t)y % 16 || (uintptr_t)gate_w % 4 ||
+        (uintptr_t)d_y % 16 || (uintptr_t)d_gate % 4)
+        return refuse_call(call, "a null or misaligned pointer");
+    if (!d_y && !d_gate) return refuse_call(call, "neither d_y nor d_gate");
+    if (d_gate && !y) return refuse_call(call, "d_gate needs y");
+    if (d_y && !gate_w) return refuse_call(call, "d_y needs gate_w");
+    const int64_t rows = a2av_recv_arena_rows(&p->cfg);
+    const size_t ny = (size_t)rows * row_bytes(p), nk = tokens(p) * p->g.k * 4;
+    const Span in[4] = {{d_out, tokens(p) * row_bytes(p)}, {y, ny}, {gate_w, nk}, {slot_map, nk}};
+    const Span out[2] = {{d_y, ny, y}, {d_gate, nk}};
+    if (clash(out, in)) return refuse_call(call, "an output overlaps another tensor");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    a2av::CombineGradArgs a;
+    memset(&a, 0, sizeof a);
+    a.g = p->g;
+    a.num_tokens = p->num_tokens;
+    a.d_out = static_cast<const uint16_t *>(d_out);
+    a.y = d_gate ? static_cast<const uint16_t *>(y) : nullptr;
+    a.gate = d_y ? gate_w : nullptr;
+    a.slot_map = slot_map;
+    a.d_y = static_cast<uint16_t *>(d_y);
+    a.d_gate = d_gate;
+    a.arena_rows = rows;
+    a.status = p->status;
+    cudaError_t e = a2av::launch_combine_grad(*p, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "combine gradient launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
+a2av_status_t a2av_block_norm(a2av_plan_t p, const a2av_block_norm_t *n, const void *x, const void *residual,
+                              void *residual_out, void *y, void *rows8, void *stream) {
+    static const char *const call = "a2av_block_norm";
+    if (const char *why = block_norm_fault(n)) return refuse_call(call, why);
+    if (!p || !aligned(x, 16) || !aligned(residual, 16) || (uintptr_t)residual_out % 16 || (uintptr_t)y % 16 ||
+        (uintptr_t)rows8 % 16)
+        return refuse_call(call, "a null or misaligned pointer");
+    if (!residual_out && !y && !rows8) return refuse_call(call, "no output");
+    if ((y || rows8) != (n->weight != nullptr)) return refuse_call(call, "weight goes with y or rows8");
+    if (p->g.H > a2av::kMaxNormRow) return refuse_call(call, "H <= 32768");
+    if (rows8 && p->g.H % 16) return refuse_call(call, "rows8 needs H % 16 == 0");
+    const size_t rows = tokens(p) * row_bytes(p), row = row_bytes(p);
+    const Span in[5] = {{x, rows}, {residual, rows}, {n->post_weight, row}, {n->gate, gate_bytes(p, n->gate_kind)},
+                        {n->weight, row}};
+    const Span out[3] = {{residual_out, rows, residual_out == x ? x : residual}, {y, rows},
+                         {rows8, tokens(p) * ((size_t)p->g.H + 16)}};
+    if (clash(out, in)) return refuse_call(call, "an output overlaps another tensor");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    a2av::BlockNormArgs a;
+    block_norm_args(p, n, x, residual, a);
+    a.residual_out = static_cast<uint16_t *>(residual_out);
+    a.y = static_cast<uint16_t *>(y);
+    a.rows8 = static_cast<uint8_t *>(rows8);
+    cudaError_t e = a2av::launch_block_norm(*p, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "block norm kernel launch");
+    p->launches += 1;
+    return A2AV_OK;
+}
+
+int64_t a2av_norm_scratch_bytes(a2av_plan_t p) { return p ? a2av::norm_scratch_bytes(*p) : -1; }
+
+a2av_status_t a2av_block_norm_grad(a2av_plan_t p, const a2av_block_norm_t *n, const void *x, const void *residual,
+                                   const void *d_y, const void *d_residual_out, void *d_x, void *d_residual,
+                                   float *d_weight, float *d_post_weight, void *d_gate, void *scratch, void *stream) {
+    static const char *const call = "a2av_block_norm_grad";
+    if (const char *why = block_norm_fault(n)) return refuse_call(call, why);
+    if (!p || !aligned(x, 16) || !aligned(residual, 16) || (uintptr_t)d_y % 16 || (uintptr_t)d_residual_out % 16 ||
+        !aligned(d_x, 16) || !aligned(d_residual, 16) || (uintptr_t)d_weight % 16 || (uintptr_t)d_post_weight % 16 ||
+        (uintptr_t)d_gate % 16 || (uintptr_t)scratch % 16)
+        return refuse_call(call, "a null or misaligned pointer");
+    if (!d_y && !d_residual_out) return refuse_call(call, "neither d_y nor d_residual_out");
+    if (d_y && !n->weight) return refuse_call(call, "d_y needs weight");
+    if (d_weight && !d_y) return refuse_call(call, "d_weight needs d_y");
+    if (d_post_weight && !n->post_weight) return refuse_call(call, "d_post_weight needs post_weight");
+    if (d_gate && !n->gate) return refuse_call(call, "d_gate needs gate");
+    const bool sums = d_weight || d_post_weight || (d_gate && n->gate_kind != A2AV_GATE_TOKEN);
+    if (sums && !scratch) return refuse_call(call, "the weights' gradients need scratch");
+    if (p->g.H > a2av::kMaxNormGradRow) return refuse_call(call, "H <= 16384");
+    const size_t rows = tokens(p) * row_bytes(p), row = row_bytes(p), gate = gate_bytes(p, n->gate_kind);
+    const Span in[7] = {{x, rows}, {residual, rows}, {n->post_weight, row}, {n->gate, gate}, {n->weight, row},
+                        {d_y, rows}, {d_residual_out, rows}};
+    const Span out[6] = {{d_x, rows, d_y},
+                         {d_residual, rows, d_residual_out},
+                         {d_weight, 2 * row},
+                         {d_post_weight, 2 * row},
+                         {d_gate, n->gate_kind == A2AV_GATE_TOKEN ? gate : 2 * gate},
+                         {sums ? scratch : nullptr, sums ? (size_t)a2av::norm_scratch_bytes(*p) : 0}};
+    if (clash(out, in)) return refuse_call(call, "an output overlaps another tensor");
+    DeviceGuard guard(p->cfg.device);
+    if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+    a2av::BlockNormArgs a;
+    block_norm_args(p, n, x, residual, a);
+    a.d_y = static_cast<const uint16_t *>(d_y);
+    a.d_residual_out = static_cast<const uint16_t *>(d_residual_out);
+    a.d_x = static_cast<uint16_t *>(d_x);
+    a.d_residual = static_cast<uint16_t *>(d_residual);
+    a.d_weight = d_weight;
+    a.d_post = d_post_weight;
+    a.d_gate = d_gate;
+    a.scratch = static_cast<float *>(scratch);
+    cudaError_t e = a2av::launch_block_norm_grad(*p, a, static_cast<cudaStream_t>(stream), p->launches);
+    return e == cudaSuccess ? A2AV_OK : cuda_fail(e, "block norm gradient launch");
 }
 
 a2av_status_t a2av_set_active_tokens(a2av_plan_t p, const int32_t *num_tokens) {

@@ -394,6 +394,128 @@ a2av_status_t a2av_expert_matmul(a2av_plan_t plan, const void *x, const void *w,
                                  int32_t K, int32_t N, int32_t weight_type, int32_t group, int32_t activation,
                                  const a2av_splits_t *splits, void *stream);
 
+/* Scores of the experts (a2av_route_rule_t.score). */
+enum {
+    A2AV_SCORE_SOFTMAX = 0, /* s_e = exp(l_e) / sum_i exp(l_i), over all E experts */
+    A2AV_SCORE_SIGMOID = 1, /* s_e = 1 / (1 + exp(-l_e)) */
+};
+
+/* How a2av_route_scores chooses experts and what their gates are. */
+typedef struct {
+    int32_t score;       /* A2AV_SCORE_* */
+    int32_t groups;      /* G: the experts in G groups of E/G consecutive ids; G divides E, G <= 64; 1 = no groups */
+    int32_t groups_kept; /* of these, how many a token may choose from: 1..G, groups_kept * E/G >= k */
+    int32_t group_best;  /* a group's value is its best choice (1) or the sum of its two best (2; E/G >= 2) */
+    int32_t renormalize; /* 1: the gates of a token are divided by their sum (before the scale) */
+    float scale;         /* factor of every gate, finite */
+} a2av_route_rule_t;
+
+/* The router by scores (one kernel).  For every token, l its logits (fp32
+ * [R][T][E]; a NaN counts as the lowest finite value, infinities as the
+ * finite ends of fp32), s their scores:
+ *   choice  c_e = s_e + bias[e] (bias fp32 [E]; a NaN sum counts as
+ *           -infinity; an expert of bias -infinity is chosen when nothing else
+ *           is left), or without a bias (NULL) the order of the logits;
+ *   groups  when groups_kept < groups: the groups_kept groups of the largest
+ *           value (group_best; without a bias the two best scores are added),
+ *           of equal ones the lower;
+ *   topk_idx[s][t][0..k-1] = the k experts of the kept groups with the largest
+ *           choice, in descending order, of equal ones the lower id;
+ *   gate_w[s][t][j] = scale * s_j, or with renormalize scale * s_j / sum_i s_i
+ *           over the chosen.  The bias takes no part in the gates.
+ * The order is that of the values in 64 bits: 32-bit values decide where they
+ * differ by more than their error, and else the token is chosen again in 64.
+ * Gates are fp32; the renormalised ones are taken from the logits' differences,
+ * so they sum to the scale also where every chosen score vanishes.
+ * Tokens that take no part (a2av_set_active_tokens) are left untouched.  Needs
+ * k <= E.  Uses no workspace.  The outputs overlap nothing else. */
+a2av_status_t a2av_route_scores(a2av_plan_t plan, const a2av_route_rule_t *rule, const float *logits,
+                                const float *bias, int32_t *topk_idx, float *gate_w, void *stream);
+
+/* The gradient of a2av_route_scores' gates (one kernel): d_logits[s][t][.] =
+ * sum_j d_gate[s][t][j] * d gate_w[s][t][j] / d logits, the choice held fixed
+ * (fp32 [R][T][E], every element written).  topk_idx as the call left it, by the
+ * same rule; an id outside [0, E) contributes nothing and sets
+ * A2AV_DEV_BAD_EXPERT, an id that occurs twice contributes for both of its
+ * slots.  The bias has no gradient.  Tokens that take no part are left
+ * untouched.  Uses no workspace.  d_logits overlaps no input. */
+a2av_status_t a2av_route_scores_grad(a2av_plan_t plan, const a2av_route_rule_t *rule, const float *logits,
+                                     const int32_t *topk_idx, const float *d_gate, float *d_logits, void *stream);
+
+/* The gradient of a2av_combine (one kernel), for d_out bf16 [R][T][H]:
+ *   d_y[slot]       = bf16_rne(gate_w[s][t][j] * d_out[s][t])  bf16 [arena_rows][H]
+ *   d_gate[s][t][j] = sum_h y[slot][h] * d_out[s][t][h]        fp32 [R][T][k], fp32 sums
+ * with slot = slot_map[s][t][j], for every assignment with slot >= 0; d_gate is
+ * 0 for the others, and a slot past the arena sets A2AV_DEV_BAD_SLOT and counts
+ * as one of them.  Rows of d_y that no slot names are left untouched; no two
+ * slots may name one row (the dispatch's never do).  d_y or d_gate may be NULL;
+ * y may be NULL without d_gate, gate_w without d_y.  d_y may be y itself, in
+ * place; otherwise the outputs overlap nothing.  Tokens that take no part are
+ * left untouched.  (The dispatch's own gradient is a2av_combine with gates of
+ * one.) */
+a2av_status_t a2av_combine_grad(a2av_plan_t plan, const void *d_out, const void *y, const float *gate_w,
+                                const int32_t *slot_map, void *d_y, float *d_gate, void *stream);
+
+/* What a gate row of a2av_block_norm belongs to. */
+enum {
+    A2AV_GATE_NONE = 0,    /* no gate: 1 */
+    A2AV_GATE_CHANNEL = 1, /* [H], every token's */
+    A2AV_GATE_RANK = 2,    /* [R][H], a row per rank */
+    A2AV_GATE_TOKEN = 3,   /* [R][T][H], a row per token */
+};
+
+/* Weights and factors of a2av_block_norm and its gradient. */
+typedef struct {
+    const void *post_weight; /* bf16 [H], or NULL: no norm behind the block */
+    const void *gate;        /* bf16, shape as gate_kind says; NULL with A2AV_GATE_NONE */
+    const void *weight;      /* bf16 [H], the next block's norm; NULL without y and rows8 */
+    int32_t gate_kind;       /* A2AV_GATE_* */
+    float residual_scale;    /* a */
+    float branch_scale;      /* b */
+    float eps;               /* of both norms, not negative */
+} a2av_block_norm_t;
+
+/* The norms before and after a block, with the block's gate and the residual's
+ * scale (one kernel): x is what a block gave, for every token
+ *   u = x * post_weight / sqrt(mean_j x_j^2 + eps)   (u = x without post_weight)
+ *   z = a * residual + b * gate * u                  fp32
+ *   residual_out = bf16_rne(z)                       if not NULL
+ *   v = z * weight / sqrt(mean_j z_j^2 + eps)        the next block's input:
+ *   y = bf16_rne(v) and/or rows8 = the 8-bit rows of v, as in a2av_rms_norm
+ * from z in fp32, not from its rounding.  x, residual, residual_out, y bf16
+ * [R][T][H]; at least one output.  residual_out may be x or residual itself; y
+ * and rows8 overlap nothing else.  Every tensor 16-byte aligned, H <= 32768,
+ * H % 16 == 0 for rows8; sums, squares and their range as in a2av_rms_norm.
+ * Tokens that take no part are left untouched. */
+a2av_status_t a2av_block_norm(a2av_plan_t plan, const a2av_block_norm_t *args, const void *x, const void *residual,
+                              void *residual_out, void *y, void *rows8, void *stream);
+
+/* Bytes of the scratch a2av_block_norm_grad needs for this plan (partial sums
+ * of the weights' gradients); -1 for a NULL plan.  Host call. */
+int64_t a2av_norm_scratch_bytes(a2av_plan_t plan);
+
+/* The gradient of a2av_block_norm with the output y (one kernel, and a second
+ * one that adds up the weights' partial sums).  From d_y (bf16, the gradient of
+ * y; NULL for 0; needs args->weight) and d_residual_out (bf16, that of
+ * residual_out; NULL for 0), at least one of them:
+ *   d_x, d_residual  bf16 [R][T][H]
+ *   d_weight, d_post_weight  fp32 [H], summed over the tokens that take part
+ *   d_gate           fp32 [H] or [R][H], summed likewise (channel, rank), or
+ *                    bf16 [R][T][H] (token)
+ * d_weight, d_post_weight and d_gate may each be NULL, and need their weight
+ * (d_weight also d_y).  z and the roots are taken again from x and residual;
+ * sums are fp32, in an order that the sizes alone decide, so two calls give the
+ * same bits.  d_x may be d_y itself and d_residual d_residual_out itself;
+ * otherwise the outputs overlap nothing.  scratch: a2av_norm_scratch_bytes; it
+ * must not be used by another call in flight; NULL when no summed gradient is
+ * asked for.  Every tensor 16-byte aligned, H <= 16384.  Tokens that take no
+ * part are left untouched (their rows of d_x, d_residual and a per-token
+ * d_gate). */
+a2av_status_t a2av_block_norm_grad(a2av_plan_t plan, const a2av_block_norm_t *args, const void *x,
+                                   const void *residual, const void *d_y, const void *d_residual_out, void *d_x,
+                                   void *d_residual, float *d_weight, float *d_post_weight, void *d_gate,
+                                   void *scratch, void *stream);
+
 /* Diagnostic hook for the failure path of the bounded waits (not part of
  * the method).  The TMA pack (default), the TMA combine
  * (A2AV_FLAG_COMBINE_TMA), the lane-per-token router (a2av_route's
