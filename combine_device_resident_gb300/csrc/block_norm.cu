@@ -86,178 +86,257 @@ __device__ __forceinline__ uint4 pack8(const pair (&f)[4]) {
     return make_uint4(bf16_of(f[0]), bf16_of(f[1]), bf16_of(f[2]), bf16_of(f[3]));
 }
 
-// A row of fp32 in shared memory, eight values of a vector apart in two halves, so that a warp's 16-byte accesses lie
-// on consecutive 16 bytes.  A thread touches its own columns alone.
-__device__ __forceinline__ void ld_shared(const ulonglong2 *row, int nvec, int i, pair (&f)[4]) {
-    const ulonglong2 lo = row[i], hi = row[nvec + i];
-    f[0] = lo.x, f[1] = lo.y, f[2] = hi.x, f[3] = hi.y;
-}
-__device__ __forceinline__ void st_shared(ulonglong2 *row, int nvec, int i, const pair (&f)[4]) {
-    row[i] = make_ulonglong2(f[0], f[1]);
-    row[nvec + i] = make_ulonglong2(f[2], f[3]);
-}
-
 // Brings `bytes` (a multiple of 16) into L2.
 __device__ __forceinline__ void prefetch_row(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// Over the block: sum of s, and of t its sum or maximum (NaN kept).  `part` is free again after the next barrier.
-template <bool kMax>
-__device__ __forceinline__ void block_reduce(float &s, float &t, float (*part)[kMaxWarps]) {
+// Sums of N values over the block, of which every thread gets all.  With two, a warp's halves take one each, so both cost
+// little more than one.  `part` is free again after the next barrier.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[kMaxWarps]) {
+    static_assert(N == 1 || N == 2, "values");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    s = warp_sum(s);
-    t = kMax ? warp_max_nan(t) : warp_sum(t);
-    if (lane == 0) {
-        part[0][warp] = s;
-        part[1][warp] = t;
+    constexpr int kLanes = 32 / N;  // that carry a value: lane / kLanes names it
+    float s = v[0];
+    if constexpr (N == 2) {
+        const bool up = lane & 16;
+        s = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
     }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((lane & (kLanes - 1)) == 0) part[lane / kLanes][warp] = s;
     __syncthreads();
-    s = warp_sum(lane < nwarps ? part[0][lane] : 0.0f);
-    t = lane < nwarps ? part[1][lane] : 0.0f;
-    t = kMax ? warp_max_nan(t) : warp_sum(t);
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMaxWarps; w += kLanes) {
+        const int from = w + (lane & (kLanes - 1));
+        if (from < nwarps) s += part[lane / kLanes][from];
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = N == 1 ? s : __shfl_sync(0xffffffffu, s, n * kLanes);
 }
 
+// Largest magnitude of a warp's values, NaN if there is one.
+__device__ __forceinline__ float warp_peak(float v) {
+    float d;
+    asm("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
+}
+
+// A thread takes 16 consecutive values of a row (C times, the threads' width apart): 32 bytes of bf16 in one access where
+// every row starts on 32 bytes (k32), else in two of 16, of which the row's last thread may have the first alone.
+struct Bits {
+    uint4 v[2];
+};
+template <bool k32>
+__device__ __forceinline__ Bits ld16(const uint16_t *p, int left) {
+    Bits b;
+    if (k32) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(b.v[0].x), "=r"(b.v[0].y), "=r"(b.v[0].z), "=r"(b.v[0].w), "=r"(b.v[1].x), "=r"(b.v[1].y),
+                       "=r"(b.v[1].z), "=r"(b.v[1].w)
+                     : "l"(p)
+                     : "memory");
+    } else {
+        b.v[0] = ld_row(p);
+        b.v[1] = left > 8 ? ld_row(p + 8) : make_uint4(0, 0, 0, 0);
+    }
+    return b;
+}
+template <bool k32>
+__device__ __forceinline__ void st16(uint16_t *p, int left, const uint4 &lo, const uint4 &hi) {
+    if (k32) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z),
+                     "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                     : "memory");
+    } else {
+        st_v4(p, lo);
+        if (left > 8) st_v4(p + 8, hi);
+    }
+}
 // A weight: the same for every row, so it stays in the L1 cache.
-__device__ __forceinline__ uint4 ld_weight(const uint16_t *w, int i) {
-    return __ldg(reinterpret_cast<const uint4 *>(w) + i);
+__device__ __forceinline__ Bits ld_weight(const uint16_t *w, int left) {
+    Bits b;
+    b.v[0] = __ldg(reinterpret_cast<const uint4 *>(w));
+    b.v[1] = left > 8 ? __ldg(reinterpret_cast<const uint4 *>(w) + 1) : make_uint4(0, 0, 0, 0);
+    return b;
+}
+__device__ __forceinline__ void unpack16(const Bits &b, pair (&f)[8]) {
+    const uint32_t w[8] = {b.v[0].x, b.v[0].y, b.v[0].z, b.v[0].w, b.v[1].x, b.v[1].y, b.v[1].z, b.v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = both(lo_f(w[i]), hi_f(w[i]));
+}
+template <bool k32>
+__device__ __forceinline__ void store16(uint16_t *p, int left, const pair (&f)[8]) {
+    st16<k32>(p, left, make_uint4(bf16_of(f[0]), bf16_of(f[1]), bf16_of(f[2]), bf16_of(f[3])),
+              make_uint4(bf16_of(f[4]), bf16_of(f[5]), bf16_of(f[6]), bf16_of(f[7])));
+}
+constexpr int kEach = 16;  // values of a row per thread (and C)
+
+// A row of fp32 in shared memory, [quarter of a thread's values][thread], so that a warp's 16-byte accesses lie side by
+// side.  A thread touches its own columns alone.
+__device__ __forceinline__ void ld_shared(const ulonglong2 *row, int slots, pair (&f)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const ulonglong2 v = row[q * slots];
+        f[2 * q] = v.x, f[2 * q + 1] = v.y;
+    }
+}
+__device__ __forceinline__ void st_shared(ulonglong2 *row, int slots, const pair (&f)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q * slots] = make_ulonglong2(f[2 * q], f[2 * q + 1]);
 }
 
 // The factor of x * r1 in z, per channel: branch_scale * post * gate, the gate left out where it is the token's own
 // (gate null here).
-__device__ __forceinline__ void set_coef(const BlockNormArgs &a, const uint16_t *gate, ulonglong2 *coef) {
-    const int nvec = a.g.H / 8;
-    for (int i = threadIdx.x; i < nvec; i += blockDim.x) {
-        pair c[4], w[4];
+template <int C>
+__device__ __forceinline__ void set_coef(const BlockNormArgs &a, const uint16_t *gate, ulonglong2 *coef, int slots) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = both(a.branch_scale);
+    for (int c = 0; c < C; ++c) {
+        const int at = (threadIdx.x + c * blockDim.x) * kEach, left = a.g.H - at;
+        if (left <= 0) continue;
+        pair f[8], w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = both(a.branch_scale);
         if (a.post) {
-            unpack8(ld_weight(a.post, i), w);
+            unpack16(ld_weight(a.post + at, left), w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = mul2(c[e], w[e]);
+            for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], w[e]);
         }
         if (gate) {
-            unpack8(ld_weight(gate, i), w);
+            unpack16(ld_weight(gate + at, left), w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = mul2(c[e], w[e]);
+            for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], w[e]);
         }
-        st_shared(coef, nvec, i, c);
+        st_shared(coef + c * blockDim.x, slots, f);
     }
 }
 
-constexpr int kV = 2;  // 16-byte vectors of a row per thread
-
 // The next row's loads are in registers while a row is worked on.  kBlocks blocks fit an SM.
-template <int V, int kThreads, int kBlocks, bool kPost, bool kToken>
+template <int C, int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
 __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_kernel(const BlockNormArgs a) {
-    extern __shared__ __align__(16) ulonglong2 coef[];  // [half of a vector][vector]
-    __shared__ float part[2][2][2][kMaxWarps];          // [which sum][row parity]
-    const int H = a.g.H, nvec = H / 8, tid = threadIdx.x, width = blockDim.x;
+    extern __shared__ __align__(16) ulonglong2 smem[];
+    __shared__ float part[2][2][2][kMaxWarps];  // [which sum][row parity]
+    const int H = a.g.H, width = blockDim.x, slots = C * width;
+    ulonglong2 *const coef = smem + threadIdx.x;
     const long long rows = (long long)a.g.R * a.g.T;
     const float inv_h = 1.0f / (float)H;
     const pair alpha = both(a.residual_scale);
+    const Bits none = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
     grid_dependency_wait();
     int parity = 0;
-    uint4 xv[V], rv[V], gv[V];
+    Bits xv[C], rv[C], gv[C];
     long long row = blockIdx.x;
     auto load = [&] {  // from the first row on that takes part
         while (row < rows && !row_active(a, row)) row += gridDim.x;
         if (row >= rows) return;
-        const size_t at = (size_t)row * H;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * width;
-            xv[j] = i < nvec ? ld_row(a.x + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
-            rv[j] = i < nvec ? ld_row(a.residual + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
-            if (kToken) gv[j] = i < nvec ? ld_row(a.gate + at + (size_t)i * 8) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < C; ++c) {
+            const int col = (threadIdx.x + c * width) * kEach, left = H - col;
+            const size_t at = (size_t)row * H + col;
+            xv[c] = left > 0 ? ld16<k32>(a.x + at, left) : none;
+            rv[c] = left > 0 ? ld16<k32>(a.residual + at, left) : none;
+            if (kToken) gv[c] = left > 0 ? ld16<k32>(a.gate + at, left) : none;
         }
     };
     load();
     const uint16_t *coef_of = nullptr;
-    if (row < rows) set_coef(a, coef_of = kToken || !a.gate ? nullptr : gate_row(a, row), coef);
+    if (row < rows) set_coef<C>(a, coef_of = kToken || !a.gate ? nullptr : gate_row(a, row), coef, slots);
     while (row < rows) {
-        const size_t at = (size_t)row * H;
+        const size_t base = (size_t)row * H;
         if (!kToken && a.gate_kind == A2AV_GATE_RANK && gate_row(a, row) != coef_of)
-            set_coef(a, coef_of = gate_row(a, row), coef);
+            set_coef<C>(a, coef_of = gate_row(a, row), coef, slots);
         uint8_t *q = a.rows8 ? a.rows8 + (size_t)row * (H + 16) : nullptr;
-        pair z[V][4];
-        float sum = 0.0f, peak = 0.0f, r1 = 1.0f;
+        pair z[C][8];
+        float r1 = 1.0f, peak = 0.0f;
         if (kPost) {
             pair s = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                pair x[4];
-                unpack8(xv[j], x);
+            for (int c = 0; c < C; ++c) {
+                pair x[8];
+                unpack16(xv[c], x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s = fma2(x[e], x[e], s);
+                for (int e = 0; e < 8; ++e) s = fma2(x[e], x[e], s);
             }
-            sum = sum2(s);
-            block_reduce<false>(sum, peak, part[0][parity]);
-            r1 = 1.0f / sqrtf(sum * inv_h + a.eps);
+            float sum[1] = {sum2(s)};
+            block_sum<1>(sum, part[0][parity]);
+            r1 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
         }
-        peak = 0.0f;
         pair s = both(0.0f);
         const pair root = both(r1);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * width;
-            if (i >= nvec) continue;
-            pair x[4], c[4];
-            unpack8(xv[j], x);
-            unpack8(rv[j], z[j]);
-            ld_shared(coef, nvec, i, c);
+        for (int c = 0; c < C; ++c) {
+            const int col = (threadIdx.x + c * width) * kEach, left = H - col;
+            if (left <= 0) continue;
+            pair x[8], f[8];
+            unpack16(xv[c], x);
+            unpack16(rv[c], z[c]);
+            ld_shared(coef + c * width, slots, f);
             if (kToken) {
-                pair g[4];
-                unpack8(gv[j], g);
+                pair g[8];
+                unpack16(gv[c], g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = mul2(c[e], g[e]);
+                for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], g[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                z[j][e] = fma2(kPost ? mul2(x[e], root) : x[e], c[e], mul2(z[j][e], alpha));
-                s = fma2(z[j][e], z[j][e], s);
+            for (int e = 0; e < 8; ++e) {
+                z[c][e] = fma2(kPost ? mul2(x[e], root) : x[e], f[e], mul2(z[c][e], alpha));
+                s = fma2(z[c][e], z[c][e], s);
             }
-            if (a.residual_out) st_v4(a.residual_out + at + (size_t)i * 8, pack8(z[j]));
+            if (a.residual_out) store16<k32>(a.residual_out + base + col, left, z[c]);
             if (a.weight) {
-                pair w[4];
-                unpack8(ld_weight(a.weight, i), w);
+                pair w[8];
+                unpack16(ld_weight(a.weight + col, left), w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    z[j][e] = mul2(z[j][e], w[e]);
-                    if (a.rows8) {
+                for (int e = 0; e < 8; ++e) z[c][e] = mul2(z[c][e], w[e]);
+                if (a.rows8)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
                         float lo, hi;
-                        split(z[j][e], lo, hi);
+                        split(z[c][e], lo, hi);
                         peak = max_nan(peak, max_nan(fabsf(lo), fabsf(hi)));
                     }
-                }
             }
         }
         row += gridDim.x;
         load();
         if (a.weight) {
-            sum = sum2(s);
-            block_reduce<true>(sum, peak, part[1][parity]);
-            const float r2 = 1.0f / sqrtf(sum * inv_h + a.eps);
-            peak *= r2;
-            const bool zero = peak < kZeroRow;  // false for NaN
-            const float inv = zero ? 0.0f : kLow8 / peak;
-            if (q && tid == 0) st_v4(q + H, make_uint4(__float_as_uint(zero ? 0.0f : peak / kLow8), 0, 0, 0));
+            const int lane = threadIdx.x & 31;
+            float *const peaks = part[1][parity][1];
+            if (a.rows8) {
+                peak = warp_peak(peak);
+                if (lane == 0) peaks[threadIdx.x >> 5] = peak;
+            }
+            float sum[1] = {sum2(s)};
+            block_sum<1>(sum, part[1][parity]);  // its barrier is the peaks', too
+            const float r2 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            const pair root2 = both(r2);
+            float inv = 0.0f;
+            if (a.rows8) {
+                peak = warp_peak(lane < (width >> 5) ? peaks[lane] : 0.0f) * r2;
+                const bool zero = peak < kZeroRow;  // false for NaN
+                inv = zero ? 0.0f : kLow8 / peak;
+                if (threadIdx.x == 0) st_v4(q + H, make_uint4(__float_as_uint(zero ? 0.0f : peak / kLow8), 0, 0, 0));
+            }
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int i = tid + j * width;
-                if (i >= nvec) continue;
+            for (int c = 0; c < C; ++c) {
+                const int col = (threadIdx.x + c * width) * kEach, left = H - col;
+                if (left <= 0) continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[j][e] = mul2(z[j][e], both(r2));
-                if (a.y) st_v4(a.y + at + (size_t)i * 8, pack8(z[j]));
-                if (q) {
-                    uint32_t b[4];
+                for (int e = 0; e < 8; ++e) z[c][e] = mul2(z[c][e], root2);
+                if (a.y) store16<k32>(a.y + base + col, left, z[c]);
+                if (q) {  // H is a multiple of 16
+                    uint32_t b[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         float lo, hi;
-                        split(mul2(z[j][e], both(inv)), lo, hi);
+                        split(mul2(z[c][e], both(inv)), lo, hi);
                         b[e] = e4m3x2(lo, hi);
                     }
-                    *reinterpret_cast<uint2 *>(q + (size_t)i * 8) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+                    st_v4(q + col, make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16));
                 }
             }
         }
@@ -271,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_kernel(const Blo
 // d_gate (times b and post) come, as the gate is the same for all of the block's rows; with a gate per token dz * gate * n.
 enum { kSumWeight, kSumBranch, kSums };
 
-// Rows of block b: consecutive, and of one rank where the gate is per rank and its products are summed.
+// Rows of block b: consecutive, and of one rank where the gate is per rank.
 __device__ __host__ inline void block_rows(const Geometry &g, bool per_rank, int blocks, int b, long long &first,
                                            long long &end) {
     const int parts = per_rank ? blocks / g.R : blocks;
@@ -285,17 +364,17 @@ __device__ __forceinline__ bool sum_branch(const BlockNormArgs &a) {
     return a.d_post || (a.d_gate && a.gate_kind != A2AV_GATE_TOKEN);
 }
 
-template <int V, int kThreads, int kBlocks, bool kPost, bool kToken>
+template <int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
 __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(const BlockNormArgs a, bool per_rank) {
-    extern __shared__ __align__(16) ulonglong2 coef[];  // then the sums, each [half of a vector][vector]
+    extern __shared__ __align__(16) ulonglong2 smem[];
     __shared__ float part[3][2][2][kMaxWarps];
-    const int H = a.g.H, nvec = H / 8, tid = threadIdx.x, width = blockDim.x;
-    const bool branch = sum_branch(a);
-    ulonglong2 *const acc = coef + 2 * nvec;
+    const int H = a.g.H, width = blockDim.x, col = threadIdx.x * kEach, left = H - col;
+    const bool branch = sum_branch(a), in = left > 0;
+    ulonglong2 *const coef = smem + threadIdx.x;
+    ulonglong2 *const acc[kSums] = {coef + 4 * width, coef + 8 * width};
     {
-        const pair zero[4] = {0, 0, 0, 0};
-        for (int i = tid; i < nvec; i += width)
-            for (int q = 0; q < kSums; ++q) st_shared(acc + q * 2 * nvec, nvec, i, zero);
+        const pair zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int q = 0; q < kSums; ++q) st_shared(acc[q], width, zero);
     }
     long long row, end;
     block_rows(a.g, per_rank, gridDim.x, blockIdx.x, row, end);
@@ -303,172 +382,143 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
     int parity = 0;
     const float inv_h = 1.0f / (float)H;
     const pair alpha = both(a.residual_scale);
-    const uint16_t *coef_of = nullptr;
-    bool coef_set = false;
+    if (row < end) set_coef<1>(a, kToken || !a.gate ? nullptr : gate_row(a, row), coef, width);
     for (; row < end; ++row) {
         if (!row_active(a, row)) continue;
-        const size_t at = (size_t)row * H;
-        const uint16_t *gate = kToken || !a.gate ? nullptr : gate_row(a, row);
-        if (!coef_set || gate != coef_of) {
-            set_coef(a, coef_of = gate, coef);
-            coef_set = true;
+        const size_t at = (size_t)row * H + col;
+        const Bits none = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
+        const Bits xv = in ? ld16<k32>(a.x + at, left) : none;
+        const Bits rv = in ? ld16<k32>(a.residual + at, left) : none;
+        const Bits dyv = in && a.d_y ? ld16<k32>(a.d_y + at, left) : none;
+        const Bits drv = in && a.d_residual_out ? ld16<k32>(a.d_residual_out + at, left) : none;
+        const Bits gv = kToken && in ? ld16<k32>(a.gate + at, left) : none;
+        if (row + 1 < end && threadIdx.x < 5) {  // the next row on its way into L2
+            const int t = threadIdx.x;
+            const uint16_t *from = t == 0   ? a.x
+                                   : t == 1 ? a.residual
+                                   : t == 2 ? a.d_y
+                                   : t == 3 ? a.d_residual_out
+                                   : kToken ? a.gate
+                                            : nullptr;
+            if (from) prefetch_row(from + (size_t)(row + 1) * H, 2 * H);
         }
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        uint4 xv[V], rv[V], dyv[V], drv[V], gv[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * width;
-            const bool in = i < nvec;
-            xv[j] = in ? ld_row(a.x + at + (size_t)i * 8) : none;
-            rv[j] = in ? ld_row(a.residual + at + (size_t)i * 8) : none;
-            dyv[j] = in && a.d_y ? ld_row(a.d_y + at + (size_t)i * 8) : none;
-            drv[j] = in && a.d_residual_out ? ld_row(a.d_residual_out + at + (size_t)i * 8) : none;
-            if (kToken) gv[j] = in ? ld_row(a.gate + at + (size_t)i * 8) : none;
-        }
-        if (row + 1 < end && tid < 5) {  // the next row on its way into L2
-            const uint16_t *from = tid == 0   ? a.x
-                                   : tid == 1 ? a.residual
-                                   : tid == 2 ? a.d_y
-                                   : tid == 3 ? a.d_residual_out
-                                   : kToken   ? a.gate
-                                              : nullptr;
-            if (from) prefetch_row(from + at + H, 2 * H);
-        }
-        float r1 = 1.0f, unused = 0.0f;
+        float r1 = 1.0f;
         if (kPost) {
-            pair s = both(0.0f);
+            pair x[8], s = both(0.0f);
+            unpack16(xv, x);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                pair x[4];
-                unpack8(xv[j], x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s = fma2(x[e], x[e], s);
-            }
-            float sum = sum2(s);
-            block_reduce<false>(sum, unused, part[0][parity]);
-            r1 = 1.0f / sqrtf(sum * inv_h + a.eps);
+            for (int e = 0; e < 8; ++e) s = fma2(x[e], x[e], s);
+            float sum[1] = {sum2(s)};
+            block_sum<1>(sum, part[0][parity]);
+            r1 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
         }
-        pair z[V][4], zz2 = both(0.0f), vz2 = both(0.0f);
         const pair root1 = both(r1);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * width;
-            if (i >= nvec) continue;
-            pair x[4], c[4];
-            unpack8(xv[j], x);
-            unpack8(rv[j], z[j]);
-            ld_shared(coef, nvec, i, c);
+        pair z[8], zz = both(0.0f), vz = both(0.0f);
+        if (in) {
+            pair x[8], f[8];
+            unpack16(xv, x);
+            unpack16(rv, z);
+            ld_shared(coef, width, f);
             if (kToken) {
-                pair g[4];
-                unpack8(gv[j], g);
+                pair g[8];
+                unpack16(gv, g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = mul2(c[e], g[e]);
+                for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], g[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                z[j][e] = fma2(kPost ? mul2(x[e], root1) : x[e], c[e], mul2(z[j][e], alpha));
-                zz2 = fma2(z[j][e], z[j][e], zz2);
+            for (int e = 0; e < 8; ++e) {
+                z[e] = fma2(kPost ? mul2(x[e], root1) : x[e], f[e], mul2(z[e], alpha));
+                zz = fma2(z[e], z[e], zz);
             }
             if (a.d_y) {
-                pair w[4], dy[4];
-                unpack8(ld_weight(a.weight, i), w);
-                unpack8(dyv[j], dy);
+                pair w[8], dy[8];
+                unpack16(ld_weight(a.weight + col, left), w);
+                unpack16(dyv, dy);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) vz2 = fma2(mul2(dy[e], w[e]), z[j][e], vz2);
+                for (int e = 0; e < 8; ++e) vz = fma2(mul2(dy[e], w[e]), z[e], vz);
             }
         }
         float r2 = 0.0f, c2 = 0.0f;
         if (a.d_y) {
-            float zz = sum2(zz2), vz = sum2(vz2);
-            block_reduce<false>(zz, vz, part[1][parity]);
-            r2 = 1.0f / sqrtf(zz * inv_h + a.eps);
-            c2 = r2 * r2 * r2 * (vz * inv_h);
+            float sum[2] = {sum2(zz), sum2(vz)};
+            block_sum<2>(sum, part[1][parity]);
+            r2 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            c2 = r2 * r2 * r2 * (sum[1] * inv_h);
         }
-        const pair root2 = both(r2), less2 = both(-c2);
-        pair nx2 = both(0.0f);
-        pair(&dn)[V][4] = z;  // z's place takes dz * coef: the gradient of n = x * r1
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * width;
-            if (i >= nvec) continue;
-            pair dz[4], x[4], c[4];
-            unpack8(drv[j], dz);
+        pair nx = both(0.0f);
+        pair(&dn)[8] = z;  // z's place takes dz * coef: the gradient of n = x * r1
+        if (in) {
+            pair dz[8], x[8], f[8], t[8];
+            unpack16(drv, dz);
             if (a.d_y) {
-                pair dy[4], w[4];
-                unpack8(dyv[j], dy);
+                const pair root2 = both(r2), less2 = both(-c2);
+                pair dy[8], w[8];
+                unpack16(dyv, dy);
                 if (a.d_weight) {
-                    pair t[4];
-                    ld_shared(acc + kSumWeight * 2 * nvec, nvec, i, t);
+                    ld_shared(acc[kSumWeight], width, t);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t[e] = fma2(dy[e], mul2(z[j][e], root2), t[e]);
-                    st_shared(acc + kSumWeight * 2 * nvec, nvec, i, t);
+                    for (int e = 0; e < 8; ++e) t[e] = fma2(dy[e], mul2(z[e], root2), t[e]);
+                    st_shared(acc[kSumWeight], width, t);
                 }
-                unpack8(ld_weight(a.weight, i), w);
+                unpack16(ld_weight(a.weight + col, left), w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dz[e] = fma2(less2, z[j][e], fma2(mul2(dy[e], w[e]), root2, dz[e]));
+                for (int e = 0; e < 8; ++e) dz[e] = fma2(less2, z[e], fma2(mul2(dy[e], w[e]), root2, dz[e]));
             }
-            {
-                pair t[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) t[e] = mul2(dz[e], alpha);
-                st_v4(a.d_residual + at + (size_t)i * 8, pack8(t));
-            }
-            unpack8(xv[j], x);
+            for (int e = 0; e < 8; ++e) t[e] = mul2(dz[e], alpha);
+            store16<k32>(a.d_residual + at, left, t);
+            unpack16(xv, x);
             if (branch) {
-                pair t[4], g[4];
-                ld_shared(acc + kSumBranch * 2 * nvec, nvec, i, t);
-                if (kToken) unpack8(gv[j], g);
+                pair g[8];
+                ld_shared(acc[kSumBranch], width, t);
+                if (kToken) unpack16(gv, g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 8; ++e)
                     t[e] = fma2(kToken ? mul2(dz[e], g[e]) : dz[e], kPost ? mul2(x[e], root1) : x[e], t[e]);
-                st_shared(acc + kSumBranch * 2 * nvec, nvec, i, t);
+                st_shared(acc[kSumBranch], width, t);
             }
-            ld_shared(coef, nvec, i, c);
+            ld_shared(coef, width, f);
             if (kToken) {
                 if (a.d_gate) {  // b * dz * u
-                    pair t[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t[e] = mul2(mul2(dz[e], c[e]), kPost ? mul2(x[e], root1) : x[e]);
-                    st_v4(static_cast<uint16_t *>(a.d_gate) + at + (size_t)i * 8, pack8(t));
+                    for (int e = 0; e < 8; ++e) t[e] = mul2(mul2(dz[e], f[e]), kPost ? mul2(x[e], root1) : x[e]);
+                    store16<k32>(static_cast<uint16_t *>(a.d_gate) + at, left, t);
                 }
-                pair g[4];
-                unpack8(gv[j], g);
+                pair g[8];
+                unpack16(gv, g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = mul2(c[e], g[e]);
+                for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], g[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dn[j][e] = mul2(dz[e], c[e]);
-                if (kPost) nx2 = fma2(dn[j][e], x[e], nx2);
+            for (int e = 0; e < 8; ++e) {
+                dn[e] = mul2(dz[e], f[e]);
+                if (kPost) nx = fma2(dn[e], x[e], nx);
             }
         }
         float c1 = 0.0f;
         if (kPost) {
-            float nx = sum2(nx2);
-            block_reduce<false>(nx, unused, part[2][parity]);
-            c1 = r1 * r1 * r1 * (nx * inv_h);
+            float sum[1] = {sum2(nx)};
+            block_sum<1>(sum, part[2][parity]);
+            c1 = r1 * r1 * r1 * (sum[0] * inv_h);
         }
-        const pair less1 = both(-c1);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * width;
-            if (i >= nvec) continue;
-            pair x[4];
-            unpack8(xv[j], x);
+        if (in) {
             if (kPost) {
+                const pair less1 = both(-c1);
+                pair x[8];
+                unpack16(xv, x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dn[j][e] = fma2(dn[j][e], root1, mul2(x[e], less1));
+                for (int e = 0; e < 8; ++e) dn[e] = fma2(dn[e], root1, mul2(x[e], less1));
             }
-            st_v4(a.d_x + at + (size_t)i * 8, pack8(dn[j]));
+            store16<k32>(a.d_x + at, left, dn);
         }
         parity ^= 1;
     }
-    for (int q = 0; q < kSums; ++q)
-        if (q == kSumWeight ? a.d_weight != nullptr : branch)
-            for (int i = tid; i < nvec; i += width) {
-                ulonglong2 *out = reinterpret_cast<ulonglong2 *>(a.scratch + ((size_t)blockIdx.x * kSums + q) * H) + 2 * i;
-                out[0] = acc[(q * 2) * nvec + i];
-                out[1] = acc[(q * 2 + 1) * nvec + i];
+    if (in)
+        for (int q = 0; q < kSums; ++q)
+            if (q == kSumWeight ? a.d_weight != nullptr : branch) {
+                ulonglong2 *out =
+                    reinterpret_cast<ulonglong2 *>(a.scratch + ((size_t)blockIdx.x * kSums + q) * H + col);
+                for (int e = 0; e < (left > 8 ? 4 : 2); ++e) out[e] = acc[q][e * width];
             }
 }
 
@@ -524,72 +574,84 @@ __global__ void __launch_bounds__(32 * kSumWarps) norm_sums_kernel(const BlockNo
     }
 }
 
-int row_threads(int H, int V) { return ((H / 8 + V - 1) / V + 31) / 32 * 32; }
+// Threads of a row, each with C times 16 values of it.
+int row_threads(int H, int C = 1) { return ((H + kEach * C - 1) / (kEach * C) + 31) / 32 * 32; }
 
-// Whether the gradient's blocks keep to a rank each.
-bool keeps_to_rank(const BlockNormArgs &a) {
-    return a.gate_kind == A2AV_GATE_RANK && (a.d_gate || a.d_post);
-}
-
-// Blocks of `threads` threads and `smem` bytes each that an SM holds, the kernels' registers allowing 1,024 threads.
+// Blocks of `threads` threads and `smem` bytes each that an SM holds, with 64 registers a thread.
 int blocks_per_sm(int threads, size_t smem) {
-    const int by_threads = threads > 512 ? 1 : 1024 / threads, by_smem = (int)(228 * 1024 / (smem + 3 * 1024));
+    const int by_threads = 1024 / threads, by_smem = (int)(228 * 1024 / (smem + 3 * 1024));
     const int n = by_threads < by_smem ? by_threads : by_smem;
     return n < 1 ? 1 : n > 16 ? 16 : n;
 }
-size_t coef_bytes(int H) { return (size_t)H * sizeof(float); }
+size_t coef_bytes(int H, int C = 1) { return (size_t)row_threads(H, C) * C * kEach * sizeof(float); }
 size_t grad_smem(int H) { return coef_bytes(H) * (1 + kSums); }
 
-// Blocks of the gradient: what the SMs hold, at most one per row, a multiple of R where each is to keep to a rank.
+// Blocks of the gradient: what the SMs hold, at most one per row, a multiple of R where each keeps to a rank.
 int grad_blocks(int num_sms, const Geometry &g, bool per_rank) {
     const long long rows = (long long)g.R * g.T;
-    const long long most = (long long)num_sms * blocks_per_sm(row_threads(g.H, kV), grad_smem(g.H));
+    const long long most = (long long)num_sms * blocks_per_sm(row_threads(g.H), grad_smem(g.H));
     if (!per_rank) return (int)(rows < most ? rows : most);
     const long long parts = most / g.R < 1 ? 1 : most / g.R;
     return g.R * (int)(g.T < parts ? g.T : parts);
 }
 
-template <int V, int kThreads, int kBlocks, bool kPost, bool kToken>
+// Every row of every tensor on 32 bytes.
+bool rows_on_32(const BlockNormArgs &a) {
+    const void *const tensors[] = {a.x, a.residual, a.residual_out, a.y, a.d_y, a.d_residual_out, a.d_x, a.d_residual,
+                                   a.gate_kind == A2AV_GATE_TOKEN ? a.gate : nullptr,
+                                   a.gate_kind == A2AV_GATE_TOKEN ? a.d_gate : nullptr};
+    uintptr_t bits = (uintptr_t)a.g.H * 2;
+    for (const void *t : tensors) bits |= reinterpret_cast<uintptr_t>(t);
+    return bits % 32 == 0;
+}
+
+template <int C, int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
 cudaError_t launch_norm(const a2av_plan_s &p, const BlockNormArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = block_norm_kernel<V, kThreads, kBlocks, kPost, kToken>;
-    const size_t smem = coef_bytes(a.g.H);
-    const cudaError_t e = allow_smem(kernel, done, p.cfg.device, coef_bytes(kMaxNormRow));
+    const auto kernel = block_norm_kernel<C, kThreads, kBlocks, kPost, kToken, k32>;
+    const size_t smem = coef_bytes(a.g.H, C);
+    const cudaError_t e = allow_smem(kernel, done, p.cfg.device, coef_bytes(kMaxNormRow, C));
     if (e != cudaSuccess) return e;
-    const int threads = row_threads(a.g.H, V);
+    const int threads = row_threads(a.g.H, C);
     const long long rows = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * blocks_per_sm(threads, smem);
     return launch_pdl(kernel, (int)(rows < cap ? rows : cap), threads, smem, s, a);
 }
 
-template <bool kPost, bool kToken>
+template <bool kPost, bool kToken, bool k32>
 cudaError_t launch_norm_rows(const a2av_plan_s &p, const BlockNormArgs &a, cudaStream_t s) {
-    if (a.g.H > 16384) return launch_norm<4, 1024, 1, kPost, kToken>(p, a, s);
-    if (a.g.H > 8192) return launch_norm<kV, 1024, 1, kPost, kToken>(p, a, s);
-    return launch_norm<kV, 512, 2, kPost, kToken>(p, a, s);
+    if (a.g.H > 16384) return launch_norm<2, 1024, 1, kPost, kToken, k32>(p, a, s);
+    if (a.g.H > 8192) return launch_norm<1, 1024, 1, kPost, kToken, k32>(p, a, s);
+    return launch_norm<1, 512, 2, kPost, kToken, k32>(p, a, s);
 }
 
-template <int V, int kThreads, int kBlocks, bool kPost, bool kToken>
-cudaError_t launch_grad(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, bool per_rank, cudaStream_t s) {
+template <int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
+cudaError_t launch_grad(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = block_norm_grad_kernel<V, kThreads, kBlocks, kPost, kToken>;
+    const auto kernel = block_norm_grad_kernel<kThreads, kBlocks, kPost, kToken, k32>;
     const cudaError_t e = allow_smem(kernel, done, p.cfg.device, grad_smem(kMaxNormGradRow));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, blocks, row_threads(a.g.H, V), grad_smem(a.g.H), s, a, per_rank);
+    return launch_pdl(kernel, blocks, row_threads(a.g.H), grad_smem(a.g.H), s, a, a.gate_kind == A2AV_GATE_RANK);
 }
 
-template <bool kPost, bool kToken>
-cudaError_t launch_grad_rows(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, bool per_rank, cudaStream_t s) {
-    if (a.g.H > 8192) return launch_grad<kV, 1024, 1, kPost, kToken>(p, a, blocks, per_rank, s);
-    if (a.g.H > 7168) return launch_grad<kV, 512, 2, kPost, kToken>(p, a, blocks, per_rank, s);
-    return launch_grad<kV, 448, 2, kPost, kToken>(p, a, blocks, per_rank, s);  // room for 72 registers
+template <bool kPost, bool kToken, bool k32>
+cudaError_t launch_grad_rows(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, cudaStream_t s) {
+    if (a.g.H > 8192) return launch_grad<1024, 1, kPost, kToken, k32>(p, a, blocks, s);
+    if (a.g.H > 7168) return launch_grad<512, 2, kPost, kToken, k32>(p, a, blocks, s);
+    return launch_grad<448, 2, kPost, kToken, k32>(p, a, blocks, s);  // room for 72 registers
 }
+
+// f<kPost, kToken, k32>, by what the call has.
+#define A2AV_FORMS(f, ...)                                                                                     \
+    (a.post ? (token ? (wide ? f<true, true, true>(__VA_ARGS__) : f<true, true, false>(__VA_ARGS__))           \
+                     : (wide ? f<true, false, true>(__VA_ARGS__) : f<true, false, false>(__VA_ARGS__)))        \
+            : (token ? (wide ? f<false, true, true>(__VA_ARGS__) : f<false, true, false>(__VA_ARGS__))         \
+                     : (wide ? f<false, false, true>(__VA_ARGS__) : f<false, false, false>(__VA_ARGS__))))
 
 }  // namespace
 
 cudaError_t launch_block_norm(const a2av_plan_s &p, const BlockNormArgs &a, cudaStream_t s) {
-    const bool token = a.gate_kind == A2AV_GATE_TOKEN;
-    if (a.post) return token ? launch_norm_rows<true, true>(p, a, s) : launch_norm_rows<true, false>(p, a, s);
-    return token ? launch_norm_rows<false, true>(p, a, s) : launch_norm_rows<false, false>(p, a, s);
+    const bool token = a.gate_kind == A2AV_GATE_TOKEN, wide = rows_on_32(a);
+    return A2AV_FORMS(launch_norm_rows, p, a, s);
 }
 
 int64_t norm_scratch_bytes(const a2av_plan_s &p) {
@@ -598,14 +660,10 @@ int64_t norm_scratch_bytes(const a2av_plan_s &p) {
 }
 
 cudaError_t launch_block_norm_grad(const a2av_plan_s &p, const BlockNormArgs &a, cudaStream_t s, int64_t &launches) {
-    const bool per_rank = keeps_to_rank(a);
-    const bool sums = a.d_weight || a.d_post || (a.d_gate && a.gate_kind != A2AV_GATE_TOKEN);
+    const bool token = a.gate_kind == A2AV_GATE_TOKEN, per_rank = a.gate_kind == A2AV_GATE_RANK, wide = rows_on_32(a);
+    const bool sums = a.d_weight || a.d_post || (a.d_gate && !token);
     const int blocks = grad_blocks(p.num_sms, a.g, per_rank);
-    const bool token = a.gate_kind == A2AV_GATE_TOKEN;
-    cudaError_t e = a.post ? (token ? launch_grad_rows<true, true>(p, a, blocks, per_rank, s)
-                                    : launch_grad_rows<true, false>(p, a, blocks, per_rank, s))
-                           : (token ? launch_grad_rows<false, true>(p, a, blocks, per_rank, s)
-                                    : launch_grad_rows<false, false>(p, a, blocks, per_rank, s));
+    cudaError_t e = A2AV_FORMS(launch_grad_rows, p, a, blocks, s);
     if (e != cudaSuccess) return e;
     ++launches;
     if (!sums) return cudaSuccess;
