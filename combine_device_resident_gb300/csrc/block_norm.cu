@@ -24,7 +24,8 @@
 namespace a2av {
 namespace {
 
-constexpr int kMaxWarps = 32;
+// Warps of a block's row, as block_sum counts them.
+constexpr int warps_of(int threads) { return threads <= 512 ? 16 : 32; }
 
 __device__ __forceinline__ bool row_active(const BlockNormArgs &a, long long row) {
     if (!a.num_tokens) return true;
@@ -92,11 +93,11 @@ __device__ __forceinline__ void prefetch_row(const void *p, uint32_t bytes) {
 }
 
 // Sums of N values over the block, of which every thread gets all.  With two, a warp's halves take one each, so both cost
-// little more than one.  `part` is free again after the next barrier.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[kMaxWarps]) {
-    static_assert(N == 1 || N == 2, "values");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+// little more than one.  `part` holds zeros where there is no warp, and is free again after the next barrier.
+template <int N, int W>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[W]) {
+    static_assert((N == 1 || N == 2) && (W == 16 || W == 32), "values, warps");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kLanes = 32 / N;  // that carry a value: lane / kLanes names it
     float s = v[0];
     if constexpr (N == 2) {
@@ -107,16 +108,19 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[kMaxWarps
     for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((lane & (kLanes - 1)) == 0) part[lane / kLanes][warp] = s;
     __syncthreads();
-    s = 0.0f;
+    // a lane reads four warps' sums
+    const float4 p = reinterpret_cast<const float4 *>(part[lane / kLanes])[lane & (W / 4 - 1)];
+    s = (p.x + p.y) + (p.z + p.w);
 #pragma unroll
-    for (int w = 0; w < kMaxWarps; w += kLanes) {
-        const int from = w + (lane & (kLanes - 1));
-        if (from < nwarps) s += part[lane / kLanes][from];
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = W / 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] = N == 1 ? s : __shfl_sync(0xffffffffu, s, n * kLanes);
+}
+// Zeros for block_sum; ends in a barrier.
+template <int n>
+__device__ __forceinline__ void clear_parts(float (&part)[n]) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) part[i] = 0.0f;
+    __syncthreads();
 }
 
 // Largest magnitude of a warp's values, NaN if there is one.
@@ -169,6 +173,25 @@ __device__ __forceinline__ void unpack16(const Bits &b, pair (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = both(lo_f(w[i]), hi_f(w[i]));
 }
+// Makes the compiler unpack these anew where they are used next: held unpacked over a block's sum they would cost twice
+// the registers.
+__device__ __forceinline__ void keep_packed(Bits &b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm volatile("" : "+r"(b.v[i].x), "+r"(b.v[i].y), "+r"(b.v[i].z), "+r"(b.v[i].w));
+}
+// Four of them.
+__device__ __forceinline__ void unpack4(const Bits &b, int q, pair (&f)[2]) {
+    const uint4 &v = b.v[q / 2];
+    const uint32_t lo = q % 2 ? v.z : v.x, hi = q % 2 ? v.w : v.y;
+    f[0] = both(lo_f(lo), hi_f(lo));
+    f[1] = both(lo_f(hi), hi_f(hi));
+}
+__device__ __forceinline__ void scale4(pair (&f)[2], const Bits &b, int q) {
+    pair g[2];
+    unpack4(b, q, g);
+    f[0] = mul2(f[0], g[0]);
+    f[1] = mul2(f[1], g[1]);
+}
 template <bool k32>
 __device__ __forceinline__ void store16(uint16_t *p, int left, const pair (&f)[8]) {
     st16<k32>(p, left, make_uint4(bf16_of(f[0]), bf16_of(f[1]), bf16_of(f[2]), bf16_of(f[3])),
@@ -188,6 +211,14 @@ __device__ __forceinline__ void ld_shared(const ulonglong2 *row, int slots, pair
 __device__ __forceinline__ void st_shared(ulonglong2 *row, int slots, const pair (&f)[8]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) row[q * slots] = make_ulonglong2(f[2 * q], f[2 * q + 1]);
+}
+
+__device__ __forceinline__ void ld_quarter(const ulonglong2 *row, int slots, int q, pair (&f)[2]) {
+    const ulonglong2 v = row[q * slots];
+    f[0] = v.x, f[1] = v.y;
+}
+__device__ __forceinline__ void st_quarter(ulonglong2 *row, int slots, int q, const pair (&f)[2]) {
+    row[q * slots] = make_ulonglong2(f[0], f[1]);
 }
 
 // The factor of x * r1 in z, per channel: branch_scale * post * gate, the gate left out where it is the token's own
@@ -219,16 +250,20 @@ __device__ __forceinline__ void set_coef(const BlockNormArgs &a, const uint16_t 
 template <int C, int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
 __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_kernel(const BlockNormArgs a) {
     extern __shared__ __align__(16) ulonglong2 smem[];
-    __shared__ float part[2][2][2][kMaxWarps];  // [which sum][row parity]
+    constexpr int W = warps_of(kThreads);
+    __shared__ __align__(16) float parts[2 * 2 * 2 * W];
+    auto part = reinterpret_cast<float(*)[2][2][W]>(parts);  // [which sum][row parity]
+    clear_parts(parts);
     const int H = a.g.H, width = blockDim.x, slots = C * width;
     ulonglong2 *const coef = smem + threadIdx.x;
     const long long rows = (long long)a.g.R * a.g.T;
     const float inv_h = 1.0f / (float)H;
     const pair alpha = both(a.residual_scale);
-    const Bits none = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
     grid_dependency_wait();
     int parity = 0;
     Bits xv[C], rv[C], gv[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) xv[c] = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};  // behind the row's end
     long long row = blockIdx.x;
     auto load = [&] {  // from the first row on that takes part
         while (row < rows && !row_active(a, row)) row += gridDim.x;
@@ -237,9 +272,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_kernel(const Blo
         for (int c = 0; c < C; ++c) {
             const int col = (threadIdx.x + c * width) * kEach, left = H - col;
             const size_t at = (size_t)row * H + col;
-            xv[c] = left > 0 ? ld16<k32>(a.x + at, left) : none;
-            rv[c] = left > 0 ? ld16<k32>(a.residual + at, left) : none;
-            if (kToken) gv[c] = left > 0 ? ld16<k32>(a.gate + at, left) : none;
+            if (left <= 0) continue;
+            xv[c] = ld16<k32>(a.x + at, left);
+            rv[c] = ld16<k32>(a.residual + at, left);
+            if (kToken) gv[c] = ld16<k32>(a.gate + at, left);
         }
     };
     load();
@@ -262,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_kernel(const Blo
                 for (int e = 0; e < 8; ++e) s = fma2(x[e], x[e], s);
             }
             float sum[1] = {sum2(s)};
-            block_sum<1>(sum, part[0][parity]);
-            r1 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            block_sum<1, W>(sum, part[0][parity]);
+            r1 = rsqrtf(fmaf(sum[0], inv_h, a.eps));
         }
         pair s = both(0.0f);
         const pair root = both(r1);
@@ -311,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_kernel(const Blo
                 if (lane == 0) peaks[threadIdx.x >> 5] = peak;
             }
             float sum[1] = {sum2(s)};
-            block_sum<1>(sum, part[1][parity]);  // its barrier is the peaks', too
-            const float r2 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            block_sum<1, W>(sum, part[1][parity]);  // its barrier is the peaks', too
+            const float r2 = rsqrtf(fmaf(sum[0], inv_h, a.eps));
             const pair root2 = both(r2);
             float inv = 0.0f;
             if (a.rows8) {
@@ -360,6 +396,9 @@ __device__ __host__ inline void block_rows(const Geometry &g, bool per_rank, int
     end = rank * rows + rows * (c + 1) / parts;
 }
 
+// Rows of up to 7168 leave room in shared memory for the weights in fp32 beside two blocks' sums.
+constexpr bool weight_shared(int threads) { return threads <= 448; }
+
 __device__ __forceinline__ bool sum_branch(const BlockNormArgs &a) {
     return a.d_post || (a.d_gate && a.gate_kind != A2AV_GATE_TOKEN);
 }
@@ -367,11 +406,18 @@ __device__ __forceinline__ bool sum_branch(const BlockNormArgs &a) {
 template <int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
 __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(const BlockNormArgs a, bool per_rank) {
     extern __shared__ __align__(16) ulonglong2 smem[];
-    __shared__ float part[3][2][2][kMaxWarps];
-    const int H = a.g.H, width = blockDim.x, col = threadIdx.x * kEach, left = H - col;
-    const bool branch = sum_branch(a), in = left > 0;
+    constexpr int W = warps_of(kThreads);
+    __shared__ __align__(16) float parts[3 * 2 * 2 * W];
+    auto part = reinterpret_cast<float(*)[2][2][W]>(parts);  // [which sum][row parity]
+    clear_parts(parts);
+    const int H = a.g.H, width = blockDim.x;
+    const bool branch = sum_branch(a), in = (int)threadIdx.x * kEach < H;
+    // a thread behind the row's end loads what the first one does and takes no part in sums and stores
+    const int col = in ? threadIdx.x * kEach : 0, left = H - col;
     ulonglong2 *const coef = smem + threadIdx.x;
     ulonglong2 *const acc[kSums] = {coef + 4 * width, coef + 8 * width};
+    constexpr bool kWeightShared = weight_shared(kThreads);
+    ulonglong2 *const weight32 = coef + 12 * width;  // the next norm's weights, unpacked, where there is room
     {
         const pair zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int q = 0; q < kSums; ++q) st_shared(acc[q], width, zero);
@@ -383,15 +429,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
     const float inv_h = 1.0f / (float)H;
     const pair alpha = both(a.residual_scale);
     if (row < end) set_coef<1>(a, kToken || !a.gate ? nullptr : gate_row(a, row), coef, width);
+    if (kWeightShared && a.d_y) {
+        pair w[8];
+        unpack16(ld_weight(a.weight + col, left), w);
+        st_shared(weight32, width, w);
+    }
+    const uint16_t *const weight = a.weight + col;
     for (; row < end; ++row) {
         if (!row_active(a, row)) continue;
         const size_t at = (size_t)row * H + col;
-        const Bits none = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
-        const Bits xv = in ? ld16<k32>(a.x + at, left) : none;
-        const Bits rv = in ? ld16<k32>(a.residual + at, left) : none;
-        const Bits dyv = in && a.d_y ? ld16<k32>(a.d_y + at, left) : none;
-        const Bits drv = in && a.d_residual_out ? ld16<k32>(a.d_residual_out + at, left) : none;
-        const Bits gv = kToken && in ? ld16<k32>(a.gate + at, left) : none;
+        Bits xv, rv, dyv, drv, gv;
+        xv = ld16<k32>(a.x + at, left);
+        rv = ld16<k32>(a.residual + at, left);
+        if (a.d_y) dyv = ld16<k32>(a.d_y + at, left);
+        if (a.d_residual_out) drv = ld16<k32>(a.d_residual_out + at, left);
+        else drv = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
+        if (kToken) gv = ld16<k32>(a.gate + at, left);
         if (row + 1 < end && threadIdx.x < 5) {  // the next row on its way into L2
             const int t = threadIdx.x;
             const uint16_t *from = t == 0   ? a.x
@@ -408,106 +461,120 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
             unpack16(xv, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s = fma2(x[e], x[e], s);
-            float sum[1] = {sum2(s)};
-            block_sum<1>(sum, part[0][parity]);
-            r1 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            float sum[1] = {in ? sum2(s) : 0.0f};
+            block_sum<1, W>(sum, part[0][parity]);
+            r1 = rsqrtf(fmaf(sum[0], inv_h, a.eps));
+            keep_packed(xv);
         }
         const pair root1 = both(r1);
         pair z[8], zz = both(0.0f), vz = both(0.0f);
-        if (in) {
-            pair x[8], f[8];
-            unpack16(xv, x);
-            unpack16(rv, z);
-            ld_shared(coef, width, f);
-            if (kToken) {
-                pair g[8];
-                unpack16(gv, g);
+        {
+            Bits wv;
+            if (!kWeightShared && a.d_y) wv = ld_weight(weight, left);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], g[e]);
-            }
+            for (int q = 0; q < 4; ++q) {  // four values at a time: what they need is soon free again
+                pair x[2], f[2], r[2], dy[2], w[2];
+                unpack4(xv, q, x);
+                unpack4(rv, q, r);
+                ld_quarter(coef, width, q, f);
+                if (kToken) scale4(f, gv, q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                z[e] = fma2(kPost ? mul2(x[e], root1) : x[e], f[e], mul2(z[e], alpha));
-                zz = fma2(z[e], z[e], zz);
-            }
-            if (a.d_y) {
-                pair w[8], dy[8];
-                unpack16(ld_weight(a.weight + col, left), w);
-                unpack16(dyv, dy);
+                for (int e = 0; e < 2; ++e) {
+                    z[2 * q + e] = fma2(kPost ? mul2(x[e], root1) : x[e], f[e], mul2(r[e], alpha));
+                    zz = fma2(z[2 * q + e], z[2 * q + e], zz);
+                }
+                if (a.d_y) {
+                    if (kWeightShared) ld_quarter(weight32, width, q, w);
+                    else unpack4(wv, q, w);
+                    unpack4(dyv, q, dy);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) vz = fma2(mul2(dy[e], w[e]), z[e], vz);
+                    for (int e = 0; e < 2; ++e) vz = fma2(mul2(dy[e], w[e]), z[2 * q + e], vz);
+                }
             }
         }
         float r2 = 0.0f, c2 = 0.0f;
         if (a.d_y) {
-            float sum[2] = {sum2(zz), sum2(vz)};
-            block_sum<2>(sum, part[1][parity]);
-            r2 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            float sum[2] = {in ? sum2(zz) : 0.0f, in ? sum2(vz) : 0.0f};
+            block_sum<2, W>(sum, part[1][parity]);
+            r2 = rsqrtf(fmaf(sum[0], inv_h, a.eps));
             c2 = r2 * r2 * r2 * (sum[1] * inv_h);
+            keep_packed(xv);
+            keep_packed(dyv);
+            if (kToken) keep_packed(gv);
         }
         pair nx = both(0.0f);
         pair(&dn)[8] = z;  // z's place takes dz * coef: the gradient of n = x * r1
         if (in) {
-            pair dz[8], x[8], f[8], t[8];
-            unpack16(drv, dz);
-            if (a.d_y) {
-                const pair root2 = both(r2), less2 = both(-c2);
-                pair dy[8], w[8];
-                unpack16(dyv, dy);
-                if (a.d_weight) {
-                    ld_shared(acc[kSumWeight], width, t);
+            const pair root2 = both(r2), less2 = both(-c2);
+            Bits wv;
+            uint32_t dr[8], dg[8];
+            if (!kWeightShared && a.d_y) wv = ld_weight(weight, left);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) t[e] = fma2(dy[e], mul2(z[e], root2), t[e]);
-                    st_shared(acc[kSumWeight], width, t);
+            for (int q = 0; q < 4; ++q) {
+                pair dz[2], x[2], n[2], f[2], t[2];
+                unpack4(drv, q, dz);
+                if (a.d_y) {
+                    pair dy[2], w[2];
+                    unpack4(dyv, q, dy);
+                    if (kWeightShared) ld_quarter(weight32, width, q, w);
+                    else unpack4(wv, q, w);
+                    if (a.d_weight) {
+                        ld_quarter(acc[kSumWeight], width, q, t);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) t[e] = fma2(dy[e], mul2(z[2 * q + e], root2), t[e]);
+                        st_quarter(acc[kSumWeight], width, q, t);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) dz[e] = fma2(less2, z[2 * q + e], fma2(mul2(dy[e], w[e]), root2, dz[e]));
                 }
-                unpack16(ld_weight(a.weight + col, left), w);
+                unpack4(xv, q, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dz[e] = fma2(less2, z[e], fma2(mul2(dy[e], w[e]), root2, dz[e]));
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = mul2(dz[e], alpha);
-            store16<k32>(a.d_residual + at, left, t);
-            unpack16(xv, x);
-            if (branch) {
-                pair g[8];
-                ld_shared(acc[kSumBranch], width, t);
-                if (kToken) unpack16(gv, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[e] = fma2(kToken ? mul2(dz[e], g[e]) : dz[e], kPost ? mul2(x[e], root1) : x[e], t[e]);
-                st_shared(acc[kSumBranch], width, t);
-            }
-            ld_shared(coef, width, f);
-            if (kToken) {
-                if (a.d_gate) {  // b * dz * u
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) t[e] = mul2(mul2(dz[e], f[e]), kPost ? mul2(x[e], root1) : x[e]);
-                    store16<k32>(static_cast<uint16_t *>(a.d_gate) + at, left, t);
+                for (int e = 0; e < 2; ++e) {
+                    dr[2 * q + e] = bf16_of(mul2(dz[e], alpha));
+                    n[e] = kPost ? mul2(x[e], root1) : x[e];
                 }
-                pair g[8];
-                unpack16(gv, g);
+                ld_quarter(coef, width, q, f);
+                if (kToken) {  // b * dz * u
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], g[e]);
-            }
+                    for (int e = 0; e < 2; ++e) dg[2 * q + e] = bf16_of(mul2(mul2(dz[e], f[e]), n[e]));
+                    scale4(f, gv, q);
+                }
+                if (branch) {
+                    pair d[2] = {dz[0], dz[1]};
+                    if (kToken) scale4(d, gv, q);
+                    ld_quarter(acc[kSumBranch], width, q, t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dn[e] = mul2(dz[e], f[e]);
-                if (kPost) nx = fma2(dn[e], x[e], nx);
+                    for (int e = 0; e < 2; ++e) t[e] = fma2(d[e], n[e], t[e]);
+                    st_quarter(acc[kSumBranch], width, q, t);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    dn[2 * q + e] = mul2(dz[e], f[e]);
+                    if (kPost) nx = fma2(dn[2 * q + e], x[e], nx);
+                }
             }
+            st16<k32>(a.d_residual + at, left, make_uint4(dr[0], dr[1], dr[2], dr[3]), make_uint4(dr[4], dr[5], dr[6], dr[7]));
+            if (kToken && a.d_gate)
+                st16<k32>(static_cast<uint16_t *>(a.d_gate) + at, left, make_uint4(dg[0], dg[1], dg[2], dg[3]),
+                          make_uint4(dg[4], dg[5], dg[6], dg[7]));
         }
         float c1 = 0.0f;
         if (kPost) {
             float sum[1] = {sum2(nx)};
-            block_sum<1>(sum, part[2][parity]);
+            block_sum<1, W>(sum, part[2][parity]);
             c1 = r1 * r1 * r1 * (sum[0] * inv_h);
+            keep_packed(xv);
         }
         if (in) {
             if (kPost) {
                 const pair less1 = both(-c1);
-                pair x[8];
-                unpack16(xv, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dn[e] = fma2(dn[e], root1, mul2(x[e], less1));
+                for (int q = 0; q < 4; ++q) {
+                    pair x[2];
+                    unpack4(xv, q, x);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) dn[2 * q + e] = fma2(dn[2 * q + e], root1, mul2(x[e], less1));
+                }
             }
             store16<k32>(a.d_x + at, left, dn);
         }
@@ -579,12 +646,12 @@ int row_threads(int H, int C = 1) { return ((H + kEach * C - 1) / (kEach * C) + 
 
 // Blocks of `threads` threads and `smem` bytes each that an SM holds, with 64 registers a thread.
 int blocks_per_sm(int threads, size_t smem) {
-    const int by_threads = 1024 / threads, by_smem = (int)(228 * 1024 / (smem + 3 * 1024));
+    const int by_threads = 1024 / threads, by_smem = (int)(228 * 1024 / (smem + 2 * 1024));  // static ones, and 1 KiB of the system's
     const int n = by_threads < by_smem ? by_threads : by_smem;
     return n < 1 ? 1 : n > 16 ? 16 : n;
 }
 size_t coef_bytes(int H, int C = 1) { return (size_t)row_threads(H, C) * C * kEach * sizeof(float); }
-size_t grad_smem(int H) { return coef_bytes(H) * (1 + kSums); }
+size_t grad_smem(int H) { return coef_bytes(H) * (1 + kSums + weight_shared(row_threads(H))); }
 
 // Blocks of the gradient: what the SMs hold, at most one per row, a multiple of R where each keeps to a rank.
 int grad_blocks(int num_sms, const Geometry &g, bool per_rank) {
@@ -637,7 +704,7 @@ template <bool kPost, bool kToken, bool k32>
 cudaError_t launch_grad_rows(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, cudaStream_t s) {
     if (a.g.H > 8192) return launch_grad<1024, 1, kPost, kToken, k32>(p, a, blocks, s);
     if (a.g.H > 7168) return launch_grad<512, 2, kPost, kToken, k32>(p, a, blocks, s);
-    return launch_grad<448, 2, kPost, kToken, k32>(p, a, blocks, s);  // room for 72 registers
+    return launch_grad<448, 2, kPost, kToken, k32>(p, a, blocks, s);  // room for 72 registers a thread
 }
 
 // f<kPost, kToken, k32>, by what the call has.
