@@ -11,9 +11,9 @@
 // the logits' own and needs no such care; the groups' does when two scores are
 // added.
 //
-// Warp kernel: one warp per token, the choices in shared memory.  k rounds of
-// a scan and two warp reductions; a further round looks at the best one left
-// out.
+// Warp kernel (any shape): one warp per token, the choices in shared memory.  k
+// rounds of a scan and two warp reductions; a further round looks at the best
+// one left out.  Lane kernel (E up to 256, k up to 8): four lanes per token, below.
 #include <float.h>
 
 #include "block_ops.cuh"
@@ -287,6 +287,427 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const ScoreAr
         if (token_active(a.num_tokens, a.g.T, (int)u)) route_one(a, u, room, lane);
 }
 
+// ---- lane kernel ------------------------------------------------------------------
+//
+// Four lanes per token, eight tokens per warp.  Lane r of a token holds the 16-byte units r, r + 4, ... of its row in
+// registers (NU of them), so every loop over logits is unrolled and none is read twice.  In order:
+//   1. choices in place of logits; a copy of them in shared memory, for the few that are looked up by number later;
+//   2. groups: two best per lane and group, merged so that lane r ends with groups r, r + 4; ranks by counting;
+//   3. tau, a lower bound of the KMAX-th largest choice: the KMAX-th largest of maxima of disjoint sets (a lane's kept
+//      groups, or its units' components), as in the plain router's lane kernel;
+//   4. the choices at or above tau (some ten of 256 for KMAX = 8) as bits, then as a list in shared memory;
+//   5. each one's rank by counting those at or above it, a lane taking every fourth; ranks below k are the answer.
+// A tie leaves a rank empty, and near neighbours are seen: the warp then orders that token's list in 64 bits (with a bias
+// tau is lowered by the choices' errors, so that the list holds whatever may lie at the border).  A list that is too
+// long, or groups that are too near: route_one.
+constexpr int kList = 32;  // candidates of a token
+constexpr int kRanks = 12;
+
+template <int KMAX>
+constexpr int tau_values() {  // that a lane gives to the bound
+    return KMAX >= 4 ? KMAX / 2 : 1;
+}
+
+__device__ __forceinline__ void order2(float &a, float &b) {
+    const float hi = fmaxf(a, b), lo = fminf(a, b);
+    a = hi;
+    b = lo;
+}
+__device__ __forceinline__ void sort4(float (&v)[4]) {
+    order2(v[0], v[1]);
+    order2(v[2], v[3]);
+    order2(v[0], v[2]);
+    order2(v[1], v[3]);
+    order2(v[1], v[2]);
+}
+// The KMAX-th largest of what the token's four lanes give, sorted in descending order each.
+template <int KMAX>
+__device__ __forceinline__ float bound_of(const float (&g)[tau_values<KMAX>()]) {
+    if constexpr (KMAX <= 2) {
+        float a = g[0], b = __shfl_xor_sync(kAll, a, 1);
+        order2(a, b);
+        const float c = __shfl_xor_sync(kAll, a, 2), d = __shfl_xor_sync(kAll, b, 2);
+        return KMAX == 1 ? fmaxf(a, c) : fmaxf(fminf(a, c), fmaxf(b, d));
+    } else {
+        constexpr int L = KMAX / 2;
+        float c[KMAX];  // two lanes' values, mine and then the other's reversed: bitonic, to be sorted
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            c[i] = g[i];
+            c[KMAX - 1 - i] = __shfl_xor_sync(kAll, g[i], 1);
+        }
+#pragma unroll
+        for (int d = L; d >= 1; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < KMAX; ++j)
+                if ((j & d) == 0) order2(c[j], c[j + d]);
+        float t = INFINITY;  // of two sorted lists of K, the K-th largest is min_i max(A_i, B_{K-1-i})
+#pragma unroll
+        for (int i = 0; i < KMAX; ++i) t = fminf(t, fmaxf(c[i], __shfl_xor_sync(kAll, c[KMAX - 1 - i], 2)));
+        return t;
+    }
+}
+
+// Row stride of the choices in shared memory, in 16-byte units: 4 mod 8, so that the eight lanes of two tokens lie on
+// different banks.
+__host__ __device__ constexpr int lane_stride(int E) { return (E / 4 + 7) / 8 * 8 + 4; }
+struct LaneList {
+    float key[8][kList + 4];  // candidates of the eight tokens, NaN behind them
+    int32_t id[8][kList];
+    float best[8][kRanks];  // by rank; NaN where there is none
+    int32_t best_id[8][kRanks];
+};
+// A warp's share: the choices of eight tokens (also room for the warp kernel's token), the lists.
+__host__ __device__ constexpr size_t lane_warp_bytes(int E) { return (size_t)8 * lane_stride(E) * 16 + sizeof(LaneList); }
+
+__device__ __forceinline__ float &part_of(float4 &v, int c) { return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w; }
+// Two best of what two sides have.
+__device__ __forceinline__ void merge2(float &a1, float &a2, float b1, float b2) {
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+}
+__device__ __forceinline__ float token_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(kAll, v, 1));
+    return fmaxf(v, __shfl_xor_sync(kAll, v, 2));
+}
+__device__ __forceinline__ float token_sum(float v) {
+    v += __shfl_xor_sync(kAll, v, 1);
+    return v + __shfl_xor_sync(kAll, v, 2);
+}
+
+// The n candidates of token u (its list's slot t), ordered in 64 bits by the whole warp.
+__device__ __noinline__ void route_list(const ScoreArgs &a, int u, LaneList &list, int t, int n, int lane) {
+    const float *l = a.logits + (size_t)u * a.g.E;
+    const int id = lane < n ? list.id[t][lane] : 0;
+    const float v = clean_logit(__ldg(l + id));
+    float m = 0.0f, zf = 1.0f;
+    double z = 1.0;
+    if (!a.sigmoid && (a.bias || !a.renorm)) {
+        m = -FLT_MAX;
+        for (int e = lane; e < a.g.E; e += 32) m = fmaxf(m, clean_logit(__ldg(l + e)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        z = 0.0;
+        for (int e = lane; e < a.g.E; e += 32) z += exp((double)clean_logit(__ldg(l + e)) - (double)m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+        zf = (float)z;
+    }
+    double c = a.bias ? fmax(exact_score(a.sigmoid, v, m, z) + (double)__ldg(a.bias + id), -(double)INFINITY) : (double)v;
+    c += 0.0;
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double other = __shfl_sync(kAll, c, i);
+        const int other_id = __shfl_sync(kAll, id, i);
+        rank += other > c || (other == c && other_id < id);
+    }
+    if (lane < n && rank < a.g.k) list.best_id[t][rank] = id;
+    __syncwarp();
+    const bool in = lane < a.g.k;
+    const int chosen = in ? list.best_id[t][lane] : 0;
+    const float g = chosen_gate(a, in ? clean_logit(__ldg(l + chosen)) : 0.0f, in, m, zf);
+    if (in) {
+        a.idx[(size_t)u * a.g.k + lane] = chosen;
+        a.gate[(size_t)u * a.g.k + lane] = g;
+    }
+    __syncwarp();
+}
+
+template <int NU, int KMAX, int G>
+__global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const ScoreArgs a) {
+    extern __shared__ __align__(16) unsigned char sm[];
+    constexpr int L = tau_values<KMAX>();
+    const int E = a.g.E, k = a.g.k, nu = E / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nwarps = blockDim.x >> 5, t = lane >> 2, r = lane & 3, stride = lane_stride(E);
+    float4 *const bias4 = reinterpret_cast<float4 *>(sm);  // a NaN as -infinity
+    unsigned char *const mine = sm + (a.bias ? (size_t)E * 4 : 0) + warp * lane_warp_bytes(E);
+    float4 *const keys4 = reinterpret_cast<float4 *>(mine) + t * stride;
+    LaneList &list = *reinterpret_cast<LaneList *>(mine + (size_t)8 * stride * 16);
+    grid_dependency_wait();
+    if (a.bias) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) reinterpret_cast<float *>(sm)[e] = clean_choice(__ldg(a.bias + e));
+        __syncthreads();
+    }
+    const int ntok = a.g.R * a.g.T, ntask = (int)(((long long)ntok + 7) / 8);
+    for (int task = blockIdx.x * nwarps + warp; task < ntask; task += gridDim.x * nwarps) {
+        const long long u = (long long)task * 8 + t;
+        const bool act = u < ntok && token_active(a.num_tokens, a.g.T, (int)u);
+        if (!__any_sync(kAll, act)) continue;
+        const float *const row = a.logits + (size_t)(act ? u : 0) * E;
+
+        // 1. logits, then choices; NaN where there is none
+        float4 v[NU];
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+            v[j] = make_float4(NAN, NAN, NAN, NAN);
+            if (act && r + 4 * j < nu) {
+                const uint4 b = ld_stream_v4(row + 4 * (r + 4 * j));
+                v[j] = make_float4(clean_logit(__uint_as_float(b.x)), clean_logit(__uint_as_float(b.y)),
+                                   clean_logit(__uint_as_float(b.z)), clean_logit(__uint_as_float(b.w)));
+            }
+        }
+        float m = 0.0f, z = 1.0f, top = 1.0f;
+        if (!a.sigmoid) {
+            float4 x = make_float4(-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX);
+#pragma unroll
+            for (int j = 0; j < NU; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) part_of(x, c) = fmaxf(part_of(x, c), part_of(v[j], c));
+            m = token_max(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+            if (a.bias || !a.renorm) {
+                z = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NU; ++j) {
+                    float4 e = make_float4(__expf(v[j].x - m), __expf(v[j].y - m), __expf(v[j].z - m), __expf(v[j].w - m));
+                    if (r + 4 * j < nu) z += (e.x + e.y) + (e.z + e.w);
+                    if (a.bias) v[j] = e;
+                }
+                z = token_sum(z);
+                top = __fdividef(1.0f, z);
+            }
+        }
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < NU; ++j)
+                if (r + 4 * j < nu) {
+                    float4 b = bias4[r + 4 * j];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        part_of(v[j], c) =
+                            (a.sigmoid ? fast_sigmoid(part_of(v[j], c)) : part_of(v[j], c) * top) + part_of(b, c);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < NU; ++j)
+            if (r + 4 * j < nu) keys4[r + 4 * j] = v[j];
+
+        // 2. groups: which are kept, as bits
+        bool near = false;
+        uint32_t keep = ~0u;
+        float peak[G];  // of this lane's choices in each group
+        if constexpr (G > 1) {
+            constexpr int UG = NU / G;
+            float b1[G], b2[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < UG; ++i) {
+                    const float4 &x = v[g * UG + i];
+                    const float h1 = fmaxf(x.x, x.y), l1 = fminf(x.x, x.y), h2 = fmaxf(x.z, x.w), l2 = fminf(x.z, x.w);
+                    const float u1 = fmaxf(h1, h2), u2 = fmaxf(fminf(h1, h2), fmaxf(l1, l2));
+                    if (i == 0) {
+                        b1[g] = u1;
+                        b2[g] = u2;
+                    } else {
+                        merge2(b1[g], b2[g], u1, u2);
+                    }
+                }
+#pragma unroll
+            for (int g = 0; g < G; ++g) peak[g] = b1[g];
+            // halved over lane ^ 1, then over lane ^ 2: this lane ends with groups r, r + 4
+            float h1[G / 2], h2[G / 2], q1[G / 4], q2[G / 4];
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i) {
+                const bool odd = r & 1;
+                h1[i] = odd ? b1[2 * i + 1] : b1[2 * i];
+                h2[i] = odd ? b2[2 * i + 1] : b2[2 * i];
+                merge2(h1[i], h2[i], __shfl_xor_sync(kAll, odd ? b1[2 * i] : b1[2 * i + 1], 1),
+                       __shfl_xor_sync(kAll, odd ? b2[2 * i] : b2[2 * i + 1], 1));
+            }
+            float value[G / 4], off[G / 4];
+#pragma unroll
+            for (int i = 0; i < G / 4; ++i) {
+                const bool up = r & 2;
+                q1[i] = up ? h1[2 * i + 1] : h1[2 * i];
+                q2[i] = up ? h2[2 * i + 1] : h2[2 * i];
+                merge2(q1[i], q2[i], __shfl_xor_sync(kAll, up ? h1[2 * i] : h1[2 * i + 1], 2),
+                       __shfl_xor_sync(kAll, up ? h2[2 * i] : h2[2 * i + 1], 2));
+                group_value(a, q1[i], q2[i], m, top, value[i], off[i]);
+            }
+            int before[G / 4];
+#pragma unroll
+            for (int i = 0; i < G / 4; ++i) before[i] = 0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int i = 0; i < G / 4; ++i) {
+                    const float other = s ? __shfl_xor_sync(kAll, value[i], s) : value[i];
+                    const int go = 4 * i + (r ^ s);
+#pragma unroll
+                    for (int q = 0; q < G / 4; ++q)
+                        before[q] += other > value[q] || (other == value[q] && go < 4 * q + r);
+                }
+            keep = 0;
+            float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < G / 4; ++i) {
+                const bool in = before[i] < a.kept;
+                keep |= (uint32_t)in << (4 * i + r);
+                if (in) lo = fminf(lo, value[i] - off[i]);
+                else hi = fmaxf(hi, value[i] + off[i]);
+            }
+            keep |= __shfl_xor_sync(kAll, keep, 1);
+            keep |= __shfl_xor_sync(kAll, keep, 2);
+            if (a.bias || a.best == 2) near = !(-token_max(-lo) >= token_max(hi));
+        }
+
+        // 3. the bound
+        float tau;
+        {
+            float c[4];
+            if constexpr (G > 1) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) peak[g] = keep >> g & 1 ? peak[g] : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = peak[i];
+                sort4(c);
+                if constexpr (G == 8) {  // the four best of both halves
+                    float d[4] = {peak[4], peak[5], peak[6], peak[7]};
+                    sort4(d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], d[3 - i]);
+                    sort4(c);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    c[i] = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < NU; ++j) c[i] = fmaxf(c[i], part_of(v[j], i));
+                }
+                if (L == 4) sort4(c);
+                if (L == 2) {
+                    c[0] = fmaxf(c[0], c[2]);
+                    c[1] = fmaxf(c[1], c[3]);
+                    order2(c[0], c[1]);
+                }
+                if (L == 1) c[0] = fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3]));
+            }
+            float g[L];
+#pragma unroll
+            for (int i = 0; i < L; ++i) g[i] = c[i];
+            tau = bound_of<KMAX>(g);
+            if (a.bias && !isinf(tau)) tau -= 4.0f * error_of(a.sigmoid, top, tau);
+        }
+
+        // 4. candidates: as bits, then listed (a NaN is none)
+        constexpr int kWords = (NU * 4 + 31) / 32;
+        uint32_t bits[kWords];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) bits[w] = 0;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+            float at = tau;
+            if constexpr (G > 1) at = keep >> (j / (NU / G)) & 1 ? tau : NAN;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (part_of(v[j], c) >= at) bits[j / 8] |= 1u << (j % 8 * 4 + c);
+        }
+        int cnt = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) cnt += __popc(bits[w]);
+        const int side = __shfl_xor_sync(kAll, cnt, 1), two = cnt + side, rest = __shfl_xor_sync(kAll, two, 2);
+        const int n = two + rest, listed = n < kList ? n : kList;
+        int pos = (r & 1 ? side : 0) + (r & 2 ? rest : 0);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+            for (uint32_t b = bits[w]; b && pos < kList; b &= b - 1, ++pos) {
+                const int i = w * 32 + __ffs(b) - 1, e = 4 * (r + 4 * (i >> 2)) + (i & 3);
+                list.key[t][pos] = reinterpret_cast<const float *>(keys4)[e];
+                list.id[t][pos] = e;
+            }
+        list.key[t][listed + r] = NAN;
+#pragma unroll
+        for (int i = 0; i < kRanks / 4; ++i) list.best[t][r + 4 * i] = NAN;
+        __syncwarp();
+
+        // 5. ranks
+        for (int from = r; from < listed; from += 16) {
+            float own[4];
+            int above[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                own[i] = from + 4 * i < listed ? list.key[t][from + 4 * i] : NAN;
+                above[i] = -1;  // each counts itself
+            }
+            for (int q = 0; q < listed; q += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&list.key[t][q]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) above[i] += (x.x >= own[i]) + (x.y >= own[i]) + (x.z >= own[i]) + (x.w >= own[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (from + 4 * i < listed && above[i] <= k) {
+                    list.best[t][above[i]] = own[i];
+                    list.best_id[t][above[i]] = list.id[t][from + 4 * i];
+                }
+        }
+        __syncwarp();
+        constexpr int SL = (KMAX + 3) / 4;  // slots per lane
+        bool again = false;
+        int id[SL];
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+            const int j = r + 4 * i;
+            id[i] = 0;
+            if (j >= k) continue;
+            const float c = list.best[t][j], next = list.best[t][j + 1];
+            id[i] = list.best_id[t][j];
+            again |= c != c || (a.bias && next == next && too_near(a.sigmoid, top, c, next));
+        }
+        const bool whole = near || n > kList;
+        const uint32_t again_all = __ballot_sync(kAll, act && (again || whole));
+        const bool ok = act && !(again_all >> (lane & ~3) & 15);
+
+        // gates
+        float l[SL], e[SL];
+#pragma unroll
+        for (int i = 0; i < SL; ++i) l[i] = ok && r + 4 * i < k ? clean_logit(__ldg(row + id[i])) : 0.0f;
+        if (a.renorm) {
+            float high = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < SL; ++i)
+                if (r + 4 * i < k) high = fmaxf(high, a.sigmoid ? fminf(l[i], 0.0f) : l[i]);
+            high = token_max(high);
+#pragma unroll
+            for (int i = 0; i < SL; ++i) {
+                e[i] = r + 4 * i < k ? expf((a.sigmoid ? fminf(l[i], 0.0f) : l[i]) - high) : 0.0f;
+                if (a.sigmoid) e[i] = __fdiv_rn(e[i], 1.0f + expf(-fabsf(l[i])));
+                sum += e[i];
+            }
+            sum = token_sum(sum);
+#pragma unroll
+            for (int i = 0; i < SL; ++i) e[i] = a.scale * __fdiv_rn(e[i], sum);
+        } else {
+#pragma unroll
+            for (int i = 0; i < SL; ++i) {
+                const float x = expf(a.sigmoid ? -fabsf(l[i]) : l[i] - m);
+                e[i] = a.scale * (a.sigmoid ? __fdiv_rn(l[i] >= 0.0f ? 1.0f : x, 1.0f + x) : __fdiv_rn(x, z));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SL; ++i)
+            if (ok && r + 4 * i < k) {
+                a.idx[(size_t)u * k + r + 4 * i] = id[i];
+                a.gate[(size_t)u * k + r + 4 * i] = e[i];
+            }
+        // those the fp32 values left open: by their list, or from the start
+        const uint32_t whole_all = __ballot_sync(kAll, act && whole);
+        for (uint32_t left = again_all; left;) {
+            const int s = (__ffs(left) - 1) >> 2;
+            left &= ~(15u << (4 * s));
+            if (!(whole_all >> (4 * s) & 15)) route_list(a, task * 8 + s, list, s, __shfl_sync(kAll, n, 4 * s), lane);
+        }
+        __syncwarp();
+        for (uint32_t left = whole_all; left;) {  // these use the choices' room
+            const int s = (__ffs(left) - 1) >> 2;
+            left &= ~(15u << (4 * s));
+            route_one(a, task * 8 + s, reinterpret_cast<double *>(mine), lane);
+        }
+        __syncwarp();  // every lane is done with the warp's shared memory
+    }
+}
+
 // The gradient.  One warp per token: lane j takes slot j, its value goes to the id's place in a row in shared memory
 // that is zero otherwise, and the row is stored.  With the whole softmax every place gets -p * sum, too.
 //   renormalised softmax r:   scale * r_j * (d_j - sum d r)
@@ -362,9 +783,46 @@ cudaError_t launch_tokens(Kernel kernel, std::atomic<uint64_t> &done, size_t per
     return launch_pdl(kernel, (int)(want < cap ? want : cap), 32 * kWarps, smem, s, a);
 }
 
+template <int NU, int KMAX, int G>
+cudaError_t launch_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = route_scores_lane_kernel<NU, KMAX, G>;
+    const auto bytes = [](int E, int warps) { return (size_t)E * 4 + warps * lane_warp_bytes(E); };
+    const cudaError_t e = allow_smem(kernel, done, p.cfg.device, bytes(16 * NU, kWarps));
+    if (e != cudaSuccess) return e;
+    // few tokens: a warp per block, so that they spread over the SMs
+    const int ntask = (int)(((long long)a.g.R * a.g.T + 7) / 8), warps = ntask <= 4 * p.num_sms ? 1 : kWarps;
+    const int want = (ntask + warps - 1) / warps, cap = p.num_sms * (4 * kWarps / warps);
+    return launch_pdl(kernel, want < cap ? want : cap, 32 * warps, bytes(a.g.E, warps), s, a);
+}
+
+template <int NU>
+cudaError_t launch_lanes_k(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
+    if (a.g.k <= 1) return launch_lanes<NU, 1, 1>(p, a, s);
+    if (a.g.k <= 2) return launch_lanes<NU, 2, 1>(p, a, s);
+    if (a.g.k <= 4) return launch_lanes<NU, 4, 1>(p, a, s);
+    return launch_lanes<NU, 8, 1>(p, a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_route_scores(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
+    const int E = a.g.E, G = a.kept < a.groups ? a.groups : 1;
+    if (a.g.k <= 8 && E <= 256 && E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0) {
+        if (G == 1) {
+            if (E <= 16) return launch_lanes_k<1>(p, a, s);
+            if (E <= 32) return launch_lanes_k<2>(p, a, s);
+            if (E <= 64) return launch_lanes_k<4>(p, a, s);
+            if (E <= 128) return launch_lanes_k<8>(p, a, s);
+            return launch_lanes_k<16>(p, a, s);
+        }
+        // groups of whole units for every lane
+        if (E == 64 && G == 4) return launch_lanes<4, 8, 4>(p, a, s);
+        if (E == 128 && G == 4) return launch_lanes<8, 8, 4>(p, a, s);
+        if (E == 128 && G == 8) return launch_lanes<8, 8, 8>(p, a, s);
+        if (E == 256 && G == 4) return launch_lanes<16, 8, 4>(p, a, s);
+        if (E == 256 && G == 8) return launch_lanes<16, 8, 8>(p, a, s);
+    }
     static std::atomic<uint64_t> done{0};
     return launch_tokens(route_scores_kernel, done, sizeof(double), p, a, s);
 }
