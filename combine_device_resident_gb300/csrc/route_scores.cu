@@ -32,16 +32,19 @@ __device__ __forceinline__ float clean_logit(float v) { return fminf(fmaxf(v, -F
 // A choice: NaN as -infinity, -0 as +0.
 __device__ __forceinline__ float clean_choice(float c) { return fmaxf(c, -INFINITY) + 0.0f; }
 
-// 1 / (1 + exp(-l)) with the fast exponential and reciprocal: the exponential is off by 2 units of 2^-23 and by its
-// argument's rounding, 1.5 * |l| * 2^-24, which the factor 1 - s damps; the sum and the reciprocal add 3 * 2^-24: below
-// 2^-21 of s.
-__device__ __forceinline__ float fast_sigmoid(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
+// 1 / (1 + exp(-l)) with the fast exponential, off by (2 + 1.17 |l|) * 2^-23 of itself, which the factor 1 - s damps to
+// (0.5 + 0.27) * 2^-23 at most, the sum's rounding, 2^-24, and the fast reciprocal's, 2^-23: below 2.3 * 2^-23.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    float s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-l)));
+    return s;
+}
 
 // Bound of the error of an fp32 choice of size |c|.  Sigmoid: fast_sigmoid's, and the bias' addition.  Softmax: every
 // score is at most `top`; exponential, sum (at most 32 terms in a row, then a tree) and quotient are off by less than
 // 64 * 2^-24 of it together.
 __device__ __forceinline__ float error_of(bool sigmoid, float top, float c) {
-    return (sigmoid ? 0x1p-21f : top * 0x1p-18f) + fabsf(c) * 0x1p-23f;
+    return (sigmoid ? 2.4f * 0x1p-23f : top * 0x1p-18f) + fabsf(c) * 0x1p-24f;
 }
 // Whether choice c may in truth lie above `last`, which fp32 puts ahead of it.  Two infinite ones are equal as they stand.
 __device__ __forceinline__ bool too_near(bool sigmoid, float top, float last, float c) {
@@ -52,8 +55,18 @@ __device__ __forceinline__ double exact_score(bool sigmoid, float l, float m, do
     return sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / z;
 }
 
-// The token with logits `l`, chosen in 64 bits by a whole warp; `key` holds E doubles.  Lane j < k gets slot j's id.
-__device__ __noinline__ int route_exact(const ScoreArgs &a, const float *l, double *key, int lane) {
+// Order of doubles as that of signed integers (no NaN; -0 below +0, so add 0 first): the 64-bit pipe is slow here.
+__device__ __forceinline__ long long order64(double v) {
+    const long long b = __double_as_longlong(v + 0.0);
+    return b ^ (b >> 63 & 0x7fffffffffffffffll);
+}
+__device__ __forceinline__ double value64(long long k) {
+    return __longlong_as_double(k ^ (k >> 63 & 0x7fffffffffffffffll));
+}
+constexpr long long kLow64 = -0x7fffffffffffffffll - 1;  // below every choice
+
+// The token with logits `l`, chosen in 64 bits by a whole warp; `key` holds E words.  Lane j < k gets slot j's id.
+__device__ __noinline__ int route_exact(const ScoreArgs &a, const float *l, long long *key, int lane) {
     const int E = a.g.E, k = a.g.k, size = E / a.groups;
     float m = -FLT_MAX;
     double z = 1.0;
@@ -62,62 +75,87 @@ __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *l, doub
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         z = 0.0;
+#pragma unroll 4
         for (int e = lane; e < E; e += 32) z += exp((double)clean_logit(__ldg(l + e)) - (double)m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
     }
-    for (int e = lane; e < E; e += 32) {
-        const float v = clean_logit(__ldg(l + e));
-        key[e] = a.bias ? fmax(exact_score(a.sigmoid, v, m, z) + (double)__ldg(a.bias + e), -(double)INFINITY) : (double)v;
+    if (a.bias) {
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32)
+            key[e] = order64(fmax(exact_score(a.sigmoid, clean_logit(__ldg(l + e)), m, z) + (double)__ldg(a.bias + e),
+                                  -(double)INFINITY));
+    } else {
+        for (int e = lane; e < E; e += 32) key[e] = order64((double)clean_logit(__ldg(l + e)));
     }
     __syncwarp();
     uint64_t keep = ~0ull;
     if (a.kept < a.groups) {
-        double value[2];
+        // lane gi and, from the 33rd group on, lane gi - 32 get group gi's two best
+        long long first[2] = {kLow64, kLow64}, second[2] = {kLow64, kLow64};
+        for (int gi = 0; gi < a.groups; ++gi) {
+            long long b1 = kLow64, b2 = kLow64;
+            for (int e = gi * size + lane; e < (gi + 1) * size; e += 32) {
+                const long long c = key[e];
+                b2 = max(b2, min(b1, c));
+                b1 = max(b1, c);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const long long c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+                b2 = max(min(b1, c1), max(b2, c2));
+                b1 = max(b1, c1);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (gi == q * 32 + lane) {
+                    first[q] = b1;
+                    second[q] = b2;
+                }
+        }
+        long long value[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int gi = q * 32 + lane;
-            double b1 = -INFINITY, b2 = -INFINITY;
-            if (gi < a.groups)
-                for (int e = gi * size; e < (gi + 1) * size; ++e) {
-                    const double c = key[e];
-                    b2 = fmax(b2, fmin(b1, c));
-                    b1 = fmax(b1, c);
-                }
-            value[q] = a.best == 1 ? b1
-                       : a.bias    ? fmax(b1 + b2, -(double)INFINITY)
-                                   : exact_score(a.sigmoid, (float)b1, m, z) + exact_score(a.sigmoid, (float)b2, m, z);
+            value[q] = first[q];
+            if (a.best == 2 && q * 32 + lane < a.groups) {
+                const double b1 = value64(first[q]), b2 = value64(second[q]);
+                value[q] = order64(a.bias ? fmax(b1 + b2, -(double)INFINITY)
+                                          : exact_score(a.sigmoid, (float)b1, m, z) + exact_score(a.sigmoid, (float)b2, m, z));
+            }
         }
         int before[2] = {0, 0};
         for (int gi = 0; gi < a.groups; ++gi) {
-            const double v = __shfl_sync(kAll, gi < 32 ? value[0] : value[1], gi & 31);
+            const long long v = __shfl_sync(kAll, gi < 32 ? value[0] : value[1], gi & 31);
 #pragma unroll
             for (int q = 0; q < 2; ++q) before[q] += v > value[q] || (v == value[q] && gi < q * 32 + lane);
         }
         keep = (uint64_t)__ballot_sync(kAll, before[0] < a.kept && lane < a.groups) |
                (uint64_t)__ballot_sync(kAll, before[1] < a.kept && lane + 32 < a.groups) << 32;
+        for (int e = lane; e < E; e += 32)
+            if (!(keep >> (e / size) & 1)) key[e] = kLow64;
+        __syncwarp();
     }
     int mine = -1;
     for (int j = 0; j < k; ++j) {
-        double best = -INFINITY;
+        long long best = kLow64;
         int id = E;
         for (int e = lane; e < E; e += 32) {
-            const double c = key[e];  // NaN: taken
-            if ((keep >> (e / size) & 1) && (c > best || (c == best && id == E))) {
+            const long long c = key[e];
+            if (c > best) {
                 best = c;
                 id = e;
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const double c = __shfl_xor_sync(kAll, best, o);
+            const long long c = __shfl_xor_sync(kAll, best, o);
             const int i = __shfl_xor_sync(kAll, id, o);
-            if (i < E && (id == E || c > best || (c == best && i < id))) {
+            if (c > best || (c == best && i < id)) {
                 best = c;
                 id = i;
             }
         }
-        if (lane == (id & 31)) key[id] = NAN;
+        if (lane == (id & 31)) key[id] = kLow64;
         __syncwarp();
         if (lane == j) mine = id;
     }
@@ -162,8 +200,8 @@ __device__ __forceinline__ void group_value(const ScoreArgs &a, float b1, float 
                                                          fabsf(value) * 0x1p-23f;
 }
 
-// One token by a warp: the fp32 choice, `room` E doubles.
-__device__ __forceinline__ void route_one(const ScoreArgs &a, long long u, double *room, int lane) {
+// One token by a warp: the fp32 choice, `room` E words of 64 bits.
+__device__ __forceinline__ void route_one(const ScoreArgs &a, long long u, long long *room, int lane) {
     const int E = a.g.E, k = a.g.k, size = E / a.groups;
     const float *l = a.logits + (size_t)u * E;
     uint32_t *key = reinterpret_cast<uint32_t *>(room);
@@ -280,7 +318,7 @@ __device__ __forceinline__ bool token_active(const int32_t *num_tokens, int T, i
 __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double *room = reinterpret_cast<double *>(sm) + (size_t)warp * a.g.E;
+    long long *room = reinterpret_cast<long long *>(sm) + (size_t)warp * a.g.E;
     const int ntok = a.g.R * a.g.T;
     grid_dependency_wait();
     for (long long u = (long long)blockIdx.x * kWarps + warp; u < ntok; u += (long long)gridDim.x * kWarps)
@@ -393,11 +431,11 @@ __device__ __noinline__ void route_list(const ScoreArgs &a, int u, LaneList &lis
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
         zf = (float)z;
     }
-    double c = a.bias ? fmax(exact_score(a.sigmoid, v, m, z) + (double)__ldg(a.bias + id), -(double)INFINITY) : (double)v;
-    c += 0.0;
+    const long long c = order64(
+        a.bias ? fmax(exact_score(a.sigmoid, v, m, z) + (double)__ldg(a.bias + id), -(double)INFINITY) : (double)v);
     int rank = 0;
     for (int i = 0; i < n; ++i) {
-        const double other = __shfl_sync(kAll, c, i);
+        const long long other = __shfl_sync(kAll, c, i);
         const int other_id = __shfl_sync(kAll, id, i);
         rank += other > c || (other == c && other_id < id);
     }
@@ -702,7 +740,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
         for (uint32_t left = whole_all; left;) {  // these use the choices' room
             const int s = (__ffs(left) - 1) >> 2;
             left &= ~(15u << (4 * s));
-            route_one(a, task * 8 + s, reinterpret_cast<double *>(mine), lane);
+            route_one(a, task * 8 + s, reinterpret_cast<long long *>(mine), lane);
         }
         __syncwarp();  // every lane is done with the warp's shared memory
     }
@@ -824,7 +862,7 @@ cudaError_t launch_route_scores(const a2av_plan_s &p, const ScoreArgs &a, cudaSt
         if (E == 256 && G == 8) return launch_lanes<16, 8, 8>(p, a, s);
     }
     static std::atomic<uint64_t> done{0};
-    return launch_tokens(route_scores_kernel, done, sizeof(double), p, a, s);
+    return launch_tokens(route_scores_kernel, done, sizeof(long long), p, a, s);
 }
 
 cudaError_t launch_route_scores_grad(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
