@@ -32,11 +32,17 @@ __device__ __forceinline__ float clean_logit(float v) { return fminf(fmaxf(v, -F
 // A choice: NaN as -infinity, -0 as +0.
 __device__ __forceinline__ float clean_choice(float c) { return fmaxf(c, -INFINITY) + 0.0f; }
 
-// 1 / (1 + exp(-l)) with the fast exponential, off by (2 + 1.17 |l|) * 2^-23 of itself, which the factor 1 - s damps to
+// exp(x) by the fast power of two, off by (2 + 1.17 |x|) * 2^-23 of itself; 0 below 2^-126.
+__device__ __forceinline__ float fast_exp(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+    return e;
+}
+// 1 / (1 + exp(-l)) with the fast exponential, whose error the factor 1 - s damps to
 // (0.5 + 0.27) * 2^-23 at most, the sum's rounding, 2^-24, and the fast reciprocal's, 2^-23: below 2.3 * 2^-23.
 __device__ __forceinline__ float fast_sigmoid(float l) {
     float s;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-l)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + fast_exp(-l)));
     return s;
 }
 
@@ -189,8 +195,8 @@ __device__ __forceinline__ void group_value(const ScoreArgs &a, float b1, float 
         return;
     }
     if (!a.bias) {  // the softmax's are not divided by their sum
-        b1 = a.sigmoid ? fast_sigmoid(b1) : __expf(b1 - m);
-        b2 = a.sigmoid ? fast_sigmoid(b2) : __expf(b2 - m);
+        b1 = a.sigmoid ? fast_sigmoid(b1) : fast_exp(b1 - m);
+        b2 = a.sigmoid ? fast_sigmoid(b2) : fast_exp(b2 - m);
         top = 1.0f;
     }
     value = clean_choice(b1 + b2);
@@ -214,7 +220,7 @@ __device__ __forceinline__ void route_one(const ScoreArgs &a, long long u, long 
             float part = 0.0f;
             int n = 0;
             for (int e = lane; e < E; e += 32) {
-                part += __expf(clean_logit(__ldg(l + e)) - m);
+                part += fast_exp(clean_logit(__ldg(l + e)) - m);
                 if (++n % 32 == 0) {  // at most 32 terms in a row
                     z += part;
                     part = 0.0f;
@@ -227,7 +233,7 @@ __device__ __forceinline__ void route_one(const ScoreArgs &a, long long u, long 
     for (int e = lane; e < E; e += 32) {
         const float v = clean_logit(__ldg(l + e));
         float c = v;
-        if (a.bias) c = clean_choice((a.sigmoid ? fast_sigmoid(v) : __expf(v - m) * top) + __ldg(a.bias + e));
+        if (a.bias) c = clean_choice((a.sigmoid ? fast_sigmoid(v) : fast_exp(v - m) * top) + __ldg(a.bias + e));
         key[e] = order_key(c);
     }
     __syncwarp();
@@ -391,9 +397,8 @@ __device__ __forceinline__ float bound_of(const float (&g)[tau_values<KMAX>()]) 
 __host__ __device__ constexpr int lane_stride(int E) { return (E / 4 + 7) / 8 * 8 + 4; }
 struct LaneList {
     float key[8][kList + 4];  // candidates of the eight tokens, NaN behind them
-    int32_t id[8][kList];
-    float best[8][kRanks];  // by rank; NaN where there is none
-    int32_t best_id[8][kRanks];
+    float best[8][kRanks];    // by rank; NaN where there is none
+    uint8_t id[8][kList], best_id[8][kRanks + 4];
 };
 // A warp's share: the choices of eight tokens (also room for the warp kernel's token), the lists.
 __host__ __device__ constexpr size_t lane_warp_bytes(int E) { return (size_t)8 * lane_stride(E) * 16 + sizeof(LaneList); }
@@ -451,8 +456,66 @@ __device__ __noinline__ void route_list(const ScoreArgs &a, int u, LaneList &lis
     __syncwarp();
 }
 
-template <int NU, int KMAX, int G>
-__global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const ScoreArgs a) {
+// The groups of token u (the warp's t-th) that are kept, as bits, its fp32 values left open.  floor[g]: choices of group g
+// below it are none of its two best; `keys` the token's choices.  All ones where too many are not.
+__device__ __noinline__ uint32_t keep_exact(const ScoreArgs &a, int u, const float *keys, const float *floor,
+                                            uint8_t *ids, int lane) {
+    const int E = a.g.E, size = E / a.groups;
+    const float *l = a.logits + (size_t)u * E;
+    int n = 0;
+    for (int e = lane; e < E; e += 32) {  // E is a multiple of 32
+        const bool in = keys[e] >= floor[e / size];
+        const uint32_t all = __ballot_sync(kAll, in);
+        const int pos = n + __popc(all & lanemask_lt());
+        if (in && pos < kList) ids[pos] = (uint8_t)e;
+        n += __popc(all);
+    }
+    __syncwarp();
+    if (n > kList) return ~0u;
+    float m = 0.0f;
+    double z = 1.0;
+    if (!a.sigmoid) {
+        m = -FLT_MAX;
+        for (int e = lane; e < E; e += 32) m = fmaxf(m, clean_logit(__ldg(l + e)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        if (a.bias) {  // else the scores' common divisor matters to no group
+            z = 0.0;
+#pragma unroll 4
+            for (int e = lane; e < E; e += 32) z += exp((double)clean_logit(__ldg(l + e)) - (double)m);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+        }
+    }
+    const int id = lane < n ? ids[lane] : 0;
+    const float v = clean_logit(__ldg(l + id));
+    const long long c = order64(
+        a.bias ? fmax(exact_score(a.sigmoid, v, m, z) + (double)__ldg(a.bias + id), -(double)INFINITY) : (double)v);
+    long long b1 = kLow64, b2 = kLow64;  // of group `lane`
+    for (int i = 0; i < n; ++i) {
+        const long long other = __shfl_sync(kAll, c, i);
+        if (__shfl_sync(kAll, id, i) / size == lane) {
+            b2 = max(b2, min(b1, other));
+            b1 = max(b1, other);
+        }
+    }
+    long long value = b1;
+    if (a.best == 2 && lane < a.groups) {
+        const double d1 = value64(b1), d2 = value64(b2);
+        value = order64(a.bias ? fmax(d1 + d2, -(double)INFINITY)
+                               : exact_score(a.sigmoid, (float)d1, m, z) + exact_score(a.sigmoid, (float)d2, m, z));
+    }
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const long long other = __shfl_sync(kAll, value, g);
+        before += other > value || (other == value && g < lane);
+    }
+    return __ballot_sync(kAll, lane < a.groups && before < a.kept);
+}
+
+// kFull: E is 16 * NU, so no unit is missing.
+template <int NU, int KMAX, int G, bool kFull>
+__global__ void __launch_bounds__(32 * kWarps, 5) route_scores_lane_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int L = tau_values<KMAX>();
     const int E = a.g.E, k = a.g.k, nu = E / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -471,19 +534,31 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
         const long long u = (long long)task * 8 + t;
         const bool act = u < ntok && token_active(a.num_tokens, a.g.T, (int)u);
         if (!__any_sync(kAll, act)) continue;
-        const float *const row = a.logits + (size_t)(act ? u : 0) * E;
+        const float *const row = a.logits + (size_t)(act ? u : 0) * E;  // of a token that takes no part nothing is kept
+        auto has = [&](int j) { return kFull || r + 4 * j < nu; };
 
         // 1. logits, then choices; NaN where there is none
         float4 v[NU];
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-            v[j] = make_float4(NAN, NAN, NAN, NAN);
-            if (act && r + 4 * j < nu) {
+            if (!kFull) v[j] = make_float4(NAN, NAN, NAN, NAN);
+            if (has(j)) {
                 const uint4 b = ld_stream_v4(row + 4 * (r + 4 * j));
-                v[j] = make_float4(clean_logit(__uint_as_float(b.x)), clean_logit(__uint_as_float(b.y)),
-                                   clean_logit(__uint_as_float(b.z)), clean_logit(__uint_as_float(b.w)));
+                v[j] = make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w));
             }
         }
+        const bool scored = a.bias && a.sigmoid;  // then an infinity needs no care
+#pragma unroll
+        for (int j = 0; j < NU; ++j)
+            if (has(j))
+#pragma unroll
+                for (int c = 0; c < 4; ++c) part_of(v[j], c) = fmaxf(part_of(v[j], c), -FLT_MAX);
+        if (!scored)
+#pragma unroll
+            for (int j = 0; j < NU; ++j)
+                if (has(j))
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) part_of(v[j], c) = fminf(part_of(v[j], c), FLT_MAX);
         float m = 0.0f, z = 1.0f, top = 1.0f;
         if (!a.sigmoid) {
             float4 x = make_float4(-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX);
@@ -496,8 +571,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                 z = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NU; ++j) {
-                    float4 e = make_float4(__expf(v[j].x - m), __expf(v[j].y - m), __expf(v[j].z - m), __expf(v[j].w - m));
-                    if (r + 4 * j < nu) z += (e.x + e.y) + (e.z + e.w);
+                    float4 e = make_float4(fast_exp(v[j].x - m), fast_exp(v[j].y - m), fast_exp(v[j].z - m), fast_exp(v[j].w - m));
+                    if (has(j)) z += (e.x + e.y) + (e.z + e.w);
                     if (a.bias) v[j] = e;
                 }
                 z = token_sum(z);
@@ -507,7 +582,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
         if (a.bias) {
 #pragma unroll
             for (int j = 0; j < NU; ++j)
-                if (r + 4 * j < nu) {
+                if (has(j)) {
                     float4 b = bias4[r + 4 * j];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -517,7 +592,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
         }
 #pragma unroll
         for (int j = 0; j < NU; ++j)
-            if (r + 4 * j < nu) keys4[r + 4 * j] = v[j];
+            if (has(j)) keys4[r + 4 * j] = v[j];
 
         // 2. groups: which are kept, as bits
         bool near = false;
@@ -586,7 +661,33 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
             }
             keep |= __shfl_xor_sync(kAll, keep, 1);
             keep |= __shfl_xor_sync(kAll, keep, 2);
-            if (a.bias || a.best == 2) near = !(-token_max(-lo) >= token_max(hi));
+            if (a.bias || a.best == 2) {
+                const float least = -token_max(-lo), most = token_max(hi);  // by every lane
+                near = act && !(least >= most);
+                uint32_t open = __ballot_sync(kAll, near);
+                if (open) {
+                    if (near)  // what may be one of a group's two best, or its best
+#pragma unroll
+                        for (int i = 0; i < G / 4; ++i) {
+                            const float q = a.best == 2 ? q2[i] : q1[i];
+                            list.best[t][4 * i + r] = a.bias && !isinf(q) ? q - 4.0f * error_of(a.sigmoid, top, q) : q;
+                        }
+                    __syncwarp();
+                    while (open) {
+                        const int s = (__ffs(open) - 1) >> 2;
+                        open &= ~(15u << (4 * s));
+                        const float *const token = reinterpret_cast<const float *>(mine) + (size_t)s * stride * 4;
+                        const uint32_t exact = keep_exact(a, task * 8 + s, token, list.best[s], list.id[s], lane);
+                        if (t == s) {
+                            near = exact == ~0u;
+                            keep = exact;
+                        }
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < NU; ++j) v[j] = keys4[r + 4 * j];  // so that they need not be held over the calls
+                }
+            }
         }
 
         // 3. the bound
@@ -821,25 +922,25 @@ cudaError_t launch_tokens(Kernel kernel, std::atomic<uint64_t> &done, size_t per
     return launch_pdl(kernel, (int)(want < cap ? want : cap), 32 * kWarps, smem, s, a);
 }
 
-template <int NU, int KMAX, int G>
+template <int NU, int KMAX, int G, bool kFull>
 cudaError_t launch_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = route_scores_lane_kernel<NU, KMAX, G>;
+    const auto kernel = route_scores_lane_kernel<NU, KMAX, G, kFull>;
     const auto bytes = [](int E, int warps) { return (size_t)E * 4 + warps * lane_warp_bytes(E); };
     const cudaError_t e = allow_smem(kernel, done, p.cfg.device, bytes(16 * NU, kWarps));
     if (e != cudaSuccess) return e;
     // few tokens: a warp per block, so that they spread over the SMs
-    const int ntask = (int)(((long long)a.g.R * a.g.T + 7) / 8), warps = ntask <= 4 * p.num_sms ? 1 : kWarps;
-    const int want = (ntask + warps - 1) / warps, cap = p.num_sms * (4 * kWarps / warps);
+    const int ntask = (int)(((long long)a.g.R * a.g.T + 7) / 8), warps = ntask <= kWarps * p.num_sms ? 1 : kWarps;
+    const int want = (ntask + warps - 1) / warps, cap = p.num_sms * (5 * kWarps / warps);
     return launch_pdl(kernel, want < cap ? want : cap, 32 * warps, bytes(a.g.E, warps), s, a);
 }
 
-template <int NU>
+template <int NU, bool kFull>
 cudaError_t launch_lanes_k(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
-    if (a.g.k <= 1) return launch_lanes<NU, 1, 1>(p, a, s);
-    if (a.g.k <= 2) return launch_lanes<NU, 2, 1>(p, a, s);
-    if (a.g.k <= 4) return launch_lanes<NU, 4, 1>(p, a, s);
-    return launch_lanes<NU, 8, 1>(p, a, s);
+    if (a.g.k <= 1) return launch_lanes<NU, 1, 1, kFull>(p, a, s);
+    if (a.g.k <= 2) return launch_lanes<NU, 2, 1, kFull>(p, a, s);
+    if (a.g.k <= 4) return launch_lanes<NU, 4, 1, kFull>(p, a, s);
+    return launch_lanes<NU, 8, 1, kFull>(p, a, s);
 }
 
 }  // namespace
@@ -848,18 +949,20 @@ cudaError_t launch_route_scores(const a2av_plan_s &p, const ScoreArgs &a, cudaSt
     const int E = a.g.E, G = a.kept < a.groups ? a.groups : 1;
     if (a.g.k <= 8 && E <= 256 && E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0) {
         if (G == 1) {
-            if (E <= 16) return launch_lanes_k<1>(p, a, s);
-            if (E <= 32) return launch_lanes_k<2>(p, a, s);
-            if (E <= 64) return launch_lanes_k<4>(p, a, s);
-            if (E <= 128) return launch_lanes_k<8>(p, a, s);
-            return launch_lanes_k<16>(p, a, s);
+            if (E <= 16) return launch_lanes_k<1, false>(p, a, s);
+            if (E <= 32) return launch_lanes_k<2, false>(p, a, s);
+            if (E <= 64) return launch_lanes_k<4, false>(p, a, s);
+            if (E < 128) return launch_lanes_k<8, false>(p, a, s);
+            if (E == 128) return launch_lanes_k<8, true>(p, a, s);
+            if (E < 256) return launch_lanes_k<16, false>(p, a, s);
+            return launch_lanes_k<16, true>(p, a, s);
         }
         // groups of whole units for every lane
-        if (E == 64 && G == 4) return launch_lanes<4, 8, 4>(p, a, s);
-        if (E == 128 && G == 4) return launch_lanes<8, 8, 4>(p, a, s);
-        if (E == 128 && G == 8) return launch_lanes<8, 8, 8>(p, a, s);
-        if (E == 256 && G == 4) return launch_lanes<16, 8, 4>(p, a, s);
-        if (E == 256 && G == 8) return launch_lanes<16, 8, 8>(p, a, s);
+        if (E == 64 && G == 4) return launch_lanes<4, 8, 4, true>(p, a, s);
+        if (E == 128 && G == 4) return launch_lanes<8, 8, 4, true>(p, a, s);
+        if (E == 128 && G == 8) return launch_lanes<8, 8, 8, true>(p, a, s);
+        if (E == 256 && G == 4) return launch_lanes<16, 8, 4, true>(p, a, s);
+        if (E == 256 && G == 8) return launch_lanes<16, 8, 8, true>(p, a, s);
     }
     static std::atomic<uint64_t> done{0};
     return launch_tokens(route_scores_kernel, done, sizeof(long long), p, a, s);
