@@ -911,6 +911,109 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_grad_kernel(const Sc
     }
 }
 
+// The same for k up to 8 and E a multiple of 4: eight lanes per token, four tokens per warp, rows stored as 16-byte
+// vectors.  With the whole softmax (NU > 0) lane r holds units r, r + 8, ... of its token's row, E at most 32 * NU.
+template <int NU>
+__global__ void __launch_bounds__(32 * kWarps) route_scores_grad_lane_kernel(const ScoreArgs a) {
+    extern __shared__ __align__(16) unsigned char sm[];
+    const int E = a.g.E, k = a.g.k, nu = E / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane >> 3, r = lane & 7;
+    float *const row = reinterpret_cast<float *>(sm) + (size_t)(warp * 4 + t) * E;
+    float4 *const row4 = reinterpret_cast<float4 *>(row);
+    for (int c = r; c < nu; c += 8) row4[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncwarp();
+    grid_dependency_wait();
+    auto sum8 = [](float v) {
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+        return v;
+    };
+    auto max8 = [](float v) {
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+        return v;
+    };
+    const int ntok = a.g.R * a.g.T, ntask = (int)(((long long)ntok + 3) / 4);
+    for (int task = blockIdx.x * kWarps + warp; task < ntask; task += gridDim.x * kWarps) {
+        const long long u = (long long)task * 4 + t;
+        const bool act = u < ntok && token_active(a.num_tokens, a.g.T, (int)u);
+        if (!__any_sync(kAll, act)) continue;
+        const float *const l = a.logits + (size_t)(act ? u : 0) * E;
+        const size_t at = (size_t)(act ? u : 0) * k + r;
+        const bool slot = act && r < k;
+        const int id = slot ? __ldg(a.idx + at) : -1;
+        const bool in = (uint32_t)id < (uint32_t)E;
+        if (slot && !in) atomicOr(a.status, A2AV_DEV_BAD_EXPERT);
+        float4 x[NU > 0 ? NU : 1];
+        if constexpr (NU > 0) {
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                x[j] = make_float4(-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX);
+                if (act && r + 8 * j < nu) {
+                    const uint4 b = ld_stream_v4(l + 4 * (r + 8 * j));
+                    x[j] = make_float4(clean_logit(__uint_as_float(b.x)), clean_logit(__uint_as_float(b.y)),
+                                       clean_logit(__uint_as_float(b.z)), clean_logit(__uint_as_float(b.w)));
+                }
+            }
+        }
+        const float d = in ? __ldg(a.d_gate + at) : 0.0f;
+        const float v = in ? clean_logit(__ldg(l + id)) : 0.0f;
+        const float ea = expf(-fabsf(v));
+        const float rest = a.sigmoid ? __fdiv_rn(v >= 0.0f ? ea : 1.0f, 1.0f + ea) : 1.0f;  // 1 - s
+        float val, sum = 0.0f, scale = 0.0f;
+        if constexpr (NU > 0) {
+            float m = -FLT_MAX, z = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NU; ++j) m = fmaxf(m, fmaxf(fmaxf(x[j].x, x[j].y), fmaxf(x[j].z, x[j].w)));
+            m = max8(m);
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                x[j] = make_float4(expf(x[j].x - m), expf(x[j].y - m), expf(x[j].z - m), expf(x[j].w - m));
+                if (r + 8 * j < nu) z += (x[j].x + x[j].y) + (x[j].z + x[j].w);
+            }
+            z = sum8(z);
+            val = in ? a.scale * d * __fdiv_rn(expf(v - m), z) : 0.0f;
+            sum = sum8(val);
+            scale = __fdiv_rn(1.0f, z);
+        } else if (a.renorm) {
+            const float base = a.sigmoid ? fminf(v, 0.0f) : v, high = max8(in ? base : -INFINITY);
+            float e = in ? expf(base - high) : 0.0f;
+            if (a.sigmoid) e = __fdiv_rn(e, 1.0f + ea);
+            const float all = sum8(e), g = in ? __fdiv_rn(e, all) : 0.0f, dot = sum8(g * d);
+            val = in ? a.scale * g * (d - dot) * rest : 0.0f;
+        } else {
+            val = in ? a.scale * d * __fdiv_rn(v >= 0.0f ? 1.0f : ea, 1.0f + ea) * rest : 0.0f;
+        }
+        // an id that occurs twice: all its slots' values, added in slot order by each of them
+        const uint32_t same = __match_any_sync(kAll, in ? t << 16 | id : -1 - lane);
+        if (__any_sync(kAll, same & (same - 1))) {
+            float all = 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                const float w = __shfl_sync(kAll, val, (lane & ~7) + j);
+                if (same >> ((lane & ~7) + j) & 1) all += w;
+            }
+            val = all;
+        }
+        if (in) row[id] = val;
+        __syncwarp();
+        float4 *const out = reinterpret_cast<float4 *>(a.d_logits + (size_t)(act ? u : 0) * E);
+        if constexpr (NU > 0) {
+#pragma unroll
+            for (int j = 0; j < NU; ++j)
+                if (act && r + 8 * j < nu) {
+                    const float4 w = row4[r + 8 * j];
+                    out[r + 8 * j] = make_float4(w.x - sum * (x[j].x * scale), w.y - sum * (x[j].y * scale),
+                                                 w.z - sum * (x[j].z * scale), w.w - sum * (x[j].w * scale));
+                }
+        } else if (act) {
+#pragma unroll 4
+            for (int c = r; c < nu; c += 8) out[c] = row4[c];
+        }
+        __syncwarp();
+        if (in) row[id] = 0.0f;
+        __syncwarp();
+    }
+}
+
 template <typename Kernel>
 cudaError_t launch_tokens(Kernel kernel, std::atomic<uint64_t> &done, size_t per_expert, const a2av_plan_s &p,
                           const ScoreArgs &a, cudaStream_t s) {
@@ -920,6 +1023,18 @@ cudaError_t launch_tokens(Kernel kernel, std::atomic<uint64_t> &done, size_t per
     const long long want = ((long long)a.g.R * a.g.T + kWarps - 1) / kWarps;
     const long long fit = (long long)(200 * 1024 / (smem + 1024)), cap = (long long)p.num_sms * (fit < 12 ? fit : 12);
     return launch_pdl(kernel, (int)(want < cap ? want : cap), 32 * kWarps, smem, s, a);
+}
+
+template <int NU>
+cudaError_t launch_grad_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = route_scores_grad_lane_kernel<NU>;
+    const cudaError_t e = allow_smem(kernel, done, p.cfg.device, (size_t)kWarps * 16 * kMaxExperts);
+    if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)kWarps * 16 * a.g.E;
+    const int ntask = (int)(((long long)a.g.R * a.g.T + 3) / 4), want = (ntask + kWarps - 1) / kWarps;
+    const int fit = (int)(220 * 1024 / (smem + 1024)), cap = p.num_sms * (fit < 12 ? fit : 12);
+    return launch_pdl(kernel, want < cap ? want : cap, 32 * kWarps, smem, s, a);
 }
 
 template <int NU, int KMAX, int G, bool kFull>
@@ -969,6 +1084,14 @@ cudaError_t launch_route_scores(const a2av_plan_s &p, const ScoreArgs &a, cudaSt
 }
 
 cudaError_t launch_route_scores_grad(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
+    const int E = a.g.E;
+    if (a.g.k <= 8 && E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.d_logits)) % 16 == 0) {
+        if (a.sigmoid || a.renorm) return launch_grad_lanes<0>(p, a, s);
+        if (E <= 32) return launch_grad_lanes<1>(p, a, s);
+        if (E <= 64) return launch_grad_lanes<2>(p, a, s);
+        if (E <= 128) return launch_grad_lanes<4>(p, a, s);
+        if (E <= 256) return launch_grad_lanes<8>(p, a, s);
+    }
     static std::atomic<uint64_t> done{0};
     return launch_tokens(route_scores_grad_kernel, done, sizeof(float), p, a, s);
 }
