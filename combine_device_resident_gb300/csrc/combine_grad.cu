@@ -3,7 +3,9 @@
 //   d_y[s] = bf16(gate * d_out[t]),   d_gate = <y[s], d_out[t]>   (fp32 sums of exact products)
 //
 // One block per token: its row of d_out stays in registers while the k rows of y come in and the k rows of d_y go out,
-// so everything moves once.  Bound by HBM.
+// so everything moves once.  Bound by HBM.  Rows of up to 16,384 (piped): while an assignment is worked on, the next one's
+// row of y is on its way, with the next token's row of d_out after the last, and the slot after that; the blocks' loads
+// then overlap their stores and sums.  Longer rows go in pieces, without.
 #include "block_ops.cuh"
 #include "row_math.cuh"
 
@@ -91,14 +93,127 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(const Combine
     }
 }
 
+template <int V, bool kRows, bool kGates>
+__global__ void __launch_bounds__(kMaxThreads, 4 / V) combine_grad_piped_kernel(const CombineGradArgs a) {
+    __shared__ float part[2][kMaxTopk][kMaxThreads / 32];  // [token parity]
+    const int k = a.g.k, H = a.g.H, nvec = H / 8, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nwarps = blockDim.x >> 5;
+    const long long ntok = (long long)a.g.R * a.g.T;
+    auto active = [&](long long u) {  // from u on, in the block's steps
+        if (a.num_tokens)
+            for (; u < ntok; u += gridDim.x) {
+                const int s = (int)(u / a.g.T);
+                if (u - (long long)s * a.g.T < active_tokens(a.num_tokens, s, a.g.T)) break;
+            }
+        return u;
+    };
+    struct Item {  // an assignment
+        long long u;
+        int j;
+        int32_t slot;  // negative: none
+        float gate;
+    };
+    auto ask = [&](Item &i) {
+        i.slot = -1;
+        i.gate = 0.0f;
+        if (i.u >= ntok) return;
+        i.slot = __ldg(a.slot_map + i.u * k + i.j);
+        if (kRows) i.gate = __ldg(a.gate + i.u * k + i.j);
+    };
+    auto after = [&](const Item &i) {
+        Item n = i;
+        if (++n.j == k) {
+            n.j = 0;
+            n.u = i.u < ntok ? active(i.u + gridDim.x) : i.u;
+        }
+        ask(n);
+        return n;
+    };
+    auto load = [&](const uint16_t *row, uint4 (&to)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = tid + v * blockDim.x;
+            if (i < nvec) to[v] = ld_row(row + (size_t)i * 8);
+        }
+    };
+    auto fits = [&](const Item &i) { return i.slot >= 0 && i.slot < a.arena_rows; };
+    grid_dependency_wait();
+    Item now;
+    now.u = active(blockIdx.x);
+    now.j = 0;
+    ask(now);
+    Item next = after(now);
+    uint4 d[V], y[V], dn[V], yn[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = y[v] = dn[v] = yn[v] = make_uint4(0, 0, 0, 0);  // behind the row's end for good
+    if (now.u < ntok) {
+        load(a.d_out + (size_t)now.u * H, d);
+        if (kGates && fits(now)) load(a.y + (size_t)now.slot * H, y);
+    }
+    int parity = 0;
+    while (now.u < ntok) {
+        const bool last = now.j == k - 1;
+        if (kGates && fits(next)) load(a.y + (size_t)next.slot * H, yn);
+        if (last && next.u < ntok) load(a.d_out + (size_t)next.u * H, dn);
+        const Item then = after(next);
+        if (now.slot >= a.arena_rows && tid == 0) atomicOr(a.status, kDevBadSlot);
+        if (kRows && fits(now)) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int i = tid + v * blockDim.x;
+                if (i < nvec) st_v4(a.d_y + (size_t)now.slot * H + (size_t)i * 8, scaled8(d[v], now.gate));
+            }
+        }
+        if (kGates) {
+            float dot = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) dot = dot8(d[v], y[v], dot);
+            dot = warp_sum(fits(now) ? dot : 0.0f);
+            if (lane == 0) part[parity][now.j][warp] = dot;
+            if (last) {
+                __syncthreads();  // the other parity's sums are written out by now, before this barrier
+                if (tid < k) {
+                    float sum = 0.0f;
+                    for (int w = 0; w < nwarps; ++w) sum += part[parity][tid][w];
+                    a.d_gate[now.u * k + tid] = sum;
+                }
+                parity ^= 1;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            y[v] = yn[v];
+            if (last) d[v] = dn[v];
+        }
+        now = next;
+        next = then;
+    }
+}
+
+// Two vectors a thread where the row fits (64 registers, two blocks of 448 per SM for H = 7168): 65,536 x 7168, top-8:
+// 2464 us (6.48 TB/s); four vectors and 224 threads 2708-2892 us at 64 to 117 registers, the same without the loads
+// ahead 2671 us; 2,040 x 5120, top-1: 10.8 us against 12.8-16.5 and 13.9.
+template <int V, bool kRows, bool kGates>
+cudaError_t launch_piped(const a2av_plan_s &p, const CombineGradArgs &a, cudaStream_t s) {
+    const int block = ((a.g.H / 8 + V - 1) / V + 31) / 32 * 32, fit = 65536 / (32 * V) / block;
+    const long long ntok = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * (fit < 1 ? 1 : fit > 16 ? 16 : fit);
+    return launch_pdl(combine_grad_piped_kernel<V, kRows, kGates>, (int)(ntok < cap ? ntok : cap), block, 0, s, a);
+}
+
+template <int V>
+cudaError_t launch_piped_form(const a2av_plan_s &p, const CombineGradArgs &a, cudaStream_t s) {
+    if (!a.d_y) return launch_piped<V, false, true>(p, a, s);
+    return a.d_gate ? launch_piped<V, true, true>(p, a, s) : launch_piped<V, true, false>(p, a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_combine_grad(const a2av_plan_s &p, const CombineGradArgs &a, cudaStream_t s) {
     const int nvec = a.g.H / 8;
-    const int want = ((nvec + kVec - 1) / kVec + 31) / 32 * 32, block = want < kMaxThreads ? want : kMaxThreads;
-    const long long ntok = (long long)a.g.R * a.g.T, per_sm = 1024 / block < 16 ? 1024 / block : 16;
-    const long long cap = (long long)p.num_sms * per_sm;
-    return launch_pdl(combine_grad_kernel, (int)(ntok < cap ? ntok : cap), block, 0, s, a);
+    if (nvec <= 2 * kMaxThreads) return launch_piped_form<2>(p, a, s);
+    if (nvec <= 4 * kMaxThreads) return launch_piped_form<4>(p, a, s);
+    const long long ntok = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * 2;
+    return launch_pdl(combine_grad_kernel, (int)(ntok < cap ? ntok : cap), kMaxThreads, 0, s, a);
 }
 
 }  // namespace a2av

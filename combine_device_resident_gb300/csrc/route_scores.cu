@@ -933,16 +933,39 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_grad_lane_kernel(con
         return v;
     };
     const int ntok = a.g.R * a.g.T, ntask = (int)(((long long)ntok + 3) / 4);
-    for (int task = blockIdx.x * kWarps + warp; task < ntask; task += gridDim.x * kWarps) {
+    // A task's ids and gradients are asked for two tasks ahead, their logits one task ahead.
+    struct Slot {
+        bool act;
+        int id;
+        float d;
+    };
+    auto ask = [&](int task) {
         const long long u = (long long)task * 4 + t;
-        const bool act = u < ntok && token_active(a.num_tokens, a.g.T, (int)u);
-        if (!__any_sync(kAll, act)) continue;
-        const float *const l = a.logits + (size_t)(act ? u : 0) * E;
-        const size_t at = (size_t)(act ? u : 0) * k + r;
-        const bool slot = act && r < k;
-        const int id = slot ? __ldg(a.idx + at) : -1;
+        Slot s;
+        s.act = task < ntask && u < ntok && token_active(a.num_tokens, a.g.T, (int)u);
+        const bool slot = s.act && r < k;
+        s.id = slot ? __ldg(a.idx + u * k + r) : -1;
+        s.d = slot ? __ldg(a.d_gate + u * k + r) : 0.0f;
+        return s;
+    };
+    auto logit = [&](int task, const Slot &s) {
+        return (uint32_t)s.id < (uint32_t)E ? __ldg(a.logits + ((size_t)task * 4 + t) * E + s.id) : 0.0f;
+    };
+    const int step = gridDim.x * kWarps;
+    int task = blockIdx.x * kWarps + warp;
+    Slot now = ask(task), next = ask(task + step);
+    float raw = logit(task, now);
+    for (; task < ntask; task += step) {
+        const bool act = now.act;
+        const long long u = act ? (long long)task * 4 + t : 0;
+        const float *const l = a.logits + (size_t)u * E;
+        const int id = now.id;
         const bool in = (uint32_t)id < (uint32_t)E;
-        if (slot && !in) atomicOr(a.status, A2AV_DEV_BAD_EXPERT);
+        if (act && r < k && !in) atomicOr(a.status, A2AV_DEV_BAD_EXPERT);
+        const float d = in ? now.d : 0.0f, v = clean_logit(raw);
+        now = next;
+        raw = logit(task + step, now);
+        next = ask(task + 2 * step);
         float4 x[NU > 0 ? NU : 1];
         if constexpr (NU > 0) {
 #pragma unroll
@@ -955,8 +978,6 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_grad_lane_kernel(con
                 }
             }
         }
-        const float d = in ? __ldg(a.d_gate + at) : 0.0f;
-        const float v = in ? clean_logit(__ldg(l + id)) : 0.0f;
         const float ea = expf(-fabsf(v));
         const float rest = a.sigmoid ? __fdiv_rn(v >= 0.0f ? ea : 1.0f, 1.0f + ea) : 1.0f;  // 1 - s
         float val, sum = 0.0f, scale = 0.0f;
@@ -995,7 +1016,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_grad_lane_kernel(con
         }
         if (in) row[id] = val;
         __syncwarp();
-        float4 *const out = reinterpret_cast<float4 *>(a.d_logits + (size_t)(act ? u : 0) * E);
+        float4 *const out = reinterpret_cast<float4 *>(a.d_logits + (size_t)u * E);
         if constexpr (NU > 0) {
 #pragma unroll
             for (int j = 0; j < NU; ++j)
