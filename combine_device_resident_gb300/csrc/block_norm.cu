@@ -589,56 +589,56 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
             }
 }
 
-// The blocks' sums S added up: d_weight = sum S, d_post = b * sum gate * S, d_gate = b * post * sum S (per rank over its
-// blocks).
-// The blocks in eight shares, each in order, then the shares in order.
-enum { kOutWeight, kOutPost, kOutGate };
-constexpr int kSumWarps = 8;
+// The blocks' sums S added up: d_weight = sum S (blockIdx.y 0); S_r = sum S over the blocks of rank r (of all, without
+// a gate per rank), d_gate[r] = b * post * S_r, d_post = b * sum_r gate[r] * S_r (blockIdx.y 1).  A block takes 32
+// columns, eight threads in 32 groups: each group adds up a share of one rank's blocks, the shares and then the ranks are
+// added in order.
+constexpr int kSumGroups = 32;
 
-__global__ void __launch_bounds__(32 * kSumWarps) norm_sums_kernel(const BlockNormArgs a, int blocks, bool per_rank) {
-    __shared__ float4 part[kSumWarps][32];
-    const int H = a.g.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x * 32 + lane;  // four columns
-    const int q = blockIdx.y < kOutGate ? blockIdx.y : kOutGate, rank = blockIdx.y - q;
-    float *out = q == kOutWeight ? a.d_weight : q == kOutPost ? a.d_post : static_cast<float *>(a.d_gate);
+__global__ void __launch_bounds__(8 * kSumGroups) norm_sums_kernel(const BlockNormArgs a, int blocks, bool per_rank) {
+    __shared__ float4 part[kSumGroups][8], ranked[kSumGroups][8];
+    const int H = a.g.H, x = threadIdx.x & 7, group = threadIdx.x >> 3, i = blockIdx.x * 8 + x;  // four columns
+    const bool weights = blockIdx.y == 0, in = i < H / 4;
+    float *const d_gate = static_cast<float *>(a.d_gate);
+    const int R = per_rank && !weights ? a.g.R : 1, parts = blocks / R;
+    const int share = R <= kSumGroups ? kSumGroups / R : 1, at_once = kSumGroups / share;  // groups per rank, ranks
     grid_dependency_wait();
-    if (!out) return;
-    const bool shared_gate = a.gate && (a.gate_kind == A2AV_GATE_CHANNEL || per_rank);
-    const int parts = per_rank ? blocks / a.g.R : blocks;  // of one gate
-    const int n = q == kOutGate ? parts : blocks, b0 = rank * parts;
-    auto weight4 = [&](const uint16_t *w, size_t row) {
-        const uint2 v = *(reinterpret_cast<const uint2 *>(w + row * H) + i);
-        return make_float4(lo_f(v.x), hi_f(v.x), lo_f(v.y), hi_f(v.y));
+    if (weights ? !a.d_weight : !a.d_post && !d_gate) return;
+    auto add4 = [](float4 &s, const float4 &v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    auto times = [&](const float4 &s, const uint16_t *w) {
+        const uint2 v = *(reinterpret_cast<const uint2 *>(w) + i);
+        return make_float4(s.x * lo_f(v.x), s.y * hi_f(v.x), s.z * lo_f(v.y), s.w * hi_f(v.y));
     };
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (i < H / 4) {
-        const float *from = a.scratch + (size_t)(q == kOutWeight ? kSumWeight : kSumBranch) * H;
-#pragma unroll 8
-        for (int b = (int)((long long)n * warp / kSumWarps); b < (int)((long long)n * (warp + 1) / kSumWarps); ++b) {
-            float4 v = *(reinterpret_cast<const float4 *>(from + (size_t)(b0 + b) * kSums * H) + i);
-            if (q == kOutPost && per_rank) {
-                const float4 w = weight4(a.gate, b / parts);
-                v.x *= w.x, v.y *= w.y, v.z *= w.z, v.w *= w.w;
-            }
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    auto store = [&](float *to, float4 s, float by) {
+        s.x *= by, s.y *= by, s.z *= by, s.w *= by;
+        reinterpret_cast<float4 *>(to)[i] = s;
+    };
+    const float *const from = a.scratch + (size_t)(weights ? kSumWeight : kSumBranch) * H;
+    float4 total = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int base = 0; base < R; base += at_once) {
+        const int rank = base + group / share, mine = group % share;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in && group / share < at_once && rank < R) {
+            const int first = rank * parts + (int)((long long)parts * mine / share);
+            const int end = rank * parts + (int)((long long)parts * (mine + 1) / share);
+#pragma unroll 4
+            for (int b = first; b < end; ++b) add4(s, *(reinterpret_cast<const float4 *>(from + (size_t)b * kSums * H) + i));
         }
+        part[group][x] = s;
+        __syncthreads();
+        if (in && group < at_once && base + group < R) {  // this thread: rank base + group
+            const int r = base + group;
+            float4 sum = part[group * share][x];
+            for (int q = 1; q < share; ++q) add4(sum, part[group * share + q][x]);
+            if (!weights && d_gate) store(d_gate + (size_t)r * H, a.post ? times(sum, a.post) : sum, a.branch_scale);
+            const bool shared_gate = a.gate_kind == A2AV_GATE_CHANNEL || a.gate_kind == A2AV_GATE_RANK;
+            ranked[group][x] = !weights && shared_gate ? times(sum, a.gate + (size_t)r * H) : sum;
+        }
+        __syncthreads();
+        if (in && group == 0)
+            for (int q = 0; q < at_once && base + q < R; ++q) add4(total, ranked[q][x]);
     }
-    part[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && i < H / 4) {
-        for (int w = 1; w < kSumWarps; ++w) {
-            const float4 v = part[w][lane];
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        const uint16_t *times = q == kOutGate ? a.post : q == kOutPost && shared_gate && !per_rank ? a.gate : nullptr;
-        if (times) {
-            const float4 w = weight4(times, 0);
-            s.x *= w.x, s.y *= w.y, s.z *= w.z, s.w *= w.w;
-        }
-        const float b = q == kOutWeight ? 1.0f : a.branch_scale;
-        s.x *= b, s.y *= b, s.z *= b, s.w *= b;
-        reinterpret_cast<float4 *>(out + (size_t)rank * H)[i] = s;
-    }
+    if (in && group == 0 && (weights || a.d_post)) store(weights ? a.d_weight : a.d_post, total, weights ? 1.0f : a.branch_scale);
 }
 
 // Threads of a row, each with C times 16 values of it.
@@ -737,8 +737,8 @@ cudaError_t launch_block_norm_grad(const a2av_plan_s &p, const BlockNormArgs &a,
     BlockNormArgs b = a;
     if (token) b.d_gate = nullptr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.g.H / 4 + 31) / 32, kOutGate + (per_rank ? a.g.R : 1));
-    cfg.blockDim = dim3(32 * kSumWarps);
+    cfg.gridDim = dim3((a.g.H / 4 + 7) / 8, 2);
+    cfg.blockDim = dim3(8 * kSumGroups);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
