@@ -92,17 +92,20 @@ __device__ __forceinline__ void prefetch_row(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// Sums of N values over the block, of which every thread gets all.  With two, a warp's halves take one each, so both cost
-// little more than one.  `part` holds zeros where there is no warp, and is free again after the next barrier.
+// Sums of N values over the block, of which every thread gets all.  With two a warp's halves take one each, with four its
+// quarters, so that they cost little more than one.  `part` holds zeros where there is no warp, and is free again after the next barrier.
 template <int N, int W>
 __device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[W]) {
-    static_assert((N == 1 || N == 2) && (W == 16 || W == 32), "values, warps");
+    static_assert((N == 1 || N == 2 || N == 4) && (W == 16 || (W == 32 && N < 4)), "values, warps");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kLanes = 32 / N;  // that carry a value: lane / kLanes names it
     float s = v[0];
-    if constexpr (N == 2) {
-        const bool up = lane & 16;
-        s = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+    const bool up = lane & 16, odd = lane & 8;
+    if constexpr (N == 2) s = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+    if constexpr (N == 4) {
+        const float b0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+        const float b1 = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+        s = (odd ? b1 : b0) + __shfl_xor_sync(0xffffffffu, odd ? b0 : b1, 8);
     }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -396,9 +399,6 @@ __device__ __host__ inline void block_rows(const Geometry &g, bool per_rank, int
     end = rank * rows + rows * (c + 1) / parts;
 }
 
-// Rows of up to 7168 leave room in shared memory for the weights in fp32 beside two blocks' sums.
-constexpr bool weight_shared(int threads) { return threads <= 448; }
-
 __device__ __forceinline__ bool sum_branch(const BlockNormArgs &a) {
     return a.d_post || (a.d_gate && a.gate_kind != A2AV_GATE_TOKEN);
 }
@@ -416,8 +416,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
     const int col = in ? threadIdx.x * kEach : 0, left = H - col;
     ulonglong2 *const coef = smem + threadIdx.x;
     ulonglong2 *const acc[kSums] = {coef + 4 * width, coef + 8 * width};
-    constexpr bool kWeightShared = weight_shared(kThreads);
-    ulonglong2 *const weight32 = coef + 12 * width;  // the next norm's weights, unpacked, where there is room
     {
         const pair zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int q = 0; q < kSums; ++q) st_shared(acc[q], width, zero);
@@ -429,11 +427,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
     const float inv_h = 1.0f / (float)H;
     const pair alpha = both(a.residual_scale);
     if (row < end) set_coef<1>(a, kToken || !a.gate ? nullptr : gate_row(a, row), coef, width);
-    if (kWeightShared && a.d_y) {
-        pair w[8];
-        unpack16(ld_weight(a.weight + col, left), w);
-        st_shared(weight32, width, w);
-    }
     const uint16_t *const weight = a.weight + col;
     for (; row < end; ++row) {
         if (!row_active(a, row)) continue;
@@ -470,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
         pair z[8], zz = both(0.0f), vz = both(0.0f);
         {
             Bits wv;
-            if (!kWeightShared && a.d_y) wv = ld_weight(weight, left);
+            if (a.d_y) wv = ld_weight(weight, left);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // four values at a time: what they need is soon free again
                 pair x[2], f[2], r[2], dy[2], w[2];
@@ -484,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
                     zz = fma2(z[2 * q + e], z[2 * q + e], zz);
                 }
                 if (a.d_y) {
-                    if (kWeightShared) ld_quarter(weight32, width, q, w);
-                    else unpack4(wv, q, w);
+                    unpack4(wv, q, w);
                     unpack4(dyv, q, dy);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) vz = fma2(mul2(dy[e], w[e]), z[2 * q + e], vz);
@@ -508,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
             const pair root2 = both(r2), less2 = both(-c2);
             Bits wv;
             uint32_t dr[8], dg[8];
-            if (!kWeightShared && a.d_y) wv = ld_weight(weight, left);
+            if (a.d_y) wv = ld_weight(weight, left);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 pair dz[2], x[2], n[2], f[2], t[2];
@@ -516,8 +508,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
                 if (a.d_y) {
                     pair dy[2], w[2];
                     unpack4(dyv, q, dy);
-                    if (kWeightShared) ld_quarter(weight32, width, q, w);
-                    else unpack4(wv, q, w);
+                    unpack4(wv, q, w);
                     if (a.d_weight) {
                         ld_quarter(acc[kSumWeight], width, q, t);
 #pragma unroll
@@ -589,6 +580,223 @@ __global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(cons
             }
 }
 
+// Rows of up to 8192 two at a time: both rows' values are in registers (128 a thread), the factors, the weights in fp32
+// and the sums over the tokens are read from shared memory once for both, and a block sum serves both.  That is half the
+// shared-memory traffic and half the barriers of the form above, which takes the longer rows.
+template <bool kPost, bool kToken, bool k32>
+__global__ void __launch_bounds__(512, 1) block_norm_grad_pair_kernel(const BlockNormArgs a, bool per_rank) {
+    extern __shared__ __align__(16) ulonglong2 smem[];
+    constexpr int W = 16;
+    __shared__ __align__(16) float parts[2 * 3 * 4 * W];
+    auto part = reinterpret_cast<float(*)[3][4][W]>(parts);  // [parity of the turn][which sum]
+    clear_parts(parts);
+    const int H = a.g.H, width = blockDim.x;
+    const bool branch = sum_branch(a), in = (int)threadIdx.x * kEach < H;
+    // a thread behind the row's end loads what the first one does and takes no part in sums and stores
+    const int col = in ? threadIdx.x * kEach : 0, left = H - col;
+    ulonglong2 *const coef = smem + threadIdx.x, *const weight = coef + 4 * width;
+    ulonglong2 *const acc[kSums] = {coef + 8 * width, coef + 12 * width};
+    {
+        const pair zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int q = 0; q < kSums; ++q) st_shared(acc[q], width, zero);
+    }
+    long long next, end;
+    block_rows(a.g, per_rank, gridDim.x, blockIdx.x, next, end);
+    grid_dependency_wait();
+    const float inv_h = 1.0f / (float)H;
+    const pair alpha = both(a.residual_scale);
+    if (next < end) set_coef<1>(a, kToken || !a.gate ? nullptr : gate_row(a, next), coef, width);
+    if (a.d_y) {
+        pair w[8];
+        unpack16(ld_weight(a.weight + col, left), w);
+        st_shared(weight, width, w);
+    }
+    auto take = [&] {  // the next row that takes part, or -1
+        while (next < end && !row_active(a, next)) ++next;
+        return next < end ? next++ : -1;
+    };
+    for (int parity = 0;; parity ^= 1) {
+        const long long row0 = take(), row1 = row0 < 0 ? -1 : take();
+        if (row0 < 0) break;
+        const bool two = row1 >= 0;  // else the first one's values stand in for the second's, and go nowhere
+        const size_t at[2] = {(size_t)row0 * H + col, (size_t)(two ? row1 : row0) * H + col};
+        Bits xv[2], rv[2], dyv[2], drv[2], gv[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            xv[r] = ld16<k32>(a.x + at[r], left);
+            rv[r] = ld16<k32>(a.residual + at[r], left);
+            if (a.d_y) dyv[r] = ld16<k32>(a.d_y + at[r], left);
+            if (a.d_residual_out) drv[r] = ld16<k32>(a.d_residual_out + at[r], left);
+            else drv[r] = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
+            if (kToken) gv[r] = ld16<k32>(a.gate + at[r], left);
+        }
+        if (next < end && threadIdx.x < 5) {  // the next two rows on their way into L2
+            const int t = threadIdx.x;
+            const uint16_t *from = t == 0   ? a.x
+                                   : t == 1 ? a.residual
+                                   : t == 2 ? a.d_y
+                                   : t == 3 ? a.d_residual_out
+                                   : kToken ? a.gate
+                                            : nullptr;
+            if (from) prefetch_row(from + (size_t)next * H, (next + 1 < end ? 4 : 2) * H);
+        }
+        float r1[2] = {1.0f, 1.0f};
+        if (kPost) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                pair s = both(0.0f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    pair x[2];
+                    unpack4(xv[r], q, x);
+                    s = fma2(x[1], x[1], fma2(x[0], x[0], s));
+                }
+                r1[r] = in ? sum2(s) : 0.0f;
+            }
+            block_sum<2, W>(r1, part[parity][0]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                r1[r] = rsqrtf(fmaf(r1[r], inv_h, a.eps));
+                keep_packed(xv[r]);
+            }
+        }
+        pair z[2][8];
+        float r2[2] = {0.0f, 0.0f}, c2[2] = {0.0f, 0.0f};
+        {
+            pair zz[2] = {0, 0}, vz[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                pair f[2], w[2];
+                ld_quarter(coef, width, q, f);
+                if (a.d_y) ld_quarter(weight, width, q, w);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    pair x[2], y[2], dy[2], c[2] = {f[0], f[1]};
+                    unpack4(xv[r], q, x);
+                    unpack4(rv[r], q, y);
+                    if (kToken) scale4(c, gv[r], q);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        pair &to = z[r][2 * q + e];
+                        to = fma2(kPost ? mul2(x[e], both(r1[r])) : x[e], c[e], mul2(y[e], alpha));
+                        zz[r] = fma2(to, to, zz[r]);
+                    }
+                    if (a.d_y) {
+                        unpack4(dyv[r], q, dy);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) vz[r] = fma2(mul2(dy[e], w[e]), z[r][2 * q + e], vz[r]);
+                    }
+                }
+            }
+            if (a.d_y) {
+                float sum[4] = {in ? sum2(zz[0]) : 0.0f, in ? sum2(zz[1]) : 0.0f, in ? sum2(vz[0]) : 0.0f,
+                                in ? sum2(vz[1]) : 0.0f};
+                block_sum<4, W>(sum, part[parity][1]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    r2[r] = rsqrtf(fmaf(sum[r], inv_h, a.eps));
+                    c2[r] = r2[r] * r2[r] * r2[r] * (sum[2 + r] * inv_h);
+                    keep_packed(xv[r]);
+                    keep_packed(dyv[r]);
+                    if (kToken) keep_packed(gv[r]);
+                }
+            }
+        }
+        pair nx[2] = {0, 0};
+        if (in) {
+            uint32_t dr[2][8], dg[2][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                pair f[2], w[2], t[2], b[2];
+                ld_quarter(coef, width, q, f);
+                if (a.d_y) ld_quarter(weight, width, q, w);
+                if (a.d_weight) ld_quarter(acc[kSumWeight], width, q, t);
+                if (branch) ld_quarter(acc[kSumBranch], width, q, b);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    pair dz[2], x[2], n[2], c[2] = {f[0], f[1]};
+                    unpack4(drv[r], q, dz);
+                    if (a.d_y) {
+                        pair dy[2];
+                        unpack4(dyv[r], q, dy);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const pair zr = mul2(z[r][2 * q + e], both(r2[r]));
+                            if (a.d_weight && (r == 0 || two)) t[e] = fma2(dy[e], zr, t[e]);
+                            dz[e] = fma2(both(-c2[r]), z[r][2 * q + e], fma2(mul2(dy[e], w[e]), both(r2[r]), dz[e]));
+                        }
+                    }
+                    unpack4(xv[r], q, x);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        dr[r][2 * q + e] = bf16_of(mul2(dz[e], alpha));
+                        n[e] = kPost ? mul2(x[e], both(r1[r])) : x[e];
+                    }
+                    if (kToken) {  // b * dz * u
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) dg[r][2 * q + e] = bf16_of(mul2(mul2(dz[e], c[e]), n[e]));
+                        scale4(c, gv[r], q);
+                    }
+                    if (branch && (r == 0 || two)) {
+                        pair d[2] = {dz[0], dz[1]};
+                        if (kToken) scale4(d, gv[r], q);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) b[e] = fma2(d[e], n[e], b[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        pair &dn = z[r][2 * q + e];  // in z's place: the gradient of n = x * r1
+                        dn = mul2(dz[e], c[e]);
+                        if (kPost) nx[r] = fma2(dn, x[e], nx[r]);
+                    }
+                }
+                if (a.d_weight) st_quarter(acc[kSumWeight], width, q, t);
+                if (branch) st_quarter(acc[kSumBranch], width, q, b);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (r == 0 || two) {
+                    st16<k32>(a.d_residual + at[r], left, make_uint4(dr[r][0], dr[r][1], dr[r][2], dr[r][3]),
+                              make_uint4(dr[r][4], dr[r][5], dr[r][6], dr[r][7]));
+                    if (kToken && a.d_gate)
+                        st16<k32>(static_cast<uint16_t *>(a.d_gate) + at[r], left,
+                                  make_uint4(dg[r][0], dg[r][1], dg[r][2], dg[r][3]),
+                                  make_uint4(dg[r][4], dg[r][5], dg[r][6], dg[r][7]));
+                }
+        }
+        float c1[2] = {sum2(nx[0]), sum2(nx[1])};
+        if (kPost) {
+            block_sum<2, W>(c1, part[parity][2]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                c1[r] = r1[r] * r1[r] * r1[r] * (c1[r] * inv_h);
+                keep_packed(xv[r]);
+            }
+        }
+        if (in)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (kPost)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        pair x[2];
+                        unpack4(xv[r], q, x);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            z[r][2 * q + e] = fma2(z[r][2 * q + e], both(r1[r]), mul2(x[e], both(-c1[r])));
+                    }
+                if (r == 0 || two) store16<k32>(a.d_x + at[r], left, z[r]);
+            }
+    }
+    if (in)
+        for (int q = 0; q < kSums; ++q)
+            if (q == kSumWeight ? a.d_weight != nullptr : branch) {
+                ulonglong2 *out =
+                    reinterpret_cast<ulonglong2 *>(a.scratch + ((size_t)blockIdx.x * kSums + q) * H + col);
+                for (int e = 0; e < (left > 8 ? 4 : 2); ++e) out[e] = acc[q][e * width];
+            }
+}
+
 // The blocks' sums S added up: d_weight = sum S (blockIdx.y 0); S_r = sum S over the blocks of rank r (of all, without
 // a gate per rank), d_gate[r] = b * post * S_r, d_post = b * sum_r gate[r] * S_r (blockIdx.y 1).  A block takes 32
 // columns, eight threads in 32 groups: each group adds up a share of one rank's blocks, the shares and then the ranks are
@@ -644,19 +852,21 @@ __global__ void __launch_bounds__(8 * kSumGroups) norm_sums_kernel(const BlockNo
 // Threads of a row, each with C times 16 values of it.
 int row_threads(int H, int C = 1) { return ((H + kEach * C - 1) / (kEach * C) + 31) / 32 * 32; }
 
-// Blocks of `threads` threads and `smem` bytes each that an SM holds, with 64 registers a thread.
-int blocks_per_sm(int threads, size_t smem) {
-    const int by_threads = 1024 / threads, by_smem = (int)(228 * 1024 / (smem + 2 * 1024));  // static ones, and 1 KiB of the system's
-    const int n = by_threads < by_smem ? by_threads : by_smem;
+// Blocks of `threads` threads and `smem` bytes each that an SM holds, with `regs` registers a thread.
+int blocks_per_sm(int threads, int regs, size_t smem) {
+    const int by_regs = 65536 / (threads * regs), by_smem = (int)(228 * 1024 / (smem + 3 * 1024));
+    const int n = by_regs < by_smem ? by_regs : by_smem;
     return n < 1 ? 1 : n > 16 ? 16 : n;
 }
 size_t coef_bytes(int H, int C = 1) { return (size_t)row_threads(H, C) * C * kEach * sizeof(float); }
-size_t grad_smem(int H) { return coef_bytes(H) * (1 + kSums + weight_shared(row_threads(H))); }
+constexpr int kPairRow = 8192;  // rows of the gradient's form that takes two at a time, at most
+size_t grad_smem(int H) { return coef_bytes(H) * (1 + kSums + (H <= kPairRow)); }
 
 // Blocks of the gradient: what the SMs hold, at most one per row, a multiple of R where each keeps to a rank.
 int grad_blocks(int num_sms, const Geometry &g, bool per_rank) {
     const long long rows = (long long)g.R * g.T;
-    const long long most = (long long)num_sms * blocks_per_sm(row_threads(g.H), grad_smem(g.H));
+    const long long most =
+        (long long)num_sms * blocks_per_sm(row_threads(g.H), g.H <= kPairRow ? 128 : 64, grad_smem(g.H));
     if (!per_rank) return (int)(rows < most ? rows : most);
     const long long parts = most / g.R < 1 ? 1 : most / g.R;
     return g.R * (int)(g.T < parts ? g.T : parts);
@@ -680,7 +890,7 @@ cudaError_t launch_norm(const a2av_plan_s &p, const BlockNormArgs &a, cudaStream
     const cudaError_t e = allow_smem(kernel, done, p.cfg.device, coef_bytes(kMaxNormRow, C));
     if (e != cudaSuccess) return e;
     const int threads = row_threads(a.g.H, C);
-    const long long rows = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * blocks_per_sm(threads, smem);
+    const long long rows = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * blocks_per_sm(threads, 64, smem);
     return launch_pdl(kernel, (int)(rows < cap ? rows : cap), threads, smem, s, a);
 }
 
@@ -691,20 +901,15 @@ cudaError_t launch_norm_rows(const a2av_plan_s &p, const BlockNormArgs &a, cudaS
     return launch_norm<1, 512, 2, kPost, kToken, k32>(p, a, s);
 }
 
-template <int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
-cudaError_t launch_grad(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, cudaStream_t s) {
-    static std::atomic<uint64_t> done{0};
-    const auto kernel = block_norm_grad_kernel<kThreads, kBlocks, kPost, kToken, k32>;
-    const cudaError_t e = allow_smem(kernel, done, p.cfg.device, grad_smem(kMaxNormGradRow));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, blocks, row_threads(a.g.H), grad_smem(a.g.H), s, a, a.gate_kind == A2AV_GATE_RANK);
-}
-
 template <bool kPost, bool kToken, bool k32>
 cudaError_t launch_grad_rows(const a2av_plan_s &p, const BlockNormArgs &a, int blocks, cudaStream_t s) {
-    if (a.g.H > 8192) return launch_grad<1024, 1, kPost, kToken, k32>(p, a, blocks, s);
-    if (a.g.H > 7168) return launch_grad<512, 2, kPost, kToken, k32>(p, a, blocks, s);
-    return launch_grad<448, 2, kPost, kToken, k32>(p, a, blocks, s);  // room for 72 registers a thread
+    static std::atomic<uint64_t> done[2];
+    const bool pairs = a.g.H <= kPairRow;
+    const auto kernel =
+        pairs ? block_norm_grad_pair_kernel<kPost, kToken, k32> : block_norm_grad_kernel<1024, 1, kPost, kToken, k32>;
+    const cudaError_t e = allow_smem(kernel, done[pairs], p.cfg.device, grad_smem(pairs ? kPairRow : kMaxNormGradRow));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, blocks, row_threads(a.g.H), grad_smem(a.g.H), s, a, a.gate_kind == A2AV_GATE_RANK);
 }
 
 // f<kPost, kToken, k32>, by what the call has.
