@@ -856,7 +856,7 @@ int row_threads(int H, int C = 1) { return ((H + kEach * C - 1) / (kEach * C) + 
 int blocks_per_sm(int threads, int regs, size_t smem) {
     const int by_regs = 65536 / (threads * regs), by_smem = (int)(228 * 1024 / (smem + 3 * 1024));
     const int n = by_regs < by_smem ? by_regs : by_smem;
-    return n < 1 ? 1 : n > 16 ? 16 : n;
+    return n < 1 ? 1 : n > 32 ? 32 : n;
 }
 size_t coef_bytes(int H, int C = 1) { return (size_t)row_threads(H, C) * C * kEach * sizeof(float); }
 constexpr int kPairRow = 8192;  // rows of the gradient's form that takes two at a time, at most

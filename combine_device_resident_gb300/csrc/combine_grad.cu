@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4 / V) combine_grad_piped_kernel(
 template <int V, bool kRows, bool kGates>
 cudaError_t launch_piped(const a2av_plan_s &p, const CombineGradArgs &a, cudaStream_t s) {
     const int block = ((a.g.H / 8 + V - 1) / V + 31) / 32 * 32, fit = 65536 / (32 * V) / block;
-    const long long ntok = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * (fit < 1 ? 1 : fit > 16 ? 16 : fit);
+    const long long ntok = (long long)a.g.R * a.g.T, cap = (long long)p.num_sms * (fit < 1 ? 1 : fit > 32 ? 32 : fit);
     return launch_pdl(combine_grad_piped_kernel<V, kRows, kGates>, (int)(ntok < cap ? ntok : cap), block, 0, s, a);
 }
 
