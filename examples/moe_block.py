@@ -2,6 +2,9 @@
 
     norm (+ residual)  ->  router  ->  dispatch  ->  experts (SwiGLU, down)  ->  combine
 
+With ``sandwich`` what comes in from the block before is normed, gated and scaled before it joins the
+residual stream; with a ``rule`` the router chooses by scores (sigmoid or softmax, a bias for balance, groups).
+
 Routing stays on the GPU, nothing is padded and nothing synchronises, so the block is one CUDA
 graph.  Three forms of the experts:
 
@@ -34,9 +37,12 @@ class MoeBlock:
     Weights are random; ``w_norm`` [H], ``w_router`` [E][H], gate and up ``w_in`` [E][2F][H], ``w_out`` [E][H][F].
     All buffers are made here; ``__call__`` only enqueues kernels on the current stream."""
 
-    def __init__(self, R, E, T, H, F, k, form="bf16", group=64, device="cuda:0", seed=0):
+    def __init__(self, R, E, T, H, F, k, form="bf16", group=64, device="cuda:0", seed=0, rule=None, sandwich=False,
+                 residual_scale=1.0, branch_scale=1.0):
         if form not in FORMS:
             raise ValueError(f"form must be one of {FORMS}, got {form!r}")
+        self.rule, self.sandwich = rule, sandwich
+        self.residual_scale, self.branch_scale = residual_scale, branch_scale
         self.form, self.eps = form, 1e-6
         self.R, self.E, self.T, self.H, self.F, self.k = R, E, T, H, F, k
         dev = torch.device(device)
@@ -49,6 +55,10 @@ class MoeBlock:
         self.w_router = normal(E, H, std=H ** -0.5).to(torch.bfloat16)
         self.router32 = self.w_router.float().T             # what its product takes, laid out once
         w_in, w_out = normal(E, 2 * F, H, std=H ** -0.5), normal(E, H, F, std=F ** -0.5)
+        # the norm behind the block before and its gate per channel; the experts' bias for the choice
+        self.w_post = (1.0 + normal(H, std=0.1)).to(torch.bfloat16) if sandwich else None
+        self.block_gate = (0.5 + normal(H, std=0.1)).to(torch.bfloat16) if sandwich else None
+        self.bias = torch.zeros(E, device=dev) if rule is not None else None
         self.s_in = self.s_out = None
         if form == "bf16":
             self.w_in, self.w_out = w_in.to(torch.bfloat16), w_out.to(torch.bfloat16)
@@ -79,14 +89,24 @@ class MoeBlock:
         self.inner8 = self.plan.new_rows8(arena, F) if form == "8bit" else None
         self.expert_out = torch.empty(arena, H, **bf)
 
-    def __call__(self, x, residual):
-        """The experts' weighted output for x + residual, normed; the sum goes into ``residual`` (the next
-        block's residual stream)."""
+    def __call__(self, x, residual, residual_out=None):
+        """The experts' weighted output for x + residual, normed; the sum goes into ``residual_out``, or where none
+        is given into ``residual`` (the next block's residual stream)."""
         p, rows = self.plan, self.rows_plan
-        p.rms_norm(x, self.w_norm, y=self.y, rows8=self.rows8, residual=residual, residual_out=residual, eps=self.eps)
+        residual_out = residual if residual_out is None else residual_out
+        if self.sandwich:
+            p.block_norm(x, residual, residual_out=residual_out, weight=self.w_norm, y=self.y, rows8=self.rows8,
+                         post_weight=self.w_post, gate=self.block_gate, residual_scale=self.residual_scale,
+                         branch_scale=self.branch_scale, eps=self.eps)
+        else:
+            p.rms_norm(x, self.w_norm, y=self.y, rows8=self.rows8, residual=residual, residual_out=residual_out,
+                       eps=self.eps)
         self.y32.copy_(self.y.view(-1, self.H))
         torch.mm(self.y32, self.router32, out=self.logits.view(-1, self.E))  # the router's projection, a library product
-        p.route(self.logits, self.topk, self.gate)
+        if self.rule is None:
+            p.route(self.logits, self.topk, self.gate)
+        else:
+            p.route_scores(self.logits, self.topk, self.gate, self.rule, bias=self.bias)
         sent = self.y if self.form != "8bit" else self.rows8.view(torch.bfloat16)
         rows.dispatch(sent, self.topk, self.splits, self.recv, self.slot_map)
         if self.form == "bf16":
@@ -123,8 +143,13 @@ def main(argv=None):
     ap.add_argument("--inner", type=int, default=2048, help="an expert's inner width")
     ap.add_argument("--topk", type=int, default=2)
     ap.add_argument("--steps", type=int, default=50)
+    ap.add_argument("--sandwich", action="store_true", help="norm, gate and scale behind the block before")
+    ap.add_argument("--score", choices=["softmax", "sigmoid"], help="route by scores with a bias (default: by logits)")
+    ap.add_argument("--groups", type=int, default=1, help="with --score: groups of experts")
+    ap.add_argument("--groups-kept", type=int, help="of these, how many a token may choose from")
     a = ap.parse_args(argv)
-    block = MoeBlock(a.ranks, a.experts, a.tokens, a.hidden, a.inner, a.topk, a.form)
+    rule = a2av.RouteRule(score=a.score, groups=a.groups, groups_kept=a.groups_kept) if a.score else None
+    block = MoeBlock(a.ranks, a.experts, a.tokens, a.hidden, a.inner, a.topk, a.form, rule=rule, sandwich=a.sandwich)
     dev = block.out.device
     x = torch.randn(a.ranks, a.tokens, a.hidden, device=dev).to(torch.bfloat16)
     residual = torch.randn_like(x)
