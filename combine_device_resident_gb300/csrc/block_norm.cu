@@ -57,11 +57,6 @@ __device__ __forceinline__ pair mul2(pair a, pair b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ pair add2(pair a, pair b) {
-    pair d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
     pair d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -77,16 +72,6 @@ __device__ __forceinline__ uint32_t bf16_of(pair p) {
     split(p, lo, hi);
     return bf16x2(lo, hi);
 }
-// Eight bf16 values as four pairs, and back.
-__device__ __forceinline__ void unpack8(const uint4 &v, pair (&f)[4]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = both(lo_f(w[i]), hi_f(w[i]));
-}
-__device__ __forceinline__ uint4 pack8(const pair (&f)[4]) {
-    return make_uint4(bf16_of(f[0]), bf16_of(f[1]), bf16_of(f[2]), bf16_of(f[3]));
-}
-
 // Brings `bytes` (a multiple of 16) into L2.
 __device__ __forceinline__ void prefetch_row(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -403,10 +388,10 @@ __device__ __forceinline__ bool sum_branch(const BlockNormArgs &a) {
     return a.d_post || (a.d_gate && a.gate_kind != A2AV_GATE_TOKEN);
 }
 
-template <int kThreads, int kBlocks, bool kPost, bool kToken, bool k32>
-__global__ void __launch_bounds__(kThreads, kBlocks) block_norm_grad_kernel(const BlockNormArgs a, bool per_rank) {
+template <bool kPost, bool kToken, bool k32>
+__global__ void __launch_bounds__(1024, 1) block_norm_grad_kernel(const BlockNormArgs a, bool per_rank) {
     extern __shared__ __align__(16) ulonglong2 smem[];
-    constexpr int W = warps_of(kThreads);
+    constexpr int W = 32;
     __shared__ __align__(16) float parts[3 * 2 * 2 * W];
     auto part = reinterpret_cast<float(*)[2][2][W]>(parts);  // [which sum][row parity]
     clear_parts(parts);
@@ -906,7 +891,7 @@ cudaError_t launch_grad_rows(const a2av_plan_s &p, const BlockNormArgs &a, int b
     static std::atomic<uint64_t> done[2];
     const bool pairs = a.g.H <= kPairRow;
     const auto kernel =
-        pairs ? block_norm_grad_pair_kernel<kPost, kToken, k32> : block_norm_grad_kernel<1024, 1, kPost, kToken, k32>;
+        pairs ? block_norm_grad_pair_kernel<kPost, kToken, k32> : block_norm_grad_kernel<kPost, kToken, k32>;
     const cudaError_t e = allow_smem(kernel, done[pairs], p.cfg.device, grad_smem(pairs ? kPairRow : kMaxNormGradRow));
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, blocks, row_threads(a.g.H), grad_smem(a.g.H), s, a, a.gate_kind == A2AV_GATE_RANK);

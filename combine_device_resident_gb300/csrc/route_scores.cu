@@ -16,6 +16,8 @@
 // one left out.  Lane kernel (E up to 256, k up to 8): four lanes per token, below.
 #include <float.h>
 
+#include <type_traits>
+
 #include "block_ops.cuh"
 #include "expert_common.cuh"
 #include "route_select.cuh"
@@ -338,12 +340,13 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const ScoreAr
 //   1. choices in place of logits; a copy of them in shared memory, for the few that are looked up by number later;
 //   2. groups: two best per lane and group, merged so that lane r ends with groups r, r + 4; ranks by counting;
 //   3. tau, a lower bound of the KMAX-th largest choice: the KMAX-th largest of maxima of disjoint sets (a lane's kept
-//      groups, or its units' components), as in the plain router's lane kernel;
+//      units, by component);
 //   4. the choices at or above tau (some ten of 256 for KMAX = 8) as bits, then as a list in shared memory;
 //   5. each one's rank by counting those at or above it, a lane taking every fourth; ranks below k are the answer.
-// A tie leaves a rank empty, and near neighbours are seen: the warp then orders that token's list in 64 bits (with a bias
-// tau is lowered by the choices' errors, so that the list holds whatever may lie at the border).  A list that is too
-// long, or groups that are too near: route_one.
+// A tie leaves a rank empty, and near neighbours are seen.  Then the warp ranks once more, equal choices by id, which is
+// right where they come from equal logits and biases; for the rest it orders the token's list in 64 bits (with a bias tau is lowered
+// by the choices' errors, so that the list holds whatever may lie at the border).  Groups that are too near are settled
+// in 64 bits before tau (keep_exact).  A list that is too long: route_one.
 constexpr int kList = 32;  // candidates of a token
 constexpr int kRanks = 12;
 
@@ -398,7 +401,8 @@ __host__ __device__ constexpr int lane_stride(int E) { return (E / 4 + 7) / 8 * 
 struct LaneList {
     float key[8][kList + 4];  // candidates of the eight tokens, NaN behind them
     float best[8][kRanks];    // by rank; NaN where there is none
-    uint8_t id[8][kList], best_id[8][kRanks + 4];
+    alignas(4) uint8_t id[8][kList];
+    uint8_t best_id[8][kRanks + 4];
 };
 // A warp's share: the choices of eight tokens (also room for the warp kernel's token), the lists.
 __host__ __device__ constexpr size_t lane_warp_bytes(int E) { return (size_t)8 * lane_stride(E) * 16 + sizeof(LaneList); }
@@ -515,7 +519,7 @@ __device__ __noinline__ uint32_t keep_exact(const ScoreArgs &a, int u, const flo
 
 // kFull: E is 16 * NU, so no unit is missing.
 template <int NU, int KMAX, int G, bool kFull>
-__global__ void __launch_bounds__(32 * kWarps, 5) route_scores_lane_kernel(const ScoreArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int L = tau_values<KMAX>();
     const int E = a.g.E, k = a.g.k, nu = E / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -597,7 +601,6 @@ __global__ void __launch_bounds__(32 * kWarps, 5) route_scores_lane_kernel(const
         // 2. groups: which are kept, as bits
         bool near = false;
         uint32_t keep = ~0u;
-        float peak[G];  // of this lane's choices in each group
         if constexpr (G > 1) {
             constexpr int UG = NU / G;
             float b1[G], b2[G];
@@ -615,8 +618,6 @@ __global__ void __launch_bounds__(32 * kWarps, 5) route_scores_lane_kernel(const
                         merge2(b1[g], b2[g], u1, u2);
                     }
                 }
-#pragma unroll
-            for (int g = 0; g < G; ++g) peak[g] = b1[g];
             // halved over lane ^ 1, then over lane ^ 2: this lane ends with groups r, r + 4
             float h1[G / 2], h2[G / 2], q1[G / 4], q2[G / 4];
 #pragma unroll
@@ -693,35 +694,20 @@ __global__ void __launch_bounds__(32 * kWarps, 5) route_scores_lane_kernel(const
         // 3. the bound
         float tau;
         {
-            float c[4];
-            if constexpr (G > 1) {
+            float c[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            // maxima of the kept units' components
 #pragma unroll
-                for (int g = 0; g < G; ++g) peak[g] = keep >> g & 1 ? peak[g] : -INFINITY;
+            for (int j = 0; j < NU; ++j)
+                if (G == 1 || (keep >> (j / (NU / G)) & 1))
 #pragma unroll
-                for (int i = 0; i < 4; ++i) c[i] = peak[i];
-                sort4(c);
-                if constexpr (G == 8) {  // the four best of both halves
-                    float d[4] = {peak[4], peak[5], peak[6], peak[7]};
-                    sort4(d);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], d[3 - i]);
-                    sort4(c);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    c[i] = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < NU; ++j) c[i] = fmaxf(c[i], part_of(v[j], i));
-                }
-                if (L == 4) sort4(c);
-                if (L == 2) {
-                    c[0] = fmaxf(c[0], c[2]);
-                    c[1] = fmaxf(c[1], c[3]);
-                    order2(c[0], c[1]);
-                }
-                if (L == 1) c[0] = fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3]));
+                    for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], part_of(v[j], i));
+            if (L == 4) sort4(c);
+            if (L == 2) {
+                c[0] = fmaxf(c[0], c[2]);
+                c[1] = fmaxf(c[1], c[3]);
+                order2(c[0], c[1]);
             }
+            if (L == 1) c[0] = fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3]));
             float g[L];
 #pragma unroll
             for (int i = 0; i < L; ++i) g[i] = c[i];
@@ -761,39 +747,65 @@ __global__ void __launch_bounds__(32 * kWarps, 5) route_scores_lane_kernel(const
         __syncwarp();
 
         // 5. ranks
-        for (int from = r; from < listed; from += 16) {
-            float own[4];
-            int above[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                own[i] = from + 4 * i < listed ? list.key[t][from + 4 * i] : NAN;
-                above[i] = -1;  // each counts itself
-            }
-            for (int q = 0; q < listed; q += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&list.key[t][q]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) above[i] += (x.x >= own[i]) + (x.y >= own[i]) + (x.z >= own[i]) + (x.w >= own[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (from + 4 * i < listed && above[i] <= k) {
-                    list.best[t][above[i]] = own[i];
-                    list.best_id[t][above[i]] = list.id[t][from + 4 * i];
-                }
-        }
-        __syncwarp();
         constexpr int SL = (KMAX + 3) / 4;  // slots per lane
-        bool again = false;
         int id[SL];
+        // Places the candidates by rank and takes this lane's slots; false where that may not be the order.  by_id: of
+        // equal choices the lower id first, right only for equal logits and biases, which are then compared.
+        auto rank = [&](auto by_id) {
+            constexpr bool kById = decltype(by_id)::value;
+            for (int from = r; from < listed; from += 16) {
+                float own[4];
+                int above[4], own_id[4];
 #pragma unroll
-        for (int i = 0; i < SL; ++i) {
-            const int j = r + 4 * i;
-            id[i] = 0;
-            if (j >= k) continue;
-            const float c = list.best[t][j], next = list.best[t][j + 1];
-            id[i] = list.best_id[t][j];
-            again |= c != c || (a.bias && next == next && too_near(a.sigmoid, top, c, next));
-        }
+                for (int i = 0; i < 4; ++i) {
+                    const bool there = from + 4 * i < listed;
+                    own[i] = there ? list.key[t][from + 4 * i] : NAN;
+                    if (kById) own_id[i] = there ? list.id[t][from + 4 * i] : 0;
+                    above[i] = kById ? 0 : -1;  // each counts itself
+                }
+                for (int q = 0; q < listed; q += 4) {
+                    float4 x = *reinterpret_cast<const float4 *>(&list.key[t][q]);
+                    const uint32_t ids = kById ? *reinterpret_cast<const uint32_t *>(&list.id[t][q]) : 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float o = part_of(x, c);
+                            if (kById) above[i] += o > own[i] || (o == own[i] && (int)(ids >> (8 * c) & 255) < own_id[i]);
+                            else above[i] += o >= own[i];
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (from + 4 * i < listed && above[i] <= k) {
+                        list.best[t][above[i]] = own[i];
+                        list.best_id[t][above[i]] = list.id[t][from + 4 * i];
+                    }
+            }
+            __syncwarp();
+            bool right = true;
+#pragma unroll
+            for (int i = 0; i < SL; ++i) {
+                const int j = r + 4 * i;
+                id[i] = 0;
+                if (j >= k) continue;
+                const float c = list.best[t][j], next = list.best[t][j + 1];
+                id[i] = list.best_id[t][j];
+                bool good = c == c;
+                if (a.bias && next == next && too_near(a.sigmoid, top, c, next)) {
+                    good = false;
+                    if (kById && act && c == next) {
+                        const int other = list.best_id[t][j + 1];
+                        const float *const bias = reinterpret_cast<const float *>(sm);
+                        good = clean_logit(__ldg(row + id[i])) == clean_logit(__ldg(row + other)) && bias[id[i]] == bias[other];
+                    }
+                }
+                right = right && good;
+            }
+            return right;
+        };
+        bool again = !rank(std::false_type{});
+        if (__any_sync(kAll, act && again && n <= kList)) again = !rank(std::true_type{});
         const bool whole = near || n > kList;
         const uint32_t again_all = __ballot_sync(kAll, act && (again || whole));
         const bool ok = act && !(again_all >> (lane & ~3) & 15);
@@ -1067,7 +1079,7 @@ cudaError_t launch_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t 
     if (e != cudaSuccess) return e;
     // few tokens: a warp per block, so that they spread over the SMs
     const int ntask = (int)(((long long)a.g.R * a.g.T + 7) / 8), warps = ntask <= kWarps * p.num_sms ? 1 : kWarps;
-    const int want = (ntask + warps - 1) / warps, cap = p.num_sms * (5 * kWarps / warps);
+    const int want = (ntask + warps - 1) / warps, cap = p.num_sms * (4 * kWarps / warps);
     return launch_pdl(kernel, want < cap ? want : cap, 32 * warps, bytes(a.g.E, warps), s, a);
 }
 

@@ -150,6 +150,39 @@ def test_ties_go_to_the_lower_id(E, k, rule, biased):
     plan.close()
 
 
+@pytest.mark.parametrize("E,k,groups,kept,best", [(64, 6, 1, 1, 1), (256, 8, 8, 4, 2), (256, 8, 4, 1, 1), (128, 2, 1, 1, 1),
+                                                  (512, 8, 8, 4, 2), (30, 5, 1, 1, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [None, "zero", "few"])
+def test_logits_of_few_bits(E, k, groups, kept, best, score, bias):
+    """Logits out of a product in bf16 meet ties in most tokens; a bias starts at zero, or holds a few values."""
+    plan, logits, b = make(2, E, 37, k, 9)
+    logits = logits.bfloat16().float()
+    b = {None: None, "zero": torch.zeros_like(b), "few": torch.round(b * 20) / 20}[bias]
+    check(plan, logits, A.RouteRule(score=score, groups=groups, groups_kept=kept, group_best=best), b)
+    plan.close()
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_any_shape_and_rule(seed):
+    """Seeded sizes, rules and inputs: widths around the kernels' limits, kept groups from one to all."""
+    rng = np.random.default_rng(seed)
+    E = int(rng.choice([4, 8, 12, 16, 20, 28, 32, 40, 44, 60, 64, 68, 100, 128, 132, 160, 192, 252, 256, 260, 320, 512]))
+    R = int(rng.choice([r for r in (1, 2, 4) if E % r == 0]))
+    groups = int(rng.choice([g for g in (1, 1, 2, 4, 8, 16) if E % g == 0]))
+    kept = int(rng.integers(1, groups + 1))
+    k = int(rng.integers(1, min(12, kept * E // groups) + 1))
+    best = int(rng.integers(1, 3)) if E // groups > 1 else 1
+    rule = A.RouteRule(score=str(rng.choice(["softmax", "sigmoid"])), groups=groups, groups_kept=kept, group_best=best,
+                       renormalize=bool(rng.integers(2)), scale=float(rng.choice([1.0, 0.5, 2.5])))
+    plan, logits, bias = make(R, E, int(rng.integers(1, 70)), k, seed)
+    if rng.integers(3) == 0:
+        logits = logits * 20
+    idx, _ = check(plan, logits, rule, bias if rng.integers(2) else None)
+    grad_check(plan, logits, idx, rule, seed)
+    plan.close()
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,kept,best", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
 def test_choices_nearer_than_fp32_tells_apart(score, groups, kept, best):
