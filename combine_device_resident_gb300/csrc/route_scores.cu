@@ -1017,12 +1017,15 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_grad_lane_kernel(con
             val = in ? a.scale * d * __fdiv_rn(v >= 0.0f ? 1.0f : ea, 1.0f + ea) * rest : 0.0f;
         }
         // an id that occurs twice: all its slots' values, added in slot order by each of them
-        const uint32_t same = __match_any_sync(kAll, in ? t << 16 | id : -1 - lane);
-        if (__any_sync(kAll, same & (same - 1))) {
+        bool twice = false;
+#pragma unroll
+        for (int o = 1; o < 8; ++o) twice |= __shfl_xor_sync(kAll, id, o) == id;
+        if (__any_sync(kAll, in && twice)) {
             float all = 0.0f;
             for (int j = 0; j < 8; ++j) {
+                const int other = __shfl_sync(kAll, id, (lane & ~7) + j);
                 const float w = __shfl_sync(kAll, val, (lane & ~7) + j);
-                if (same >> ((lane & ~7) + j) & 1) all += w;
+                if (other == id) all += w;
             }
             val = all;
         }
