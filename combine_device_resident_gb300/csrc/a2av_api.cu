@@ -63,16 +63,16 @@ size_t tokens(const a2av_plan_s *p) { return (size_t)p->g.R * p->g.T; }
 struct Span {
     const void *p;
     size_t n;
-    const void *may_be;  // an input this output may be itself
+    uint32_t may_be;  // the inputs (bits by their place) of which this output may be one itself, in place
 };
 
-// Whether an output overlaps an input (other than the one it may be) or another output.
+// Whether an output overlaps an input (other than one it may be) or another output.
 template <int O, int I>
 bool clash(const Span (&out)[O], const Span (&in)[I]) {
     for (int o = 0; o < O; ++o) {
         if (!out[o].p) continue;
         for (int i = 0; i < I; ++i)
-            if (in[i].p && !(out[o].p == in[i].p && out[o].may_be == in[i].p) &&
+            if (in[i].p && !(out[o].p == in[i].p && (out[o].may_be >> i & 1)) &&
                 overlap(out[o].p, out[o].n, in[i].p, in[i].n))
                 return true;
         for (int q = 0; q < o; ++q)
@@ -718,7 +718,7 @@ a2av_status_t a2av_combine_grad(a2av_plan_t p, const void *d_out, const void *y,
     const int64_t rows = a2av_recv_arena_rows(&p->cfg);
     const size_t ny = (size_t)rows * row_bytes(p), nk = tokens(p) * p->g.k * 4;
     const Span in[4] = {{d_out, tokens(p) * row_bytes(p)}, {y, ny}, {gate_w, nk}, {slot_map, nk}};
-    const Span out[2] = {{d_y, ny, y}, {d_gate, nk}};
+    const Span out[2] = {{d_y, ny, 1u << 1}, {d_gate, nk}};
     if (clash(out, in)) return refuse_call(call, "an output overlaps another tensor");
     DeviceGuard guard(p->cfg.device);
     if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
@@ -754,7 +754,7 @@ a2av_status_t a2av_block_norm(a2av_plan_t p, const a2av_block_norm_t *n, const v
     const size_t rows = tokens(p) * row_bytes(p), row = row_bytes(p);
     const Span in[5] = {{x, rows}, {residual, rows}, {n->post_weight, row}, {n->gate, gate_bytes(p, n->gate_kind)},
                         {n->weight, row}};
-    const Span out[3] = {{residual_out, rows, residual_out == x ? x : residual}, {y, rows},
+    const Span out[3] = {{residual_out, rows, 1u << 0 | 1u << 1}, {y, rows},
                          {rows8, tokens(p) * ((size_t)p->g.H + 16)}};
     if (clash(out, in)) return refuse_call(call, "an output overlaps another tensor");
     DeviceGuard guard(p->cfg.device);
@@ -792,8 +792,9 @@ a2av_status_t a2av_block_norm_grad(a2av_plan_t p, const a2av_block_norm_t *n, co
     const size_t rows = tokens(p) * row_bytes(p), row = row_bytes(p), gate = gate_bytes(p, n->gate_kind);
     const Span in[7] = {{x, rows}, {residual, rows}, {n->post_weight, row}, {n->gate, gate}, {n->weight, row},
                         {d_y, rows}, {d_residual_out, rows}};
-    const Span out[6] = {{d_x, rows, d_y},
-                         {d_residual, rows, d_residual_out},
+    const uint32_t one = d_y == d_residual_out ? 1u << 5 | 1u << 6 : 0;  // a tensor that is both gradients
+    const Span out[6] = {{d_x, rows, 1u << 5 | one},
+                         {d_residual, rows, 1u << 6 | one},
                          {d_weight, 2 * row},
                          {d_post_weight, 2 * row},
                          {d_gate, n->gate_kind == A2AV_GATE_TOKEN ? gate : 2 * gate},

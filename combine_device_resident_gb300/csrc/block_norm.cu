@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(1024, 1) block_norm_grad_kernel(const BlockNor
             float sum[2] = {in ? sum2(zz) : 0.0f, in ? sum2(vz) : 0.0f};
             block_sum<2, W>(sum, part[1][parity]);
             r2 = rsqrtf(fmaf(sum[0], inv_h, a.eps));
-            c2 = r2 * r2 * r2 * (sum[1] * inv_h);
+            c2 = r2 * (r2 * (r2 * (sum[1] * inv_h)));  // the cube alone may overflow
             keep_packed(xv);
             keep_packed(dyv);
             if (kToken) keep_packed(gv);
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(1024, 1) block_norm_grad_kernel(const BlockNor
         if (kPost) {
             float sum[1] = {sum2(nx)};
             block_sum<1, W>(sum, part[2][parity]);
-            c1 = r1 * r1 * r1 * (sum[0] * inv_h);
+            c1 = r1 * (r1 * (r1 * (sum[0] * inv_h)));
             keep_packed(xv);
         }
         if (in) {
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(512, 1) block_norm_grad_pair_kernel(const Bloc
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     r2[r] = rsqrtf(fmaf(sum[r], inv_h, a.eps));
-                    c2[r] = r2[r] * r2[r] * r2[r] * (sum[2 + r] * inv_h);
+                    c2[r] = r2[r] * (r2[r] * (r2[r] * (sum[2 + r] * inv_h)));  // the cube alone may overflow
                     keep_packed(xv[r]);
                     keep_packed(dyv[r]);
                     if (kToken) keep_packed(gv[r]);
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(512, 1) block_norm_grad_pair_kernel(const Bloc
             block_sum<2, W>(c1, part[parity][2]);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                c1[r] = r1[r] * r1[r] * r1[r] * (c1[r] * inv_h);
+                c1[r] = r1[r] * (r1[r] * (r1[r] * (c1[r] * inv_h)));
                 keep_packed(xv[r]);
             }
         }

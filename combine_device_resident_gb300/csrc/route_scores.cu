@@ -49,8 +49,9 @@ __device__ __forceinline__ float fast_sigmoid(float l) {
 }
 
 // Bound of the error of an fp32 choice of size |c|.  Sigmoid: fast_sigmoid's, and the bias' addition.  Softmax: every
-// score is at most `top`; exponential, sum (at most 32 terms in a row, then a tree) and quotient are off by less than
-// 64 * 2^-24 of it together.
+// score is at most `top`; exponential, sum (at most 32 terms in a row, then a tree) and quotient are off by some 70 * 2^-24 of
+// it at most, all but 5 of these by a factor common to the token's scores, so two such bounds (128 * 2^-24) hold a
+// difference's error.
 __device__ __forceinline__ float error_of(bool sigmoid, float top, float c) {
     return (sigmoid ? 2.4f * 0x1p-23f : top * 0x1p-18f) + fabsf(c) * 0x1p-24f;
 }

@@ -356,6 +356,25 @@ def test_other_stream_and_graph():
     plan.close()
 
 
+@pytest.mark.parametrize("H", [48, 1040, 8200])
+def test_gradient_of_tiny_rows(H):
+    """Rows of some 1e-14 with eps = 0: the roots' cubes lie past fp32's range, the gradients do not."""
+    plan = A.Plan(1, 1, 5, H, 1, device=DEV)
+    i = inputs(1, 5, H, True, "channel", 6)
+    i["x"], i["residual"] = i["x"] * 2.0 ** -46, i["residual"] * 2.0 ** -46
+    d_x, d_res = torch.empty_like(i["x"]), torch.empty_like(i["x"])
+    plan.block_norm_grad(i["x"], i["residual"], d_x, d_res, weight=i["weight"], d_y=i["d_y"], post_weight=i["post_weight"],
+                         gate=i["gate"], residual_scale=2.0, branch_scale=2.0 ** -46, eps=0.0)
+    x, res = i["x"].double().requires_grad_(), i["residual"].double().requires_grad_()
+    f = reference(dict(i, x=x, residual=res), 2.0, 2.0 ** -46, eps=0.0)
+    loss = (f["z"] * f["r2"] * i["weight"].double() * i["d_y"].double()).sum()
+    for got, want in zip((d_x, d_res), torch.autograd.grad(loss, (x, res))):
+        assert torch.isfinite(got).all()
+        # each element within the roundings of its row's terms (header): 2^-15 and bf16's half step of the row's largest
+        within(got, want, want.abs().amax(-1, keepdim=True) * (BF + 2.0 ** -13))
+    plan.close()
+
+
 def test_refusals():
     R, T, H = 1, 4, 64
     plan = A.Plan(R, R, T, H, 1, device=DEV)
@@ -378,6 +397,12 @@ def test_refusals():
         (lambda: plan.block_norm(x, res, weight=w, y=x), "overlaps"),
         (lambda: plan.block_norm(x, res, weight=w, y=out, residual_out=out), "overlaps"),
         (lambda: plan.block_norm(room[:T].view_as(x), res, residual_out=shifted), "overlaps"),
+        # a weight or a gate in the first row of what is written in place
+        (lambda: plan.block_norm(x, res, residual_out=x, gate=x[0, 0]), "overlaps"),
+        (lambda: plan.block_norm(x, res, residual_out=res, post_weight=res[0, 0]), "overlaps"),
+        (lambda: plan.block_norm(x, res, residual_out=x, gate=x[0, :1].view(1, H)), "overlaps"),
+        (lambda: plan.block_norm(x, res, residual_out=x, y=out, weight=x[0, 0]), "overlaps"),
+        (lambda: plan.block_norm_grad(x, res, i["d_y"], d, d_y=i["d_y"], weight=i["d_y"][0, 0]), "overlaps"),
         (lambda: plan.block_norm(x, res, residual_out=room.flatten()[1:1 + x.numel()].view_as(x)), "misaligned"),
         (lambda: odd.block_norm(ox, ox, weight=ow, rows8=odd.new_rows8((1, 2), 24)), "H % 16"),
         (lambda: huge.block_norm(hx, hx, residual_out=torch.empty_like(hx)), "H <= 32768"),
