@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const ScoreAr
 // Four lanes per token, eight tokens per warp.  Lane r of a token holds the 16-byte units r, r + 4, ... of its row in
 // registers (NU of them), so every loop over logits is unrolled and none is read twice.  In order:
 //   1. choices in place of logits; a copy of them in shared memory, for the few that are looked up by number later;
-//   2. groups: two best per lane and group, merged so that lane r ends with groups r, r + 4; ranks by counting;
+//   2. groups: lane r reads groups r, r + 4, ... out of the shared copy, each lane from another unit on (so that four lie on
+//      different banks), and takes their two best; ranks by counting;
 //   3. tau, a lower bound of the KMAX-th largest choice: the KMAX-th largest of maxima of disjoint sets (a lane's kept
 //      units, by component);
 //   4. the choices at or above tau (some ten of 256 for KMAX = 8) as bits, then as a list in shared memory;
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const ScoreAr
 // by the choices' errors, so that the list holds whatever may lie at the border).  Groups that are too near are settled
 // in 64 bits before tau (keep_exact).  A list that is too long: route_one.
 constexpr int kList = 32;  // candidates of a token
-constexpr int kRanks = 12;
+constexpr int kRanks = 16;  // room for a token's ranks, and for its groups' values
+constexpr int kLaneGroups = 16;
 
 template <int KMAX>
 constexpr int tau_values() {  // that a lane gives to the bound
@@ -403,7 +405,7 @@ struct LaneList {
     float key[8][kList + 4];  // candidates of the eight tokens, NaN behind them
     float best[8][kRanks];    // by rank; NaN where there is none
     alignas(4) uint8_t id[8][kList];
-    uint8_t best_id[8][kRanks + 4];
+    uint8_t best_id[8][kRanks];
 };
 // A warp's share: the choices of eight tokens (also room for the warp kernel's token), the lists.
 __host__ __device__ constexpr size_t lane_warp_bytes(int E) { return (size_t)8 * lane_stride(E) * 16 + sizeof(LaneList); }
@@ -468,8 +470,8 @@ __device__ __noinline__ uint32_t keep_exact(const ScoreArgs &a, int u, const flo
     const int E = a.g.E, size = E / a.groups;
     const float *l = a.logits + (size_t)u * E;
     int n = 0;
-    for (int e = lane; e < E; e += 32) {  // E is a multiple of 32
-        const bool in = keys[e] >= floor[e / size];
+    for (int e = lane; e - lane < E; e += 32) {
+        const bool in = e < E && keys[e] >= floor[e / size];
         const uint32_t all = __ballot_sync(kAll, in);
         const int pos = n + __popc(all & lanemask_lt());
         if (in && pos < kList) ids[pos] = (uint8_t)e;
@@ -521,7 +523,7 @@ __device__ __noinline__ uint32_t keep_exact(const ScoreArgs &a, int u, const flo
 // kFull: E is 16 * NU, so no unit is missing.  Bound by instructions: 65,536 tokens of 256 logits, sigmoid with bias, 4 of 8
 // groups, top-8 take 34.5-38 us (their 71 MB are 10.5), some 1,930 instructions a warp for eight tokens; one warp per
 // token takes 224.  Four blocks an SM with 128 registers; five with 96 took 44 us, three with 160 37.
-template <int NU, int KMAX, int G, bool kFull>
+template <int NU, int KMAX, bool kGroups, bool kFull>
 __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int L = tau_values<KMAX>();
@@ -601,68 +603,42 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
         for (int j = 0; j < NU; ++j)
             if (has(j)) keys4[r + 4 * j] = v[j];
 
-        // 2. groups: which are kept, as bits
+        // 2. groups: which are kept, as bits, and which of this lane's units are theirs
         bool near = false;
-        uint32_t keep = ~0u;
-        if constexpr (G > 1) {
-            constexpr int UG = NU / G;
-            float b1[G], b2[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < UG; ++i) {
-                    const float4 &x = v[g * UG + i];
+        uint32_t units = ~0u;
+        if constexpr (kGroups) {
+            __syncwarp();
+            const int upg = E / a.groups / 4, log_upg = 31 - __clz(upg);  // units per group: a power of two
+            for (int g = r; g < a.groups; g += 4) {
+                float b1 = -INFINITY, b2 = -INFINITY;
+                for (int i = 0; i < upg; ++i) {
+                    const float4 x = keys4[g * upg + ((i + r) & (upg - 1))];
                     const float h1 = fmaxf(x.x, x.y), l1 = fminf(x.x, x.y), h2 = fmaxf(x.z, x.w), l2 = fminf(x.z, x.w);
-                    const float u1 = fmaxf(h1, h2), u2 = fmaxf(fminf(h1, h2), fmaxf(l1, l2));
-                    if (i == 0) {
-                        b1[g] = u1;
-                        b2[g] = u2;
-                    } else {
-                        merge2(b1[g], b2[g], u1, u2);
-                    }
+                    merge2(b1, b2, fmaxf(h1, h2), fmaxf(fminf(h1, h2), fmaxf(l1, l2)));
                 }
-            // halved over lane ^ 1, then over lane ^ 2: this lane ends with groups r, r + 4
-            float h1[G / 2], h2[G / 2], q1[G / 4], q2[G / 4];
-#pragma unroll
-            for (int i = 0; i < G / 2; ++i) {
-                const bool odd = r & 1;
-                h1[i] = odd ? b1[2 * i + 1] : b1[2 * i];
-                h2[i] = odd ? b2[2 * i + 1] : b2[2 * i];
-                merge2(h1[i], h2[i], __shfl_xor_sync(kAll, odd ? b1[2 * i] : b1[2 * i + 1], 1),
-                       __shfl_xor_sync(kAll, odd ? b2[2 * i] : b2[2 * i + 1], 1));
+                float value, off;
+                group_value(a, b1, b2, m, top, value, off);
+                list.key[t][g] = value;
+                list.key[t][kLaneGroups + g] = off;
+                const float q = a.best == 2 ? b2 : b1;  // below it by more than its error: none of the group's best
+                list.best[t][g] = a.bias && !isinf(q) ? q - 4.0f * error_of(a.sigmoid, top, q) : q;
             }
-            float value[G / 4], off[G / 4];
-#pragma unroll
-            for (int i = 0; i < G / 4; ++i) {
-                const bool up = r & 2;
-                q1[i] = up ? h1[2 * i + 1] : h1[2 * i];
-                q2[i] = up ? h2[2 * i + 1] : h2[2 * i];
-                merge2(q1[i], q2[i], __shfl_xor_sync(kAll, up ? h1[2 * i] : h1[2 * i + 1], 2),
-                       __shfl_xor_sync(kAll, up ? h2[2 * i] : h2[2 * i + 1], 2));
-                group_value(a, q1[i], q2[i], m, top, value[i], off[i]);
-            }
-            int before[G / 4];
-#pragma unroll
-            for (int i = 0; i < G / 4; ++i) before[i] = 0;
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int i = 0; i < G / 4; ++i) {
-                    const float other = s ? __shfl_xor_sync(kAll, value[i], s) : value[i];
-                    const int go = 4 * i + (r ^ s);
-#pragma unroll
-                    for (int q = 0; q < G / 4; ++q)
-                        before[q] += other > value[q] || (other == value[q] && go < 4 * q + r);
-                }
-            keep = 0;
+            __syncwarp();
+            uint32_t keep = 0;
             float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < G / 4; ++i) {
-                const bool in = before[i] < a.kept;
-                keep |= (uint32_t)in << (4 * i + r);
-                if (in) lo = fminf(lo, value[i] - off[i]);
-                else hi = fmaxf(hi, value[i] + off[i]);
+            for (int g = r; g < a.groups; g += 4) {
+                const float value = list.key[t][g], off = list.key[t][kLaneGroups + g];
+                int before = 0;
+                for (int q = 0; q < a.groups; ++q) {
+                    const float other = list.key[t][q];
+                    before += other > value || (other == value && q < g);
+                }
+                const bool in = before < a.kept;
+                keep |= (uint32_t)in << g;
+                if (in) lo = fminf(lo, value - off);
+                else hi = fmaxf(hi, value + off);
             }
+            __syncwarp();  // lanes of a token may have gone apart over their groups
             keep |= __shfl_xor_sync(kAll, keep, 1);
             keep |= __shfl_xor_sync(kAll, keep, 2);
             if (a.bias || a.best == 2) {
@@ -670,13 +646,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                 near = act && !(least >= most);
                 uint32_t open = __ballot_sync(kAll, near);
                 if (open) {
-                    if (near)  // what may be one of a group's two best, or its best
-#pragma unroll
-                        for (int i = 0; i < G / 4; ++i) {
-                            const float q = a.best == 2 ? q2[i] : q1[i];
-                            list.best[t][4 * i + r] = a.bias && !isinf(q) ? q - 4.0f * error_of(a.sigmoid, top, q) : q;
-                        }
-                    __syncwarp();
                     while (open) {
                         const int s = (__ffs(open) - 1) >> 2;
                         open &= ~(15u << (4 * s));
@@ -689,9 +658,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                         __syncwarp();
                     }
 #pragma unroll
-                    for (int j = 0; j < NU; ++j) v[j] = keys4[r + 4 * j];  // so that they need not be held over the calls
+                    for (int j = 0; j < NU; ++j)  // so that they need not be held over the calls
+                        if (has(j)) v[j] = keys4[r + 4 * j];
                 }
             }
+            units = 0;
+#pragma unroll
+            for (int j = 0; j < NU; ++j) units |= (keep >> ((r + 4 * j) >> log_upg) & 1) << j;
         }
 
         // 3. the bound
@@ -701,7 +674,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
             // maxima of the kept units' components
 #pragma unroll
             for (int j = 0; j < NU; ++j)
-                if (G == 1 || (keep >> (j / (NU / G)) & 1))
+                if (!kGroups || (units >> j & 1))
 #pragma unroll
                     for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], part_of(v[j], i));
             if (L == 4) sort4(c);
@@ -725,8 +698,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
         for (int w = 0; w < kWords; ++w) bits[w] = 0;
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-            float at = tau;
-            if constexpr (G > 1) at = keep >> (j / (NU / G)) & 1 ? tau : NAN;
+            const float at = !kGroups || (units >> j & 1) ? tau : NAN;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (part_of(v[j], c) >= at) bits[j / 8] |= 1u << (j % 8 * 4 + c);
@@ -1077,10 +1049,10 @@ cudaError_t launch_grad_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStre
     return launch_pdl(kernel, want < cap ? want : cap, 32 * kWarps, smem, s, a);
 }
 
-template <int NU, int KMAX, int G, bool kFull>
+template <int NU, int KMAX, bool kGroups, bool kFull>
 cudaError_t launch_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = route_scores_lane_kernel<NU, KMAX, G, kFull>;
+    const auto kernel = route_scores_lane_kernel<NU, KMAX, kGroups, kFull>;
     const auto bytes = [](int E, int warps) { return (size_t)E * 4 + warps * lane_warp_bytes(E); };
     const cudaError_t e = allow_smem(kernel, done, p.cfg.device, bytes(16 * NU, kWarps));
     if (e != cudaSuccess) return e;
@@ -1092,10 +1064,10 @@ cudaError_t launch_lanes(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t 
 
 template <int NU, bool kFull>
 cudaError_t launch_lanes_k(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s) {
-    if (a.g.k <= 1) return launch_lanes<NU, 1, 1, kFull>(p, a, s);
-    if (a.g.k <= 2) return launch_lanes<NU, 2, 1, kFull>(p, a, s);
-    if (a.g.k <= 4) return launch_lanes<NU, 4, 1, kFull>(p, a, s);
-    return launch_lanes<NU, 8, 1, kFull>(p, a, s);
+    if (a.g.k <= 1) return launch_lanes<NU, 1, false, kFull>(p, a, s);
+    if (a.g.k <= 2) return launch_lanes<NU, 2, false, kFull>(p, a, s);
+    if (a.g.k <= 4) return launch_lanes<NU, 4, false, kFull>(p, a, s);
+    return launch_lanes<NU, 8, false, kFull>(p, a, s);
 }
 
 }  // namespace
@@ -1112,12 +1084,13 @@ cudaError_t launch_route_scores(const a2av_plan_s &p, const ScoreArgs &a, cudaSt
             if (E < 256) return launch_lanes_k<16, false>(p, a, s);
             return launch_lanes_k<16, true>(p, a, s);
         }
-        // groups of whole units for every lane
-        if (E == 64 && G == 4) return launch_lanes<4, 8, 4, true>(p, a, s);
-        if (E == 128 && G == 4) return launch_lanes<8, 8, 4, true>(p, a, s);
-        if (E == 128 && G == 8) return launch_lanes<8, 8, 8, true>(p, a, s);
-        if (E == 256 && G == 4) return launch_lanes<16, 8, 4, true>(p, a, s);
-        if (E == 256 && G == 8) return launch_lanes<16, 8, 8, true>(p, a, s);
+        // groups of whole units, their number a power of two
+        const int upg = E / G / 4;
+        if (G <= kLaneGroups && E % (4 * G) == 0 && (upg & (upg - 1)) == 0) {
+            if (E <= 64) return launch_lanes<4, 8, true, false>(p, a, s);
+            if (E <= 128) return launch_lanes<8, 8, true, false>(p, a, s);
+            return E == 256 ? launch_lanes<16, 8, true, true>(p, a, s) : launch_lanes<16, 8, true, false>(p, a, s);
+        }
     }
     static std::atomic<uint64_t> done{0};
     return launch_tokens(route_scores_kernel, done, sizeof(long long), p, a, s);
