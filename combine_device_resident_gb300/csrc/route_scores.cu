@@ -611,6 +611,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
             const int upg = E / a.groups / 4, log_upg = 31 - __clz(upg);  // units per group: a power of two
             for (int g = r; g < a.groups; g += 4) {
                 float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 4
                 for (int i = 0; i < upg; ++i) {
                     const float4 x = keys4[g * upg + ((i + r) & (upg - 1))];
                     const float h1 = fmaxf(x.x, x.y), l1 = fminf(x.x, x.y), h2 = fmaxf(x.z, x.w), l2 = fminf(x.z, x.w);
@@ -629,6 +630,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
             for (int g = r; g < a.groups; g += 4) {
                 const float value = list.key[t][g], off = list.key[t][kLaneGroups + g];
                 int before = 0;
+#pragma unroll 4
                 for (int q = 0; q < a.groups; ++q) {
                     const float other = list.key[t][q];
                     before += other > value || (other == value && q < g);
