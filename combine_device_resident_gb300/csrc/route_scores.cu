@@ -521,7 +521,7 @@ __device__ __noinline__ uint32_t keep_exact(const ScoreArgs &a, int u, const flo
 }
 
 // kFull: E is 16 * NU, so no unit is missing.  Bound by instructions: 65,536 tokens of 256 logits, sigmoid with bias, 4 of 8
-// groups, top-8 take 37-41 us (their 71 MB are 10.5), some 2,300 instructions a warp for eight tokens; one warp per
+// groups, top-8 take 37-42 us (their 71 MB are 10.5), some 2,300 instructions a warp for eight tokens; one warp per
 // token takes 224.  Four blocks an SM with 128 registers: 35-38 us where five with 96 took 44 and three with 160 37 (with
 // the groups merged in registers, which only groups of 16 and more allow).
 template <int NU, int KMAX, bool kGroups, bool kFull>
