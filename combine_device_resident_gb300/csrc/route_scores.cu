@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                 if (j >= k) continue;
                 const float c = list.best[t][j], next = list.best[t][j + 1];
                 id[i] = list.best_id[t][j];
-                bool good = c == c;
+                bool good = c == c && !(a.bias && next != next && listed > j + 1);  // equal ones left the next rank empty
                 if (a.bias && next == next && too_near(a.sigmoid, top, c, next)) {
                     good = false;
                     if (kById && act && c == next) {

@@ -1,0 +1,50 @@
+"""The router by scores where few candidates of a token stand close together at a border: at the last chosen expert, and at
+the last kept group.  Ids are those of the 64-bit order, whatever the warp's other tokens do: a token per call."""
+import numpy as np
+import pytest
+import torch
+
+import combine_device_resident_gb300 as A
+from tests.test_gpu_route_scores import DEV, check
+
+pytestmark = pytest.mark.gpu
+
+
+def one_token(logits, bias, k, rule):
+    E = len(logits)
+    plan = A.Plan(1, E, 1, 8, k, device=DEV)
+    check(plan, torch.tensor(logits, dtype=torch.float32, device=DEV).view(1, 1, E), rule,
+          torch.tensor(bias, dtype=torch.float32, device=DEV))
+    plan.close()
+
+
+def border(rng, E, ahead, pair_first):
+    """Logits and biases of E experts: `ahead` clearly in front, then a single expert and two alike whose choices in 64 bits
+    lie within a few steps of fp32 of each other, the two alike in front or behind, the rest far below."""
+    while True:
+        logits, bias = np.zeros(E, np.float32), (-1.0 - 0.01 * rng.permutation(E)).astype(np.float32)
+        at = rng.permutation(E)[:ahead + 3]
+        logits[at], bias[at] = 1.0, 3.0 + np.arange(ahead + 3)
+        single, alike = at[0], at[1:3]
+        logits[single], logits[alike] = rng.uniform(15.0, 18.0, 2)
+        bias[single], bias[alike] = 0.25 + rng.integers(-8, 9, 2) * 2.0 ** -26
+        s = 1.0 / (1.0 + np.exp(-logits.astype(np.float64))) + bias.astype(np.float64)
+        if abs(s[single] - s[alike[0]]) > 1e-14 and (s[alike[0]] > s[single]) == pair_first:
+            return logits, bias
+
+
+LOW = float(torch.finfo(torch.float32).min)
+WIDTHS = [(4, 0), (8, 1), (16, 0), (16, 3), (64, 7), (100, 2), (128, 0), (256, 5), (256, 0)]
+
+
+def test_last_chosen_against_two_equal_ones():
+    """In fp32 expert 0 leads (1.2500001 against 1.25, twice), in 64 bits expert 1 does."""
+    one_token([16.86, 100.0, 100.0, 0.0], [0.25 + 3 * 2.0 ** -25, 0.25 + 2.0 ** -24, 0.25 + 2.0 ** -24, -1.0], 1,
+              A.RouteRule(score="sigmoid"))
+
+
+@pytest.mark.parametrize("E,ahead", WIDTHS)
+def test_two_equal_ones_at_the_border(E, ahead):
+    rng = np.random.default_rng(E + ahead)
+    for _ in range(40):
+        one_token(*border(rng, E, ahead, True), ahead + 1, A.RouteRule(score="sigmoid"))
