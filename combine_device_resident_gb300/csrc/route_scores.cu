@@ -773,9 +773,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                 if (a.bias && next == next && too_near(a.sigmoid, top, c, next)) {
                     good = false;
                     if (kById && act && c == next) {
-                        const int other = list.best_id[t][j + 1];
                         const float *const bias = reinterpret_cast<const float *>(sm);
-                        good = clean_logit(__ldg(row + id[i])) == clean_logit(__ldg(row + other)) && bias[id[i]] == bias[other];
+                        const float l0 = clean_logit(__ldg(row + id[i])), b0 = bias[id[i]];
+                        auto alike = [&](int other) { return clean_logit(__ldg(row + other)) == l0 && bias[other] == b0; };
+                        good = alike(list.best_id[t][j + 1]);
+                        if (j == k - 1)  // the last slot answers for all behind it, and one alike says nothing of the next
+                            for (int q = 0; good && q < listed; ++q) {
+                                const float x = list.key[t][q];
+                                if (x <= c && too_near(a.sigmoid, top, c, x)) good = alike(list.id[t][q]);
+                            }
                     }
                 }
                 right = right && good;

@@ -48,3 +48,23 @@ def test_two_equal_ones_at_the_border(E, ahead):
     rng = np.random.default_rng(E + ahead)
     for _ in range(40):
         one_token(*border(rng, E, ahead, True), ahead + 1, A.RouteRule(score="sigmoid"))
+
+
+@pytest.mark.parametrize("E,ahead", WIDTHS)
+def test_one_behind_two_equal_ones_at_the_border(E, ahead):
+    """fp32 may put the two alike in front, the last chosen's neighbour then says nothing about the one behind it."""
+    rng = np.random.default_rng(E + ahead + 1000)
+    for _ in range(40):
+        one_token(*border(rng, E, ahead, False), ahead + 1, A.RouteRule(score="sigmoid"))
+
+
+def test_many_equal_ones_at_the_border():
+    """Five alike, of which one is chosen, and one more that belongs in front of them."""
+    rng = np.random.default_rng(5)
+    for E in (16, 64, 256):
+        for _ in range(40):
+            logits, bias = border(rng, E, 0, False)
+            alike = [e for e in range(E) if (logits == logits[e]).sum() == 2]
+            more = rng.permutation(np.flatnonzero(bias <= -1.0))[:3]
+            logits[more], bias[more] = logits[alike[0]], bias[alike[0]]
+            one_token(logits, bias, 2, A.RouteRule(score="sigmoid"))
