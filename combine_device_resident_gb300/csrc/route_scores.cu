@@ -188,8 +188,9 @@ __device__ __forceinline__ float chosen_gate(const ScoreArgs &a, float l, bool i
     return a.scale * __fdiv_rn(l >= 0.0f ? 1.0f : e, 1.0f + e);
 }
 
-// A group's value out of its best choices (without a bias they are logits), and a bound of its error.  A sum that
-// overflows, or one of two infinities, is left to the 64-bit form.
+// A group's value out of its best choices (without a bias they are logits), and a bound of its error.  Of two best it is
+// half the sum, which cannot overflow and has the sum's order.  An infinite choice is the bias, in 64 bits too, and so is
+// one past 2^56, where no score moves it: the sum of two infinite ones, or of two equal ones that large, is exact.
 __device__ __forceinline__ void group_value(const ScoreArgs &a, float b1, float b2, float m, float top, float &value,
                                             float &off) {
     if (a.best == 1) {
@@ -202,11 +203,9 @@ __device__ __forceinline__ void group_value(const ScoreArgs &a, float b1, float 
         b2 = a.sigmoid ? fast_sigmoid(b2) : fast_exp(b2 - m);
         top = 1.0f;
     }
-    value = clean_choice(b1 + b2);
-    off = value == -INFINITY && b1 < INFINITY && b2 == -INFINITY ? 0.0f
-          : isinf(b1) || isinf(b2) || isinf(value)               ? INFINITY
-                                                   : error_of(a.sigmoid, top, b1) + error_of(a.sigmoid, top, b2) +
-                                                         fabsf(value) * 0x1p-23f;
+    value = clean_choice(fmaf(0.5f, b1, 0.5f * b2));
+    off = 0.5f * (error_of(a.sigmoid, top, b1) + error_of(a.sigmoid, top, b2)) + fabsf(value) * 0x1p-23f;
+    if (fmaxf(b1, -b2) > 0x1p56f && (b1 == b2 || isinf(b1) || isinf(b2))) off = 0.0f;
 }
 
 // One token by a warp: the fp32 choice, `room` E words of 64 bits.

@@ -68,3 +68,34 @@ def test_many_equal_ones_at_the_border():
             more = rng.permutation(np.flatnonzero(bias <= -1.0))[:3]
             logits[more], bias[more] = logits[alike[0]], bias[alike[0]]
             one_token(logits, bias, 2, A.RouteRule(score="sigmoid"))
+
+
+BIG = 2.0 ** 126
+
+
+@pytest.mark.parametrize("E,groups", [(16, 4), (64, 8), (256, 8), (256, 4), (24, 6), (20, 10)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("pairs", [
+    [(2e38, 2e38), (3e38, 3e38)],                       # both sums past fp32's range: 64 bits tell them apart
+    [(3e38, 1e38), (3e38, 2e38), (2e38, 2e38)],
+    [(-3e38, -3e38), (-2e38, -2e38)],
+    [(-np.inf, -np.inf), (LOW, LOW)],                   # masked by -infinity, and by the type's lowest value
+    [(LOW, -np.inf), (LOW, LOW)],
+    [(np.inf, -np.inf), (np.inf, 0.0), (LOW, LOW)],     # the first is no number: -infinity
+    [(np.inf, 0.0), (3e38, 3e38), (np.inf, np.inf)],    # the infinite ones are equal
+    [(LOW, LOW), (LOW, LOW)],
+    [(BIG, BIG), (np.nextafter(np.float32(BIG), np.float32(0)), BIG)],
+])
+def test_sums_of_two_best_at_the_ends_of_fp32(E, groups, score, pairs):
+    """Groups whose two best are these, one or two kept; the others are further down, masked, or further up."""
+    size = E // groups
+    rng = np.random.default_rng(E + groups)
+    rest = -np.inf if min(min(p) for p in pairs) < 0 else -1.0
+    for kept in (1, 2):
+        for _ in range(4):
+            logits = rng.standard_normal(E).astype(np.float32)
+            bias = np.full((groups, size), rest, np.float32)
+            for group, pair in zip(rng.permutation(groups), pairs):
+                bias[group, rng.permutation(size)[:2]] = pair
+            k = min(size, 3)
+            one_token(logits, bias.flatten(), k, A.RouteRule(score=score, groups=groups, groups_kept=kept, group_best=2))
