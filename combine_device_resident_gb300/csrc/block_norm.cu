@@ -810,6 +810,14 @@ __global__ void __launch_bounds__(8 * kSumGroups) norm_sums_kernel(const BlockNo
         s.x *= by, s.y *= by, s.z *= by, s.w *= by;
         reinterpret_cast<float4 *>(to)[i] = s;
     };
+    // Whether any token of the sum took part: an empty one is zero, whatever the weights it would be multiplied by hold
+    // (a rank without tokens may have no gate).
+    auto has_tokens = [&](int r) {
+        if (!a.num_tokens) return true;
+        for (int s = per_rank ? r : 0; s < (per_rank ? r + 1 : a.g.R); ++s)
+            if (active_tokens(a.num_tokens, s, a.g.T) > 0) return true;
+        return false;
+    };
     const float *const from = a.scratch + (size_t)(weights ? kSumWeight : kSumBranch) * H;
     float4 total = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int base = 0; base < R; base += at_once) {
@@ -827,9 +835,10 @@ __global__ void __launch_bounds__(8 * kSumGroups) norm_sums_kernel(const BlockNo
             const int r = base + group;
             float4 sum = part[group * share][x];
             for (int q = 1; q < share; ++q) add4(sum, part[group * share + q][x]);
-            if (!weights && d_gate) store(d_gate + (size_t)r * H, a.post ? times(sum, a.post) : sum, a.branch_scale);
+            const bool live = !weights && has_tokens(r);
+            if (!weights && d_gate) store(d_gate + (size_t)r * H, live && a.post ? times(sum, a.post) : sum, a.branch_scale);
             const bool shared_gate = a.gate_kind == A2AV_GATE_CHANNEL || a.gate_kind == A2AV_GATE_RANK;
-            ranked[group][x] = !weights && shared_gate ? times(sum, a.gate + (size_t)r * H) : sum;
+            ranked[group][x] = live && shared_gate ? times(sum, a.gate + (size_t)r * H) : sum;
         }
         __syncthreads();
         if (in && group == 0)
