@@ -99,8 +99,14 @@ class RouteRule(ctypes.Structure):
     def __init__(self, score="softmax", groups=1, groups_kept=None, group_best=1, renormalize=True, scale=1.0):
         if score not in SCORES:
             raise A2avError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-        kept = groups if groups_kept is None else groups_kept
-        super().__init__(SCORES[score], int(groups), int(kept), int(group_best), int(bool(renormalize)), float(scale))
+        whole = []
+        for name, v in (("groups", groups), ("groups_kept", groups if groups_kept is None else groups_kept),
+                        ("group_best", group_best)):
+            # a field would drop a fraction and what is past 32 bits
+            if isinstance(v, str) or not abs(v) < 2 ** 31 or int(v) != v:
+                raise A2avError(f"{name} must be a whole number of 32 bits, got {v!r}")
+            whole.append(int(v))
+        super().__init__(SCORES[score], *whole, int(bool(renormalize)), float(scale))
 
 
 class BlockNormArgs(ctypes.Structure):
