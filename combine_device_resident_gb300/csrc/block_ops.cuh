@@ -47,7 +47,7 @@ struct BlockNormArgs {
     uint16_t *d_x, *d_residual;
     float *d_weight, *d_post;  // may be null
     void *d_gate;              // may be null
-    float *scratch;            // [blocks][3][H]: a block's sums for weight, post_weight, gate
+    float *scratch;            // [blocks][2][H]: a block's sums for the weight, and for post_weight and gate together
 };
 
 cudaError_t launch_route_scores(const a2av_plan_s &p, const ScoreArgs &a, cudaStream_t s);
