@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (from + 4 * i < listed && above[i] <= k) {
+                    if (from + 4 * i < listed && above[i] < (kById ? kRanks : k + 1)) {
                         list.best[t][above[i]] = own[i];
                         list.best_id[t][above[i]] = list.id[t][from + 4 * i];
                     }
@@ -777,9 +777,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) route_scores_lane_kernel(const
                         auto alike = [&](int other) { return clean_logit(__ldg(row + other)) == l0 && bias[other] == b0; };
                         good = alike(list.best_id[t][j + 1]);
                         if (j == k - 1)  // the last slot answers for all behind it, and one alike says nothing of the next
-                            for (int q = 0; good && q < listed; ++q) {
-                                const float x = list.key[t][q];
-                                if (x <= c && too_near(a.sigmoid, top, c, x)) good = alike(list.id[t][q]);
+                            for (int q = j + 2; good && q < listed; ++q) {
+                                if (q < kRanks && !too_near(a.sigmoid, top, c, list.best[t][q])) break;
+                                good = q < kRanks && alike(list.best_id[t][q]);
                             }
                     }
                 }
