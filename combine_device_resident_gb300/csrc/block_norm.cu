@@ -16,8 +16,8 @@
 // z and the roots are taken again from x and residual: three block sums, each
 // after the one before.  A block takes consecutive rows, two at a time; its threads keep their
 // columns, so the sums over the tokens are each thread's own in shared memory;
-// the blocks' sums are added by a second kernel in a fixed order.  65,536 x 7168: 1068 us (5.28 TB/s); bound by the way
-// through a pair of rows: one block of 14 warps fits an SM, and 58% of its issue slots are empty.
+// the blocks' sums are added by a second kernel in a fixed order.  65,536 x 7168: 1066 us (5.29 TB/s); bound by the way
+// through a pair of rows: one block of 14 warps is on an SM, and 58% of its issue slots are empty.
 #include "block_ops.cuh"
 #include "expert_common.cuh"
 #include "row_math.cuh"
@@ -567,11 +567,14 @@ __global__ void __launch_bounds__(1024, 1) block_norm_grad_kernel(const BlockNor
             }
 }
 
-// Rows of up to 8192 two at a time: both rows' values are in registers (128 a thread), the factors, the weights in fp32
+// Rows of up to 8192 two at a time: both rows' values are in registers, the factors, the weights in fp32
 // and the sums over the tokens are read from shared memory once for both, and a block sum serves both.  That is half the
-// shared-memory traffic and half the barriers of the form above, which takes the longer rows.  (One row at a time in two
-// blocks of 448 threads: 1087 us for 1068 on 65,536 x 7168, and with post norm 458 for 284 on 65,536 x 2048 in three or
-// four smaller ones; eight values a thread and twice the threads: 1355.)
+// shared-memory traffic and half the barriers of the form above, which takes the longer rows.  128 registers a thread, of
+// which some values spill: 36 bytes a thread without the post norm, 144 with it, 550-690 with a gate per token (the form
+// above: 84, 140, 280-300).  All the same it is the faster one at each width timed, in us against the form above, post
+// norm and a gate per channel, then per token: 65,536 x 2048 279 (458), 439 (726); 2,040 x 5120 44 (57), 53 (75);
+// 26,208 x 5120 358 (448), 490 (658); 16,384 x 7168 283 (412), 422 (595); 16,384 x 8192 318 (507), 475 (780).  Eight
+// values a thread and twice the threads took 1355 on 65,536 x 7168.
 template <bool kPost, bool kToken, bool k32>
 __global__ void __launch_bounds__(512, 1) block_norm_grad_pair_kernel(const BlockNormArgs a, bool per_rank) {
     extern __shared__ __align__(16) ulonglong2 smem[];
